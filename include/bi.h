@@ -405,6 +405,111 @@ BI_API bi_status bi_attention_decode_noalloc(const void *Q, const void *K_cache,
                                              int32_t Hkv, int32_t head_dim, int32_t block_size, int32_t max_seq_len,
                                              float scale, void *O, bi_stream stream);
 
+/*
+ * ---- The 4-bit forms. A decode step reads every cached key and value and
+ * every weight once, so their bytes bound it; these calls hold both in 4 bits:
+ * bi_gemm_int4 (qkv) -> bi_kv_int4_append -> bi_attention_decode_int4 (or
+ * _extend_int4 for more than one new token) -> bi_gemm_int4 (output). The
+ * pages have no 4-bit cache; the batch-invariance rule is the same: nothing a
+ * row or sequence sees depends on the batch.
+ *
+ * The cache of one layer, for keys and for values:
+ *   codes   u8   [num_blocks][Hkv][block_size][64]
+ *   scales  bf16 [num_blocks][Hkv][block_size][4]
+ * A row holds one token's 128 dimensions of one KV head; each 32 consecutive
+ * dimensions share a scale s, and dimension d is held as an integer n in
+ * -7..7 with the value n * s. With amax the group's largest magnitude,
+ *   s = the smallest number with four significant bits that is >= amax / 7,
+ *       kept in [2^-100, 2^120],
+ *   n = x / s rounded to the nearest integer (ties to even), kept in -7..7,
+ * on the exact quotients, so the stored form does not depend on how or with
+ * what else it was computed, and n * s is a bf16 number exactly. A group that
+ * holds an infinity or a NaN reads back as NaN. Magnitudes above 7 * 2^120
+ * saturate. The order of the codes inside a row is chosen for the kernels and
+ * differs between keys and values: dimension d = 32 i + 8 q + r (r < 8, q < 4)
+ * is nibble q (code n + 8) of the row's 16-bit word 8 (r / 2) + 2 i + r % 2 of
+ * keys, 4 r + i of values. Code rows are 16-byte aligned, scales 8-byte.
+ * The attention over this cache multiplies the same bf16 operands in the same
+ * order as bi_attention_decode / _extend over a bf16 cache that holds the same
+ * values: the results are the same bits.
+ * num_blocks * Hkv * block_size must be below 2^32 - 1.
+ */
+
+/*
+ * bi_kv_int4_append -- quantise T tokens' keys and values into the cache.
+ *   K, V    bf16, token t's [Hkv][128] rows at K + t * ldk, V + t * ldv
+ *           (elements; strided, so slices of a fused projection need no copy)
+ *   slots   i64 [T] (device)  token t goes to block slots[t] / block_size,
+ *           offset slots[t] % block_size; -1: the token is skipped (padding)
+ * A slot outside the cache is skipped and the device status becomes
+ * BI_ERR_INVALID_ARG. The slots of one call must differ (two tokens of one
+ * call with the same slot leave an unspecified mixture there). Everything
+ * else in the cache stays as it was.
+ * Requirements: head_dim == 128; ldk, ldv >= Hkv * 128 and multiples of 8.
+ */
+BI_API bi_status bi_kv_int4_append(const void *K, int64_t ldk, const void *V, int64_t ldv, int64_t T,
+                                   const int64_t *slots, uint8_t *k_codes, void *k_scales, uint8_t *v_codes,
+                                   void *v_scales, int64_t num_blocks, int32_t Hkv, int32_t head_dim,
+                                   int32_t block_size, bi_stream stream);
+
+/*
+ * bi_kv_int4_read -- the values of T cached tokens, as bf16 (exact): to copy
+ * tokens to another cache, or to look at what is held. Arguments as for
+ * bi_kv_int4_append, with K and V written; a slot may be given more than once.
+ * Slot -1, or one outside the cache (status BI_ERR_INVALID_ARG), gives zeros.
+ */
+BI_API bi_status bi_kv_int4_read(const uint8_t *k_codes, const void *k_scales, const uint8_t *v_codes,
+                                 const void *v_scales, int64_t num_blocks, int32_t Hkv, int32_t head_dim,
+                                 int32_t block_size, const int64_t *slots, int64_t T, void *K, int64_t ldk, void *V,
+                                 int64_t ldv, bi_stream stream);
+
+/*
+ * bi_attention_decode_int4 -- bi_attention_decode over the 4-bit cache: the
+ * same bits as bi_attention_decode over a bf16 cache holding the same values
+ * (same chunks, product order and merge; same workspace size; same checks and
+ * skips of sequence lengths and blocks). A chunk whose blocks all lie outside
+ * the cache counts nothing.
+ */
+BI_API bi_status bi_attention_decode_int4(const void *Q, const uint8_t *k_codes, const void *k_scales,
+                                          const uint8_t *v_codes, const void *v_scales, const int32_t *block_table,
+                                          int32_t max_blocks_per_seq, int64_t num_blocks, const int32_t *seq_lens,
+                                          int64_t B, int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t block_size,
+                                          int32_t max_seq_len, float scale, void *workspace, int64_t workspace_bytes,
+                                          void *O, bi_stream stream);
+
+/*
+ * bi_attention_extend_int4 -- bi_attention_extend over the 4-bit cache, which
+ * already holds the new tokens' keys and values: the same bits as
+ * bi_attention_extend over a bf16 cache holding the same values, and as
+ * bi_attention_decode_int4 of each token's cut sequence. No workspace.
+ */
+BI_API bi_status bi_attention_extend_int4(const void *Q, const int32_t *cu_q, int32_t total_q, const uint8_t *k_codes,
+                                          const void *k_scales, const uint8_t *v_codes, const void *v_scales,
+                                          const int32_t *block_table, int32_t max_blocks_per_seq, int64_t num_blocks,
+                                          const int32_t *seq_lens, int64_t B, int32_t Hq, int32_t Hkv,
+                                          int32_t head_dim, int32_t block_size, int32_t max_seq_len,
+                                          int32_t max_q_len, float scale, void *O, bi_stream stream);
+
+/*
+ * bi_gemm_int4 -- batch-invariant linear layer with 4-bit weights and group scales.
+ *   Y[i][j] = bf16( sum_g s[j][g] * sum_{k in group g} X[i][k] * (u[j][k] - z[j][g]) )
+ * The weights enter the products as the exact integers u - z; each group's (or
+ * each 128 k of a longer group's) sum is fp32, scaled and added in fp32. K is
+ * cut into blocks of 128, the blocks into segments fixed by K alone; groups are
+ * added in ascending order within a segment and the segments' sums in segment
+ * order. Row i of Y does not depend on M or on the other rows, bit for bit.
+ *   X       bf16 [M][ldx]
+ *   W       u8   [N][K/2]      codes 0..15, k in byte k/2, low nibble for even k
+ *   scales  bf16 [N][K/group]
+ *   zeros   u8   [N][K/group]  0..15 (the low four bits count); NULL: 8 throughout
+ *   Y       bf16 [M][ldy]
+ * Made for few rows, where the weights' bytes bound it; any M is computed.
+ * Requirements: group 32, 64 or a multiple of 128; K % group == 0; N % 8 == 0;
+ * ldx, ldy multiples of 8, ldx >= K, ldy >= N.
+ */
+BI_API bi_status bi_gemm_int4(const void *X, int64_t ldx, const uint8_t *W, const void *scales, const uint8_t *zeros,
+                              void *Y, int64_t ldy, int64_t M, int64_t N, int64_t K, int64_t group, bi_stream stream);
+
 /* Operation ids for bi_plan. */
 enum { BI_OP_GEMM_BF16 = 0, BI_OP_GROUPED_GEMM_BF16 = 1, BI_OP_GEMM_NVFP4 = 2, BI_OP_RMSNORM = 3,
        BI_OP_QUANTIZE_NVFP4 = 4, BI_OP_GROUPED_GEMM_SILU_BF16 = 5 /* N carries I */ };

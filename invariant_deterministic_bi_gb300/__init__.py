@@ -7,13 +7,16 @@ calls the matching ``extern "C"`` entry point of ``libbi.so`` (declared in
 is no CPU or PyTorch fallback. If the library is missing this module raises.
 
 Names follow the C ABI: ``gemm_bf16``, ``grouped_gemm_bf16``, ``gemm_nvfp4``,
-``quantize_nvfp4``, ``rmsnorm``, ``plan``, ``device_status``, ``check_wait_timeout``.
+``quantize_nvfp4``, ``rmsnorm``, ``plan``, ``device_status``, ``check_wait_timeout``;
+the 4-bit forms ``kv_int4_cache``, ``kv_int4_append``, ``kv_int4_read``,
+``attention_decode_int4``, ``attention_extend_int4``, ``gemm_int4``.
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import threading
+from typing import Any, NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # BI_LIBRARY=debug selects the debug build (bounds-checked kernels, same results)
@@ -78,6 +81,12 @@ def load() -> ctypes.CDLL:
             "bi_last_bounds_line": [],
             "bi_check_bounds": [I32, I32, P],
             "bi_attention_extend": [P, P, I32, P, P, P, I32, I64, P, I64, I32, I32, I32, I32, I32, I32, F, P, P],
+            "bi_kv_int4_append": [P, I64, P, I64, I64, P, P, P, P, P, I64, I32, I32, I32, P],
+            "bi_kv_int4_read": [P, P, P, P, I64, I32, I32, I32, P, I64, P, I64, P, I64, P],
+            "bi_attention_decode_int4": [P, P, P, P, P, P, I32, I64, P, I64, I32, I32, I32, I32, I32, F, P, I64, P, P],
+            "bi_attention_extend_int4": [P, P, I32, P, P, P, P, P, I32, I64, P, I64, I32, I32, I32, I32, I32, I32, F, P,
+                                         P],
+            "bi_gemm_int4": [P, I64, P, P, P, P, I64, I64, I64, I64, I64, P],
             "bi_plan": [I32, I64, I64, I64, I32, ctypes.POINTER(Plan)],
             "bi_device_status": [P],
             "bi_check_wait_timeout": [ctypes.c_uint32, P],
@@ -409,6 +418,206 @@ def attention_extend(Q, cu_q, K_cache, V_cache, block_table, seq_lens, max_seq_l
                                       block_table.shape[1], nblk, _ptr(seq_lens), B, Hq, Hkv, D, bs, max_seq_len,
                                       max_q_len, float(scale), _ptr(O), _stream(stream)), "bi_attention_extend")
     return O
+
+
+class KVInt4Cache(NamedTuple):
+    """One layer's paged 4-bit K/V cache (see bi.h): codes uint8 [blocks, Hkv,
+    block_size, 64], scales bfloat16 [blocks, Hkv, block_size, 4]."""
+    k_codes: Any
+    k_scales: Any
+    v_codes: Any
+    v_scales: Any
+
+
+def kv_int4_cache(num_blocks: int, block_size: int, Hkv: int, device="cuda") -> KVInt4Cache:
+    """An empty 4-bit K/V cache (every row reads as zeros)."""
+    import torch
+    rows = (num_blocks, Hkv, block_size)
+    return KVInt4Cache(*(torch.zeros(rows + (w,), dtype=d, device=device)
+                         for w, d in ((64, torch.uint8), (4, torch.bfloat16)) * 2))
+
+
+def _cache_args(cache):
+    """(num_blocks, Hkv, block_size) of a checked KVInt4Cache."""
+    import torch
+    kc, ks, vc, vs = cache
+    for t, d, n in ((kc, torch.uint8, "k_codes"), (ks, torch.bfloat16, "k_scales"), (vc, torch.uint8, "v_codes"),
+                    (vs, torch.bfloat16, "v_scales")):
+        _dev(t, d, n)
+        if t.dim() != 4 or not t.is_contiguous() or t.shape[:3] != kc.shape[:3]:
+            raise ValueError(f"{n} must be contiguous [blocks, Hkv, block_size, ...], the same for keys and values")
+    if kc.shape[3] != 64 or vc.shape[3] != 64 or ks.shape[3] != 4 or vs.shape[3] != 4:
+        raise ValueError("a cache row holds 64 bytes of codes and 4 scales")
+    return kc.shape[:3]
+
+
+def _one_device(*tensors):
+    """All tensors on the current device (the calls launch there)."""
+    import torch
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"tensors must be on the current device cuda:{cur}, got {t.device}")
+
+
+def _new(shape, dtype, like, stream):
+    """An uninitialised tensor that stays allocated until the work of `stream` that uses it is done."""
+    import torch
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _kv_rows(t, T, Hkv, name):
+    """Token stride of bf16 rows [T, Hkv, 128] whose heads are contiguous within a token."""
+    import torch
+    _dev(t, torch.bfloat16, name)
+    if tuple(t.shape) != (T, Hkv, 128):
+        raise ValueError(f"{name} must be [T, Hkv, 128] = {(T, Hkv, 128)}, got {tuple(t.shape)}")
+    if t.numel() and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != 128)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous (a token stride is allowed)")
+    return t.stride(0) if T > 1 else Hkv * 128
+
+
+def _slots(slots):
+    import torch
+    _dev(slots, torch.int64, "slots")
+    if slots.dim() != 1 or not slots.is_contiguous():
+        raise ValueError("slots must be contiguous [T]")
+    return slots.numel()
+
+
+def kv_int4_append(K, V, slots, cache: KVInt4Cache, stream=None) -> KVInt4Cache:
+    """Quantise tokens' keys and values into the 4-bit cache (see bi.h); returns the cache.
+
+    K, V bf16 [T, Hkv, 128] (a token stride is allowed: slices of a fused
+    projection); slots int64 [T]: block * block_size + offset, -1 to skip a
+    token. The slots of one call must differ."""
+    nblk, Hkv, bs = _cache_args(cache)
+    T = _slots(slots)
+    ldk, ldv = _kv_rows(K, T, Hkv, "K"), _kv_rows(V, T, Hkv, "V")
+    _one_device(K, V, slots, *cache)
+    _check(load().bi_kv_int4_append(_ptr(K), ldk, _ptr(V), ldv, T, _ptr(slots), *map(_ptr, cache), nblk, Hkv, 128, bs,
+                                    _stream(stream)), "bi_kv_int4_append")
+    return cache
+
+
+def kv_int4_read(cache: KVInt4Cache, slots, K=None, V=None, stream=None):
+    """(K, V) bf16 [T, Hkv, 128]: the values held at `slots` (int64 [T]; -1 gives zeros)."""
+    import torch
+    nblk, Hkv, bs = _cache_args(cache)
+    T = _slots(slots)
+    _one_device(slots, K, V, *cache)
+    if K is None:
+        K = _new((T, Hkv, 128), torch.bfloat16, slots, stream)
+    if V is None:
+        V = _new((T, Hkv, 128), torch.bfloat16, slots, stream)
+    ldk, ldv = _kv_rows(K, T, Hkv, "K"), _kv_rows(V, T, Hkv, "V")
+    _check(load().bi_kv_int4_read(*map(_ptr, cache), nblk, Hkv, 128, bs, _ptr(slots), T, _ptr(K), ldk, _ptr(V), ldv,
+                                  _stream(stream)), "bi_kv_int4_read")
+    return K, V
+
+
+def _attention_int4_args(Q, cache, block_table, seq_lens, O):
+    """Checks shared by the 4-bit attention calls: (nblk, Hkv, block_size)."""
+    import torch
+    nblk, Hkv, bs = _cache_args(cache)
+    _dev(Q, torch.bfloat16, "Q"), _dev(block_table, torch.int32, "block_table"), _dev(seq_lens, torch.int32, "seq_lens")
+    for t, n in ((Q, "Q"), (block_table, "block_table"), (seq_lens, "seq_lens")):
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    if Q.dim() != 3 or Q.shape[2] != 128 or block_table.dim() != 2 or block_table.shape[0] != seq_lens.numel():
+        raise ValueError(f"shape mismatch Q{tuple(Q.shape)} block_table{tuple(block_table.shape)} "
+                         f"seq_lens{tuple(seq_lens.shape)}")
+    if O is not None:
+        _dev(O, torch.bfloat16, "O")
+        if O.shape != Q.shape or not O.is_contiguous():
+            raise ValueError("O must be contiguous, of Q's shape")
+    return nblk, Hkv, bs
+
+
+def attention_decode_int4(Q, cache: KVInt4Cache, block_table, seq_lens, max_seq_len: int, scale: float,
+                          workspace=None, O=None, stream=None):
+    """Decode attention over the 4-bit cache: the bits of ``attention_decode`` over a bf16 cache of the same values.
+
+    Q bf16 [B, Hq, 128]; block_table int32 [B, max_blocks]; seq_lens int32 [B].
+    The workspace (uint8, ``attention_decode_workspace_size`` bytes) is
+    allocated with torch if not given."""
+    import torch
+    nblk, Hkv, bs = _attention_int4_args(Q, cache, block_table, seq_lens, O)
+    B, Hq, D = Q.shape
+    if seq_lens.numel() != B:
+        raise ValueError("one query token a sequence: Q must have seq_lens.numel() rows")
+    _one_device(Q, block_table, seq_lens, workspace, O, *cache)
+    if workspace is None:
+        workspace = _new(max(attention_decode_workspace_size(B, Hq, max_seq_len), 16), torch.uint8, Q, stream)
+    _dev(workspace, torch.uint8, "workspace")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if O is None:
+        O = _new(Q.shape, Q.dtype, Q, stream)
+    _check(load().bi_attention_decode_int4(_ptr(Q), *map(_ptr, cache), _ptr(block_table), block_table.shape[1], nblk,
+                                           _ptr(seq_lens), B, Hq, Hkv, D, bs, max_seq_len, float(scale),
+                                           _ptr(workspace), workspace.numel(), _ptr(O), _stream(stream)),
+           "bi_attention_decode_int4")
+    return O
+
+
+def attention_extend_int4(Q, cu_q, cache: KVInt4Cache, block_table, seq_lens, max_seq_len: int, max_q_len: int,
+                          scale: float, O=None, stream=None):
+    """Causal extend (prefill) attention over the 4-bit cache: the bits of ``attention_extend`` over a bf16 cache
+    of the same values.
+
+    Q bf16 [total_q, Hq, 128]; cu_q int32 [B+1]; block_table int32 [B, max_blocks];
+    seq_lens int32 [B], the new tokens (already in the cache) included."""
+    import torch
+    nblk, Hkv, bs = _attention_int4_args(Q, cache, block_table, seq_lens, O)
+    _dev(cu_q, torch.int32, "cu_q")
+    B = seq_lens.numel()
+    if cu_q.numel() != B + 1 or not cu_q.is_contiguous():
+        raise ValueError("cu_q must be contiguous [B + 1]")
+    _one_device(Q, cu_q, block_table, seq_lens, O, *cache)
+    T, Hq, D = Q.shape
+    if O is None:
+        O = _new(Q.shape, Q.dtype, Q, stream)
+    _check(load().bi_attention_extend_int4(_ptr(Q), _ptr(cu_q), T, *map(_ptr, cache), _ptr(block_table),
+                                           block_table.shape[1], nblk, _ptr(seq_lens), B, Hq, Hkv, D, bs, max_seq_len,
+                                           max_q_len, float(scale), _ptr(O), _stream(stream)),
+           "bi_attention_extend_int4")
+    return O
+
+
+def gemm_int4(X, W, scales, zeros=None, Y=None, stream=None):
+    """Y[M,N] = X[M,K] dequant(W)[N,K]^T, batch-invariant, for 4-bit weights with group scales.
+
+    X bf16 [M, K] (may be a row-strided view); W uint8 [N, K/2], two codes a
+    byte, low nibble for even k; scales bf16 [N, K/g]; zeros uint8 [N, K/g] or
+    None (8 throughout). A weight is (code - zero) * scale."""
+    import torch
+    _dev(X, torch.bfloat16, "X"), _dev(W, torch.uint8, "W"), _dev(scales, torch.bfloat16, "scales")
+    if X.dim() != 2 or W.dim() != 2 or scales.dim() != 2 or X.shape[1] != 2 * W.shape[1] or scales.shape[0] != W.shape[0]:
+        raise ValueError(f"shape mismatch X{tuple(X.shape)} W{tuple(W.shape)} scales{tuple(scales.shape)}")
+    M, K = X.shape
+    N, groups = scales.shape
+    if X.stride(1) != 1 or not W.is_contiguous() or not scales.is_contiguous():
+        raise ValueError("X needs unit column stride; W and scales must be contiguous")
+    if groups < 1 or K % groups:
+        raise ValueError("scales must divide K into groups")
+    if zeros is not None:
+        _dev(zeros, torch.uint8, "zeros")
+        if zeros.shape != scales.shape or not zeros.is_contiguous():
+            raise ValueError("zeros must be contiguous, of scales' shape")
+    _one_device(X, W, scales, zeros, Y)
+    if Y is None:
+        Y = _new((M, N), torch.bfloat16, X, stream)
+    _dev(Y, torch.bfloat16, "Y")
+    if Y.shape != (M, N) or Y.stride(1) != 1:
+        raise ValueError("Y must be [M, N] with unit column stride")
+    _check(load().bi_gemm_int4(_ptr(X), X.stride(0) if M > 1 else K, _ptr(W), _ptr(scales),
+                               _ptr(zeros) if zeros is not None else None, _ptr(Y), Y.stride(0) if M > 1 else N, M, N, K,
+                               K // groups, _stream(stream)), "bi_gemm_int4")
+    return Y
 
 
 def plan(op: int, M: int, N: int, K: int, num_sms: int = 0) -> dict:

@@ -348,6 +348,126 @@ bi_status bi_attention_extend(const void *Q, const int32_t *cu_q, int32_t total_
                                    as_stream(stream));
 }
 
+namespace {
+inline bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+// The cache arguments of the 4-bit calls: BI_OK, or what is wrong with them.
+bi_status check_kv_int4(const uint8_t *kc, const void *ks, const uint8_t *vc, const void *vs, int64_t num_blocks,
+                        int32_t Hkv, int32_t head_dim, int32_t bs, KvInt4 *out) {
+    if (num_blocks < 1 || Hkv < 1 || bs < 1) return BI_ERR_INVALID_ARG;
+    if (!kc || !ks || !vc || !vs) return BI_ERR_INVALID_ARG;
+    if (head_dim != 128) return BI_ERR_UNSUPPORTED;
+    // rows are numbered in 32 bits (2^32 of them hold 288 GB of codes)
+    const int64_t per = static_cast<int64_t>(Hkv) * bs;
+    if (num_blocks > (static_cast<int64_t>(0xFFFFFFFF) - 1) / per) return BI_ERR_UNSUPPORTED;
+    if (!aligned16(kc) || !aligned16(vc) || !aligned8(ks) || !aligned8(vs)) return BI_ERR_MISALIGNED;
+    *out = KvInt4{const_cast<uint8_t *>(kc), static_cast<uint16_t *>(const_cast<void *>(ks)), const_cast<uint8_t *>(vc),
+                  static_cast<uint16_t *>(const_cast<void *>(vs)), num_blocks, Hkv, bs};
+    return BI_OK;
+}
+// The rows of K and V and the slots of bi_kv_int4_append / _read.
+bi_status check_kv_rows(const void *K, int64_t ldk, const void *V, int64_t ldv, const int64_t *slots, int32_t Hkv) {
+    if (!K || !V || !slots) return BI_ERR_INVALID_ARG;
+    if (ldk < static_cast<int64_t>(Hkv) * 128 || ldv < static_cast<int64_t>(Hkv) * 128) return BI_ERR_INVALID_ARG;
+    if (ldk % 8 != 0 || ldv % 8 != 0 || !aligned16(K) || !aligned16(V) || !aligned8(slots)) return BI_ERR_MISALIGNED;
+    return BI_OK;
+}
+}  // namespace
+
+bi_status bi_kv_int4_append(const void *K, int64_t ldk, const void *V, int64_t ldv, int64_t T, const int64_t *slots,
+                            uint8_t *k_codes, void *k_scales, uint8_t *v_codes, void *v_scales, int64_t num_blocks,
+                            int32_t Hkv, int32_t head_dim, int32_t block_size, bi_stream stream) {
+    if (T < 0 || T >= kI32Max) return BI_ERR_INVALID_ARG;
+    if (T == 0) return BI_OK;
+    KvInt4 c;
+    bi_status st = check_kv_int4(k_codes, k_scales, v_codes, v_scales, num_blocks, Hkv, head_dim, block_size, &c);
+    if (st != BI_OK) return st;
+    st = check_kv_rows(K, ldk, V, ldv, slots, Hkv);
+    if (st != BI_OK) return st;
+    st = require_device();
+    if (st != BI_OK) return st;
+    return launch_kv_int4_append(c, slots, K, ldk, V, ldv, T, as_stream(stream));
+}
+
+bi_status bi_kv_int4_read(const uint8_t *k_codes, const void *k_scales, const uint8_t *v_codes, const void *v_scales,
+                          int64_t num_blocks, int32_t Hkv, int32_t head_dim, int32_t block_size, const int64_t *slots,
+                          int64_t T, void *K, int64_t ldk, void *V, int64_t ldv, bi_stream stream) {
+    if (T < 0 || T >= kI32Max) return BI_ERR_INVALID_ARG;
+    if (T == 0) return BI_OK;
+    KvInt4 c;
+    bi_status st = check_kv_int4(k_codes, k_scales, v_codes, v_scales, num_blocks, Hkv, head_dim, block_size, &c);
+    if (st != BI_OK) return st;
+    st = check_kv_rows(K, ldk, V, ldv, slots, Hkv);
+    if (st != BI_OK) return st;
+    st = require_device();
+    if (st != BI_OK) return st;
+    return launch_kv_int4_read(c, slots, K, ldk, V, ldv, T, as_stream(stream));
+}
+
+bi_status bi_attention_decode_int4(const void *Q, const uint8_t *k_codes, const void *k_scales, const uint8_t *v_codes,
+                                   const void *v_scales, const int32_t *block_table, int32_t max_blocks_per_seq,
+                                   int64_t num_blocks, const int32_t *seq_lens, int64_t B, int32_t Hq, int32_t Hkv,
+                                   int32_t head_dim, int32_t block_size, int32_t max_seq_len, float scale,
+                                   void *workspace, int64_t workspace_bytes, void *O, bi_stream stream) {
+    if (B < 0 || B > 65535 || Hq < 1 || Hkv < 1 || max_seq_len < 1 || max_seq_len > BI_ATTENTION_MAX_SEQ_LEN ||
+        max_blocks_per_seq < 1 || !(scale == scale))
+        return BI_ERR_INVALID_ARG;
+    if (B == 0) return BI_OK;
+    if (!Q || !block_table || !seq_lens || !workspace || !O) return BI_ERR_INVALID_ARG;
+    KvInt4 c;
+    bi_status st = check_kv_int4(k_codes, k_scales, v_codes, v_scales, num_blocks, Hkv, head_dim, block_size, &c);
+    if (st != BI_OK) return st;
+    if (Hq % Hkv != 0) return BI_ERR_UNSUPPORTED;
+    const int32_t G = Hq / Hkv;
+    if (G != 1 && G != 2 && G != 4 && G != 8) return BI_ERR_UNSUPPORTED;
+    const int64_t need = attention_decode_workspace_bytes(B, Hq, max_seq_len);
+    if (need < 0 || workspace_bytes < need) return BI_ERR_INVALID_ARG;
+    if (!aligned16(Q) || !aligned16(O) || !aligned16(workspace) || !aligned4(block_table) || !aligned4(seq_lens))
+        return BI_ERR_MISALIGNED;
+    st = require_device();
+    if (st != BI_OK) return st;
+    return launch_attention_decode_int4(Q, c, block_table, max_blocks_per_seq, seq_lens, B, Hq, max_seq_len, scale,
+                                        workspace, O, as_stream(stream));
+}
+
+bi_status bi_attention_extend_int4(const void *Q, const int32_t *cu_q, int32_t total_q, const uint8_t *k_codes,
+                                   const void *k_scales, const uint8_t *v_codes, const void *v_scales,
+                                   const int32_t *block_table, int32_t max_blocks_per_seq, int64_t num_blocks,
+                                   const int32_t *seq_lens, int64_t B, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                                   int32_t block_size, int32_t max_seq_len, int32_t max_q_len, float scale, void *O,
+                                   bi_stream stream) {
+    if (B < 0 || B > 65535 || total_q < 0 || Hq < 1 || Hkv < 1 || max_seq_len < 1 ||
+        max_seq_len > BI_ATTENTION_MAX_SEQ_LEN || max_q_len < 1 || max_blocks_per_seq < 1 || !(scale == scale))
+        return BI_ERR_INVALID_ARG;
+    if (B == 0 || total_q == 0) return BI_OK;
+    if (!Q || !cu_q || !block_table || !seq_lens || !O) return BI_ERR_INVALID_ARG;
+    KvInt4 c;
+    bi_status st = check_kv_int4(k_codes, k_scales, v_codes, v_scales, num_blocks, Hkv, head_dim, block_size, &c);
+    if (st != BI_OK) return st;
+    if (Hq % Hkv != 0) return BI_ERR_UNSUPPORTED;
+    const int32_t G = Hq / Hkv;
+    if (G != 1 && G != 2 && G != 4 && G != 8) return BI_ERR_UNSUPPORTED;
+    if (!aligned16(Q) || !aligned16(O) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(cu_q))
+        return BI_ERR_MISALIGNED;
+    st = require_device();
+    if (st != BI_OK) return st;
+    return launch_attention_extend_int4(Q, cu_q, total_q, c, block_table, max_blocks_per_seq, seq_lens, B, Hq, max_seq_len,
+                                        max_q_len, scale, O, as_stream(stream));
+}
+
+bi_status bi_gemm_int4(const void *X, int64_t ldx, const uint8_t *W, const void *scales, const uint8_t *zeros, void *Y,
+                       int64_t ldy, int64_t M, int64_t N, int64_t K, int64_t group, bi_stream stream) {
+    if (M < 0 || N < 0 || K <= 0 || M >= kI32Max || N >= kI32Max || K >= kI32Max || group < 1) return BI_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return BI_OK;
+    if (!X || !W || !scales || !Y || ldx < K || ldy < N) return BI_ERR_INVALID_ARG;
+    if (!(group == 32 || group == 64 || group % 128 == 0) || K % group != 0 || N % 8 != 0) return BI_ERR_UNSUPPORTED;
+    if (ldx % 8 != 0 || ldy % 8 != 0 || !aligned16(X) || !aligned16(W) || !aligned16(Y) ||
+        (reinterpret_cast<uintptr_t>(scales) & 1u))
+        return BI_ERR_MISALIGNED;
+    const bi_status st = require_device();
+    if (st != BI_OK) return st;
+    return launch_gemm_int4(X, ldx, W, scales, zeros, Y, ldy, M, N, K, group, as_stream(stream));
+}
+
 bi_status bi_plan(int32_t op, int64_t M, int64_t N, int64_t K, int32_t num_sms, bi_plan_t *out) {
     if (!out || M < 0 || N < 0 || K < 0 || num_sms < 0) return BI_ERR_INVALID_ARG;
     int sms = num_sms;

@@ -50,70 +50,18 @@
 
 #include <mutex>
 
+#include "attn_common.cuh"
 #include "bi_internal.h"
 #include "bi_ptx.cuh"
+#include "kv_int4.cuh"
 
 namespace bi {
 namespace {
 
-constexpr int kD = 128;
-constexpr int kChunk = 128;                    // tokens per chunk: fixed, by position
 constexpr int kThreads = 256;                  // split kernel
 constexpr int kCombineThreads = 128;           // one thread per output dimension
 constexpr int kRowBytes = kD * 2;              // one token's K (or V) row of one KV head
 constexpr int kTileBytes = kChunk * kRowBytes; // 32 KB
-
-
-// 16-byte global -> shared copy; src_bytes = 0 writes 16 zero bytes and reads nothing.
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint32_t src_bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// D += A B on the tensor cores, one warp: A 16x16 bf16 (row-major fragment
-// a0..a3), B 16x8 bf16 (column fragment b0, b1), D 16x8 fp32.
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-                 "{%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Four 8x8 bf16 matrices from shared memory, transposed (lanes 8i..8i+7 give
-// the 16-byte rows of matrix i).
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3,
-                                                  uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3) : "r"(addr));
-}
-// Four 8x8 bf16 matrices from shared memory (lanes 8i..8i+7 give the 16-byte
-// rows of matrix i); lane (g, c) receives row g, columns 2c and 2c+1 of each.
-__device__ __forceinline__ void ldmatrix_x4(uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3, uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3) : "r"(addr));
-}
-// (p0, p1) = hi + lo, hi and lo packed bf16 pairs (round to nearest even);
-// hi + lo carries 16 significant bits of each p.
-__device__ __forceinline__ void split_bf16x2(float p0, float p1, uint32_t &hi, uint32_t &lo) {
-    hi = pack_bf16x2(__float_as_uint(p0), __float_as_uint(p1));
-    const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xFFFF0000u);
-    lo = pack_bf16x2(__float_as_uint(p0 - h0), __float_as_uint(p1 - h1));
-}
-
-// Merge one chunk's (m_c, l_c, o_c) into the running (m, l, o) of a query
-// row, in chunk order: m' = max(m, m_c); o = o e^{m - m'} + o_c e^{m_c - m'},
-// l likewise (the first chunk finds m = -inf, l = o = 0). Decode and extend
-// attention both merge through this one definition.
-__device__ __forceinline__ void merge_factors(float m, float m_c, float &m_new, float &alpha, float &beta) {
-    m_new = fmaxf(m, m_c);
-    alpha = expf(__fsub_rn(m, m_new));
-    beta = expf(__fsub_rn(m_c, m_new));
-}
-__device__ __forceinline__ float merge_value(float run, float chunk, float alpha, float beta) {
-    return __fmaf_rn(chunk, beta, __fmul_rn(run, alpha));
-}
 
 struct AttnParams {
     const uint16_t *Q;       // [B][Hq][D]
@@ -683,14 +631,20 @@ attn_combine_kernel(const AttnParams p) {
 constexpr int kExtRows = 128;                  // query rows (token, head) per CTA: one m16 tile per warp
 constexpr int kExtThreads = 256;
 // K and V tiles twice (the next chunk loads while this one is used), q rows,
-// the K/V row offsets of three chunks.
+// the K/V row offsets of three chunks. Over the 4-bit cache: four chunks' row
+// offsets, and the codes and scales of two chunks (K then V).
 constexpr int kExtSmem = 4 * kTileBytes + kExtRows * kD * 2 + 3 * kChunk * 8;
+constexpr int kI4StageCodes = kChunk * kI4Row, kI4StageScales = kChunk * kI4Scales * 2;
+constexpr int kI4Stage = 2 * (kI4StageCodes + kI4StageScales);
+constexpr int kExtSmemI4 = kExtSmem + kChunk * 8 + 2 * kI4Stage;
+static_assert(kExtSmemI4 <= 232448, "one CTA's shared memory");
 
 struct ExtParams {
     const uint16_t *Q;       // [total_q][Hq][D]
     const int32_t *cu_q;     // [B+1]
     const uint16_t *K;       // [blocks][bs][Hkv][D]
     const uint16_t *V;
+    KvInt4 c;                // the 4-bit form's cache, in place of K and V
     const int32_t *table;    // [B][max_blocks]
     const int32_t *lens;     // [B], cached length including the new tokens
     uint16_t *O;             // [total_q][Hq][D]
@@ -705,16 +659,21 @@ struct ExtParams {
 __device__ __forceinline__ void turn_wait(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void turn_pass(int id) { asm volatile("bar.arrive %0, 256;" ::"r"(id) : "memory"); }
 
-template <int G>
+// I4: over the 4-bit cache. Its codes and scales arrive in staging buffers two
+// chunks ahead, and one chunk ahead the CTA expands them into the same bf16
+// tile that the bf16 form copies, so everything after the tile is shared.
+template <int G, bool I4>
 __global__ void __launch_bounds__(kExtThreads, 1)
 attn_extend_kernel(const ExtParams p) {
+    constexpr int kRowBufs = I4 ? 4 : 3;               // chunks whose row offsets are held
     constexpr int kTQ = kExtRows / G;                  // query tokens per CTA
     grid_dep_wait();      // earlier work of the stream is complete and visible
     grid_dep_launch();
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t *KV = smem;                                                    // [2][K, V] tiles, swizzled rows
     uint16_t *qb = reinterpret_cast<uint16_t *>(smem + 4 * kTileBytes);   // [kExtRows][kD] bf16
-    int64_t *rowoff = reinterpret_cast<int64_t *>(qb + kExtRows * kD);     // [3][kChunk], -1: no row
+    int64_t *rowoff = reinterpret_cast<int64_t *>(qb + kExtRows * kD);     // [kRowBufs][kChunk], -1: no row
+    uint8_t *stage = reinterpret_cast<uint8_t *>(rowoff + kRowBufs * kChunk); // I4: [2][K codes, V codes, K, V scales]
     // blockIdx.x = (tile from the last, sequence, KV head): the tiles with the
     // latest tokens (the most chunks) of every sequence start first, so the
     // light ones fill the tail
@@ -747,7 +706,7 @@ attn_extend_kernel(const ExtParams p) {
         cp_async_16(smem_u32(qb + r * kD + ((x ^ (r & 7)) * 8)),
                     v ? p.Q + ((q0 + i0 + r / G) * p.Hq + g * G + r % G) * kD + x * 8 : p.Q, v ? 16u : 0u);
     }
-    // row offsets of chunk c's K/V rows (threads 0..127; buffer c % 3, so a
+    // row offsets of chunk c's K/V rows (threads 0..127; buffer c % kRowBufs, so a
     // buffer is rewritten only after every warp has left the chunk that used it)
     auto chunk_rows = [&](int c) -> int {
         int bad = 0;
@@ -757,19 +716,42 @@ attn_extend_kernel(const ExtParams p) {
             if (j < L_last) {
                 const int64_t blk = p.table[b * p.max_blocks + j / p.bs];
                 if (blk >= 0 && blk < p.num_blocks) {
-                    off = ((blk * p.bs + j % p.bs) * p.Hkv + g) * kD;
+                    off = I4 ? (blk * p.Hkv + g) * p.bs + j % p.bs : ((blk * p.bs + j % p.bs) * p.Hkv + g) * kD;
                 } else {
                     atomicOr(p.status, kDevBadOffsets);
                     bad = 1;
                 }
             }
-            rowoff[(c % 3) * kChunk + tid] = off;
+            rowoff[(c % kRowBufs) * kChunk + tid] = off;
         }
         return bad;
     };
     auto issue_chunk = [&](int c) {                    // after chunk_rows(c) and a barrier
         const int buf = c & 1;
-        const int64_t *ro = rowoff + (c % 3) * kChunk;
+        const int64_t *ro = rowoff + (c % kRowBufs) * kChunk;
+        if (I4) {
+            // 64 bytes of codes (16 a thread) and 8 of scales per row, K then V
+            const uint32_t dst0 = smem_u32(stage + buf * kI4Stage);
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                const uint8_t *codes = which == 0 ? p.c.kc : p.c.vc;
+                const uint8_t *scales = reinterpret_cast<const uint8_t *>(which == 0 ? p.c.ks : p.c.vs);
+#pragma unroll
+                for (int r = 0; r < kChunk * 4 / kExtThreads; ++r) {
+                    const int i = tid + r * kExtThreads;
+                    const int64_t off = ro[i >> 2];
+                    cp_async_16(dst0 + which * kI4StageCodes + i * 16,
+                                off >= 0 ? codes + off * kI4Row + (i & 3) * 16 : codes, off >= 0 ? 16u : 0u);
+                }
+                if (tid < kChunk) {
+                    const int64_t off = ro[tid];
+                    cp_async_8(dst0 + 2 * kI4StageCodes + which * kI4StageScales + tid * 8,
+                               off >= 0 ? scales + off * kI4Scales * 2 : scales, off >= 0 ? 8u : 0u);
+                }
+            }
+            cp_async_commit();
+            return;
+        }
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             const uint16_t *src = which == 0 ? p.K : p.V;
@@ -785,9 +767,48 @@ attn_extend_kernel(const ExtParams p) {
         }
         cp_async_commit();
     };
+    // I4: chunk c's staged codes to the bf16 tile. A thread takes one row's 32
+    // dimensions of a scale at a time: the word of dimensions 2a, 2a + 1 mod 8
+    // gives their pairs at the four 16-byte pieces of those dimensions.
+    auto expand_chunk = [&](int c) {
+        const uint8_t *st = stage + (c & 1) * kI4Stage;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const uint32_t dst0 = smem_u32(KV + (2 * (c & 1) + which) * kTileBytes);
+#pragma unroll
+            for (int r = 0; r < kChunk * 4 / kExtThreads; ++r) {
+                const int t = (tid + r * kExtThreads) >> 2, i = tid & 3;
+                const uint8_t *codes = st + which * kI4StageCodes + t * kI4Row;
+                const uint32_t sc = *reinterpret_cast<const uint16_t *>(st + 2 * kI4StageCodes + which * kI4StageScales +
+                                                                        t * kI4Scales * 2 + 2 * i);
+                const uint32_t s2 = sc | (sc << 16), c2 = mul_bf16x2(s2, kBf16x2_m136);
+                uint32_t v[4][4];                      // [a][q]
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    uint32_t w;
+                    if (which == 0) {
+                        w = *reinterpret_cast<const uint32_t *>(codes + (4 * a + i) * 4);
+                    } else {
+                        const uint16_t *h = reinterpret_cast<const uint16_t *>(codes);
+                        w = static_cast<uint32_t>(h[8 * a + i]) | (static_cast<uint32_t>(h[8 * a + 4 + i]) << 16);
+                    }
+                    i4_expand(w, s2, c2, v[a]);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    st_shared_v4(dst0 + t * kRowBytes + (((4 * i + q) ^ (t & 7)) << 4), v[0][q], v[1][q], v[2][q], v[3][q]);
+            }
+        }
+    };
     // q rows and chunk 0's row offsets; bad_cur: chunk c has a token without a valid block
-    int bad_cur = __syncthreads_or(chunk_rows(0));
+    int bad_cur = __syncthreads_or(chunk_rows(0)), bad_two = 0;
     issue_chunk(0);
+    if (I4) {                                          // chunk 0's tile, and chunk 1's codes on the way
+        cp_async_wait<0>();
+        bad_two = __syncthreads_or(nchunks > 1 ? chunk_rows(1) : 0);
+        if (nchunks > 1) issue_chunk(1);
+        expand_chunk(0);
+    }
 
     const int gq = lane >> 2, cq = lane & 3;           // fragment row group, column pair
     const int rt = warp;                               // this warp's 16-row tile
@@ -815,22 +836,25 @@ attn_extend_kernel(const ExtParams p) {
 
     for (int c = 0; c < nchunks; ++c) {
         const int j0 = c * kChunk;
-        const int64_t *ro = rowoff + (c % 3) * kChunk;
+        const int64_t *ro = rowoff + (c % kRowBufs) * kChunk;
         const uint8_t *Ks = KV + (2 * (c & 1)) * kTileBytes;
         const uint8_t *Vs = KV + (2 * (c & 1) + 1) * kTileBytes;
-        const bool more = c + 1 < nchunks;
-        // every warp has left chunk c - 1 (its K/V buffer is free) and chunk
-        // c + 1's row offsets are written
-        const int bad_next = __syncthreads_or(more ? chunk_rows(c + 1) : 0);
+        const int ahead = I4 ? 2 : 1;                  // chunks between a chunk's copies and its use
+        const bool more = c + ahead < nchunks;
+        // every warp has left chunk c - 1 (its K/V buffer is free), chunk
+        // c + ahead's row offsets are written, and (I4) chunk c's tile is
+        const int bad_next = __syncthreads_or(more ? chunk_rows(c + ahead) : 0);
         const bool bad = bad_cur != 0;
-        bad_cur = bad_next;
+        bad_cur = I4 ? bad_two : bad_next;
+        bad_two = bad_next;
         if (more) {
-            issue_chunk(c + 1);
-            cp_async_wait<1>();                        // this thread's copies of chunk c
+            issue_chunk(c + ahead);
+            cp_async_wait<1>();                        // this thread's copies of chunk c (I4: c + 1)
         } else {
             cp_async_wait<0>();
         }
         __syncthreads();                               // everyone's
+        if (I4 && c + 1 < nchunks) expand_chunk(c + 1);
 
         // tokens of this chunk each row sees (decode of the sequence cut after the row's token)
         const int na = max(0, min(kChunk, len_a - j0)), nb = max(0, min(kChunk, len_b - j0));
@@ -895,6 +919,10 @@ attn_extend_kernel(const ExtParams p) {
                                                      : -INFINITY;
                     m[e >> 1] = fmaxf(m[e >> 1], s[nt][e]);
                 }
+        }
+        if (I4 && bad) {                               // a chunk without a valid token counts nothing
+            m[0] = fmaxf(m[0], kNoScore);
+            m[1] = fmaxf(m[1], kNoScore);
         }
         // per row: max (any order gives the same value), then e^(s - m) for the
         // tokens it sees (0 past them)
@@ -1112,23 +1140,43 @@ bi_status launch_attention_decode(const void *Q, const void *K, const void *V, c
     return launch_pdl(attn_combine_kernel, dim3(Hq, static_cast<unsigned>(B)), dim3(kCombineThreads), 0, s, p);
 }
 
-template <int G>
-bi_status launch_extend_g(const dim3 &grid, const ExtParams &p, cudaStream_t s) {
-    static unsigned long long configured = 0;
-    if (ensure_smem_attr(reinterpret_cast<const void *>(attn_extend_kernel<G>), kExtSmem, &configured) != BI_OK)
-        return BI_ERR_CUDA;
-    return launch_pdl(attn_extend_kernel<G>, grid, dim3(kExtThreads), kExtSmem, s, p);
+bi_status launch_attention_combine(const void *workspace, const int32_t *lens, int32_t max_blocks, int32_t bs, int64_t B,
+                                   int32_t Hq, int32_t max_len, void *O, cudaStream_t s) {
+    AttnParams p{};
+    p.ws = static_cast<float *>(const_cast<void *>(workspace));
+    p.lens = lens;
+    p.O = static_cast<uint16_t *>(O);
+    p.batch = B;
+    p.max_blocks = max_blocks;
+    p.Hq = Hq;
+    p.bs = bs;
+    p.chunks = static_cast<int32_t>((static_cast<int64_t>(max_len) + kChunk - 1) / kChunk);
+    p.max_len = max_len;
+    p.status = device_status_word();
+    return launch_pdl(attn_combine_kernel, dim3(Hq, static_cast<unsigned>(B)), dim3(kCombineThreads), 0, s, p);
 }
 
-bi_status launch_attention_extend(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K, const void *V,
-                                  const int32_t *table, int32_t max_blocks, int64_t num_blocks, const int32_t *lens,
-                                  int64_t B, int32_t Hq, int32_t Hkv, int32_t bs, int32_t max_len, int32_t max_q,
-                                  float scale, void *O, cudaStream_t s) {
+template <int G, bool I4>
+bi_status launch_extend_g(const dim3 &grid, const ExtParams &p, cudaStream_t s) {
+    static unsigned long long configured = 0;
+    constexpr int smem = I4 ? kExtSmemI4 : kExtSmem;
+    if (ensure_smem_attr(reinterpret_cast<const void *>(attn_extend_kernel<G, I4>), smem, &configured) != BI_OK)
+        return BI_ERR_CUDA;
+    return launch_pdl(attn_extend_kernel<G, I4>, grid, dim3(kExtThreads), smem, s, p);
+}
+
+// K and V (bf16 cache) or c (4-bit cache)
+template <bool I4>
+bi_status launch_extend(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K, const void *V,
+                        const KvInt4 &c, const int32_t *table, int32_t max_blocks, int64_t num_blocks,
+                        const int32_t *lens, int64_t B, int32_t Hq, int32_t Hkv, int32_t bs, int32_t max_len,
+                        int32_t max_q, float scale, void *O, cudaStream_t s) {
     ExtParams p{};
     p.Q = static_cast<const uint16_t *>(Q);
     p.cu_q = cu_q;
     p.K = static_cast<const uint16_t *>(K);
     p.V = static_cast<const uint16_t *>(V);
+    p.c = c;
     p.table = table;
     p.lens = lens;
     p.O = static_cast<uint16_t *>(O);
@@ -1149,12 +1197,27 @@ bi_status launch_attention_extend(const void *Q, const int32_t *cu_q, int32_t to
     if (ctas_x > 0x7fffffff) return BI_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(ctas_x));
     switch (G) {
-        case 1: return launch_extend_g<1>(grid, p, s);
-        case 2: return launch_extend_g<2>(grid, p, s);
-        case 4: return launch_extend_g<4>(grid, p, s);
-        case 8: return launch_extend_g<8>(grid, p, s);
+        case 1: return launch_extend_g<1, I4>(grid, p, s);
+        case 2: return launch_extend_g<2, I4>(grid, p, s);
+        case 4: return launch_extend_g<4, I4>(grid, p, s);
+        case 8: return launch_extend_g<8, I4>(grid, p, s);
         default: return BI_ERR_UNSUPPORTED;
     }
+}
+
+bi_status launch_attention_extend(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K, const void *V,
+                                  const int32_t *table, int32_t max_blocks, int64_t num_blocks, const int32_t *lens,
+                                  int64_t B, int32_t Hq, int32_t Hkv, int32_t bs, int32_t max_len, int32_t max_q,
+                                  float scale, void *O, cudaStream_t s) {
+    return launch_extend<false>(Q, cu_q, total_q, K, V, KvInt4{}, table, max_blocks, num_blocks, lens, B, Hq, Hkv, bs,
+                                max_len, max_q, scale, O, s);
+}
+
+bi_status launch_attention_extend_int4(const void *Q, const int32_t *cu_q, int32_t total_q, const KvInt4 &c,
+                                       const int32_t *table, int32_t max_blocks, const int32_t *lens, int64_t B,
+                                       int32_t Hq, int32_t max_len, int32_t max_q, float scale, void *O, cudaStream_t s) {
+    return launch_extend<true>(Q, cu_q, total_q, nullptr, nullptr, c, table, max_blocks, c.num_blocks, lens, B, Hq, c.Hkv,
+                               c.bs, max_len, max_q, scale, O, s);
 }
 
 }  // namespace bi
