@@ -425,10 +425,10 @@ BI_API bi_status bi_attention_decode_noalloc(const void *Q, const void *K_cache,
  * on the exact quotients, so the stored form does not depend on how or with
  * what else it was computed, and n * s is a bf16 number exactly. A group that
  * holds an infinity or a NaN reads back as NaN. Magnitudes above 7 * 2^120
- * saturate. The order of the codes inside a row is chosen for the kernels and
- * differs between keys and values: dimension d = 32 i + 8 q + r (r < 8, q < 4)
- * is nibble q (code n + 8) of the row's 16-bit word 8 (r / 2) + 2 i + r % 2 of
- * keys, 4 r + i of values. Code rows are 16-byte aligned, scales 8-byte.
+ * saturate. Dimension d = 32 i + 8 q + r (q < 4, r < 8) is nibble q (code
+ * n + 8) of 16-bit word r of the row's 16-byte segment for group i, which
+ * stands at place i ^ (offset / 2 % 4) of the row, offset the token's place in
+ * its block. All four arrays are 16-byte aligned.
  * The attention over this cache multiplies the same bf16 operands in the same
  * order as bi_attention_decode / _extend over a bf16 cache that holds the same
  * values: the results are the same bits.
@@ -481,14 +481,24 @@ BI_API bi_status bi_attention_decode_int4(const void *Q, const uint8_t *k_codes,
  * bi_attention_extend_int4 -- bi_attention_extend over the 4-bit cache, which
  * already holds the new tokens' keys and values: the same bits as
  * bi_attention_extend over a bf16 cache holding the same values, and as
- * bi_attention_decode_int4 of each token's cut sequence. No workspace.
+ * bi_attention_decode_int4 of each token's cut sequence.
+ *   workspace  caller-owned device scratch, NULLABLE. With at least
+ *              bi_attention_extend_int4_workspace_size(...) > 0 bytes, calls
+ *              with few new tokens a sequence (drafts to verify) are split over
+ *              the cache's chunks like decode; without, or where that size is
+ *              0, one CTA walks the chunks of each tile of new tokens. The
+ *              bits are the same.
+ * bi_attention_extend_int4_workspace_size returns -1 for arguments out of range.
  */
+BI_API int64_t bi_attention_extend_int4_workspace_size(int64_t total_q, int32_t Hq, int32_t Hkv, int32_t max_seq_len,
+                                                       int32_t max_q_len);
 BI_API bi_status bi_attention_extend_int4(const void *Q, const int32_t *cu_q, int32_t total_q, const uint8_t *k_codes,
                                           const void *k_scales, const uint8_t *v_codes, const void *v_scales,
                                           const int32_t *block_table, int32_t max_blocks_per_seq, int64_t num_blocks,
                                           const int32_t *seq_lens, int64_t B, int32_t Hq, int32_t Hkv,
                                           int32_t head_dim, int32_t block_size, int32_t max_seq_len,
-                                          int32_t max_q_len, float scale, void *O, bi_stream stream);
+                                          int32_t max_q_len, float scale, void *workspace,
+                                          int64_t workspace_bytes, void *O, bi_stream stream);
 
 /*
  * bi_gemm_int4 -- batch-invariant linear layer with 4-bit weights and group scales.

@@ -85,7 +85,8 @@ def load() -> ctypes.CDLL:
             "bi_kv_int4_read": [P, P, P, P, I64, I32, I32, I32, P, I64, P, I64, P, I64, P],
             "bi_attention_decode_int4": [P, P, P, P, P, P, I32, I64, P, I64, I32, I32, I32, I32, I32, F, P, I64, P, P],
             "bi_attention_extend_int4": [P, P, I32, P, P, P, P, P, I32, I64, P, I64, I32, I32, I32, I32, I32, I32, F, P,
-                                         P],
+                                         I64, P, P],
+            "bi_attention_extend_int4_workspace_size": [I64, I32, I32, I32, I32],
             "bi_gemm_int4": [P, I64, P, P, P, P, I64, I64, I64, I64, I64, P],
             "bi_plan": [I32, I64, I64, I64, I32, ctypes.POINTER(Plan)],
             "bi_device_status": [P],
@@ -99,6 +100,7 @@ def load() -> ctypes.CDLL:
             fn.restype = ctypes.c_int
         lib.bi_status_string.restype = ctypes.c_char_p
         lib.bi_attention_decode_workspace_size.restype = ctypes.c_int64
+        lib.bi_attention_extend_int4_workspace_size.restype = ctypes.c_int64
         _lib = lib
         return lib
 
@@ -564,27 +566,39 @@ def attention_decode_int4(Q, cache: KVInt4Cache, block_table, seq_lens, max_seq_
     return O
 
 
+def attention_extend_int4_workspace_size(total_q: int, Hq: int, Hkv: int, max_seq_len: int, max_q_len: int) -> int:
+    return int(load().bi_attention_extend_int4_workspace_size(total_q, Hq, Hkv, max_seq_len, max_q_len))
+
+
 def attention_extend_int4(Q, cu_q, cache: KVInt4Cache, block_table, seq_lens, max_seq_len: int, max_q_len: int,
-                          scale: float, O=None, stream=None):
+                          scale: float, workspace=None, O=None, stream=None):
     """Causal extend (prefill) attention over the 4-bit cache: the bits of ``attention_extend`` over a bf16 cache
     of the same values.
 
     Q bf16 [total_q, Hq, 128]; cu_q int32 [B+1]; block_table int32 [B, max_blocks];
-    seq_lens int32 [B], the new tokens (already in the cache) included."""
+    seq_lens int32 [B], the new tokens (already in the cache) included. The
+    workspace (uint8, ``attention_extend_int4_workspace_size`` bytes) is
+    allocated with torch if not given."""
     import torch
     nblk, Hkv, bs = _attention_int4_args(Q, cache, block_table, seq_lens, O)
     _dev(cu_q, torch.int32, "cu_q")
     B = seq_lens.numel()
     if cu_q.numel() != B + 1 or not cu_q.is_contiguous():
         raise ValueError("cu_q must be contiguous [B + 1]")
-    _one_device(Q, cu_q, block_table, seq_lens, O, *cache)
+    _one_device(Q, cu_q, block_table, seq_lens, workspace, O, *cache)
     T, Hq, D = Q.shape
+    if workspace is None:
+        workspace = _new(max(attention_extend_int4_workspace_size(T, Hq, Hkv, max_seq_len, max_q_len), 16), torch.uint8, Q,
+                         stream)
+    _dev(workspace, torch.uint8, "workspace")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     if O is None:
         O = _new(Q.shape, Q.dtype, Q, stream)
     _check(load().bi_attention_extend_int4(_ptr(Q), _ptr(cu_q), T, *map(_ptr, cache), _ptr(block_table),
                                            block_table.shape[1], nblk, _ptr(seq_lens), B, Hq, Hkv, D, bs, max_seq_len,
-                                           max_q_len, float(scale), _ptr(O), _stream(stream)),
-           "bi_attention_extend_int4")
+                                           max_q_len, float(scale), _ptr(workspace), workspace.numel(), _ptr(O),
+                                           _stream(stream)), "bi_attention_extend_int4")
     return O
 
 

@@ -359,7 +359,7 @@ bi_status check_kv_int4(const uint8_t *kc, const void *ks, const uint8_t *vc, co
     // rows are numbered in 32 bits (2^32 of them hold 288 GB of codes)
     const int64_t per = static_cast<int64_t>(Hkv) * bs;
     if (num_blocks > (static_cast<int64_t>(0xFFFFFFFF) - 1) / per) return BI_ERR_UNSUPPORTED;
-    if (!aligned16(kc) || !aligned16(vc) || !aligned8(ks) || !aligned8(vs)) return BI_ERR_MISALIGNED;
+    if (!aligned16(kc) || !aligned16(vc) || !aligned16(ks) || !aligned16(vs)) return BI_ERR_MISALIGNED;
     *out = KvInt4{const_cast<uint8_t *>(kc), static_cast<uint16_t *>(const_cast<void *>(ks)), const_cast<uint8_t *>(vc),
                   static_cast<uint16_t *>(const_cast<void *>(vs)), num_blocks, Hkv, bs};
     return BI_OK;
@@ -429,12 +429,20 @@ bi_status bi_attention_decode_int4(const void *Q, const uint8_t *k_codes, const 
                                         workspace, O, as_stream(stream));
 }
 
+int64_t bi_attention_extend_int4_workspace_size(int64_t total_q, int32_t Hq, int32_t Hkv, int32_t max_seq_len,
+                                                int32_t max_q_len) {
+    if (total_q < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || max_q_len < 1 || max_seq_len < 1 ||
+        max_seq_len > BI_ATTENTION_MAX_SEQ_LEN)
+        return -1;
+    return attention_extend_int4_workspace_bytes(total_q, Hq, Hkv, max_seq_len, max_q_len);
+}
+
 bi_status bi_attention_extend_int4(const void *Q, const int32_t *cu_q, int32_t total_q, const uint8_t *k_codes,
                                    const void *k_scales, const uint8_t *v_codes, const void *v_scales,
                                    const int32_t *block_table, int32_t max_blocks_per_seq, int64_t num_blocks,
                                    const int32_t *seq_lens, int64_t B, int32_t Hq, int32_t Hkv, int32_t head_dim,
-                                   int32_t block_size, int32_t max_seq_len, int32_t max_q_len, float scale, void *O,
-                                   bi_stream stream) {
+                                   int32_t block_size, int32_t max_seq_len, int32_t max_q_len, float scale,
+                                   void *workspace, int64_t workspace_bytes, void *O, bi_stream stream) {
     if (B < 0 || B > 65535 || total_q < 0 || Hq < 1 || Hkv < 1 || max_seq_len < 1 ||
         max_seq_len > BI_ATTENTION_MAX_SEQ_LEN || max_q_len < 1 || max_blocks_per_seq < 1 || !(scale == scale))
         return BI_ERR_INVALID_ARG;
@@ -446,10 +454,15 @@ bi_status bi_attention_extend_int4(const void *Q, const int32_t *cu_q, int32_t t
     if (Hq % Hkv != 0) return BI_ERR_UNSUPPORTED;
     const int32_t G = Hq / Hkv;
     if (G != 1 && G != 2 && G != 4 && G != 8) return BI_ERR_UNSUPPORTED;
-    if (!aligned16(Q) || !aligned16(O) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(cu_q))
+    if (!aligned16(Q) || !aligned16(O) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(cu_q) ||
+        !aligned16(workspace))
         return BI_ERR_MISALIGNED;
     st = require_device();
     if (st != BI_OK) return st;
+    const int64_t few = attention_extend_int4_workspace_bytes(total_q, Hq, Hkv, max_seq_len, max_q_len);
+    if (workspace && few > 0 && workspace_bytes >= few)
+        return launch_attention_extend_int4_few(Q, cu_q, total_q, c, block_table, max_blocks_per_seq, seq_lens, B, Hq,
+                                                max_seq_len, max_q_len, scale, workspace, O, as_stream(stream));
     return launch_attention_extend_int4(Q, cu_q, total_q, c, block_table, max_blocks_per_seq, seq_lens, B, Hq, max_seq_len,
                                         max_q_len, scale, O, as_stream(stream));
 }

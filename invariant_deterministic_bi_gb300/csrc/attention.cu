@@ -716,7 +716,8 @@ attn_extend_kernel(const ExtParams p) {
             if (j < L_last) {
                 const int64_t blk = p.table[b * p.max_blocks + j / p.bs];
                 if (blk >= 0 && blk < p.num_blocks) {
-                    off = I4 ? (blk * p.Hkv + g) * p.bs + j % p.bs : ((blk * p.bs + j % p.bs) * p.Hkv + g) * kD;
+                    off = I4 ? ((blk * p.Hkv + g) * p.bs + j % p.bs) * 4 + i4_place(0, j % p.bs)   // row, segment 0's place
+                             : ((blk * p.bs + j % p.bs) * p.Hkv + g) * kD;
                 } else {
                     atomicOr(p.status, kDevBadOffsets);
                     bad = 1;
@@ -740,13 +741,13 @@ attn_extend_kernel(const ExtParams p) {
                 for (int r = 0; r < kChunk * 4 / kExtThreads; ++r) {
                     const int i = tid + r * kExtThreads;
                     const int64_t off = ro[i >> 2];
-                    cp_async_16(dst0 + which * kI4StageCodes + i * 16,
-                                off >= 0 ? codes + off * kI4Row + (i & 3) * 16 : codes, off >= 0 ? 16u : 0u);
+                    cp_async_16(dst0 + which * kI4StageCodes + i * 16,   // segment i & 3
+                                off >= 0 ? codes + (off >> 2) * kI4Row + ((i ^ off) & 3) * 16 : codes, off >= 0 ? 16u : 0u);
                 }
                 if (tid < kChunk) {
                     const int64_t off = ro[tid];
                     cp_async_8(dst0 + 2 * kI4StageCodes + which * kI4StageScales + tid * 8,
-                               off >= 0 ? scales + off * kI4Scales * 2 : scales, off >= 0 ? 8u : 0u);
+                               off >= 0 ? scales + (off >> 2) * kI4Scales * 2 : scales, off >= 0 ? 8u : 0u);
                 }
             }
             cp_async_commit();
@@ -782,18 +783,12 @@ attn_extend_kernel(const ExtParams p) {
                 const uint32_t sc = *reinterpret_cast<const uint16_t *>(st + 2 * kI4StageCodes + which * kI4StageScales +
                                                                         t * kI4Scales * 2 + 2 * i);
                 const uint32_t s2 = sc | (sc << 16), c2 = mul_bf16x2(s2, kBf16x2_m136);
+                const uint4 seg = *reinterpret_cast<const uint4 *>(codes + 16 * i);
                 uint32_t v[4][4];                      // [a][q]
-#pragma unroll
-                for (int a = 0; a < 4; ++a) {
-                    uint32_t w;
-                    if (which == 0) {
-                        w = *reinterpret_cast<const uint32_t *>(codes + (4 * a + i) * 4);
-                    } else {
-                        const uint16_t *h = reinterpret_cast<const uint16_t *>(codes);
-                        w = static_cast<uint32_t>(h[8 * a + i]) | (static_cast<uint32_t>(h[8 * a + 4 + i]) << 16);
-                    }
-                    i4_expand(w, s2, c2, v[a]);
-                }
+                i4_expand(seg.x, s2, c2, v[0]);
+                i4_expand(seg.y, s2, c2, v[1]);
+                i4_expand(seg.z, s2, c2, v[2]);
+                i4_expand(seg.w, s2, c2, v[3]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     st_shared_v4(dst0 + t * kRowBytes + (((4 * i + q) ^ (t & 7)) << 4), v[0][q], v[1][q], v[2][q], v[3][q]);
@@ -1137,22 +1132,6 @@ bi_status launch_attention_decode(const void *Q, const void *K, const void *V, c
         case 8: SPLIT_LAUNCH(8); break;
         default: return BI_ERR_UNSUPPORTED;
     }
-    return launch_pdl(attn_combine_kernel, dim3(Hq, static_cast<unsigned>(B)), dim3(kCombineThreads), 0, s, p);
-}
-
-bi_status launch_attention_combine(const void *workspace, const int32_t *lens, int32_t max_blocks, int32_t bs, int64_t B,
-                                   int32_t Hq, int32_t max_len, void *O, cudaStream_t s) {
-    AttnParams p{};
-    p.ws = static_cast<float *>(const_cast<void *>(workspace));
-    p.lens = lens;
-    p.O = static_cast<uint16_t *>(O);
-    p.batch = B;
-    p.max_blocks = max_blocks;
-    p.Hq = Hq;
-    p.bs = bs;
-    p.chunks = static_cast<int32_t>((static_cast<int64_t>(max_len) + kChunk - 1) / kChunk);
-    p.max_len = max_len;
-    p.status = device_status_word();
     return launch_pdl(attn_combine_kernel, dim3(Hq, static_cast<unsigned>(B)), dim3(kCombineThreads), 0, s, p);
 }
 

@@ -117,9 +117,6 @@ bi_status launch_attention_extend(const void *Q, const int32_t *cu_q, int32_t to
                                   const int32_t *table, int32_t max_blocks, int64_t num_blocks, const int32_t *lens,
                                   int64_t B, int32_t Hq, int32_t Hkv, int32_t bs, int32_t max_len, int32_t max_q,
                                   float scale, void *O, cudaStream_t s);
-// Step 2 of decode attention on the chunk results in `workspace`.
-bi_status launch_attention_combine(const void *workspace, const int32_t *lens, int32_t max_blocks, int32_t bs, int64_t B,
-                                   int32_t Hq, int32_t max_len, void *O, cudaStream_t s);
 bi_status launch_kv_int4_append(const KvInt4 &c, const int64_t *slots, const void *K, int64_t ldk, const void *V,
                                 int64_t ldv, int64_t T, cudaStream_t s);
 bi_status launch_kv_int4_read(const KvInt4 &c, const int64_t *slots, void *K, int64_t ldk, void *V, int64_t ldv,
@@ -130,6 +127,12 @@ bi_status launch_attention_decode_int4(const void *Q, const KvInt4 &c, const int
 bi_status launch_attention_extend_int4(const void *Q, const int32_t *cu_q, int32_t total_q, const KvInt4 &c,
                                        const int32_t *table, int32_t max_blocks, const int32_t *lens, int64_t B,
                                        int32_t Hq, int32_t max_len, int32_t max_q, float scale, void *O, cudaStream_t s);
+bi_status launch_attention_extend_int4_few(const void *Q, const int32_t *cu_q, int32_t total_q, const KvInt4 &c,
+                                           const int32_t *table, int32_t max_blocks, const int32_t *lens, int64_t B,
+                                           int32_t Hq, int32_t max_len, int32_t max_q, float scale, void *workspace,
+                                           void *O, cudaStream_t s);
+// Bytes the split over chunks wants for these sizes; 0: the tiled kernel is used and wants none; -1: past int64_t.
+int64_t attention_extend_int4_workspace_bytes(int64_t total_q, int32_t Hq, int32_t Hkv, int32_t max_len, int32_t max_q);
 bi_status launch_gemm_int4(const void *X, int64_t ldx, const uint8_t *W, const void *scales, const uint8_t *zeros, void *Y,
                            int64_t ldy, int64_t M, int64_t N, int64_t K, int64_t group, cudaStream_t s);
 bi_status launch_bounds_check(int32_t index, int32_t limit, cudaStream_t s);

@@ -7,7 +7,7 @@
 // on the exact quotients. Half a warp takes one row: lane (i, q) holds the
 // eight dimensions 32 i + 8 q + r as one 16-byte load, the four lanes of a
 // group share its maximum by two shuffles, and their codes, each at nibble q,
-// are joined by or-shuffles into the row's 16-bit words (layout: kv_int4.cuh).
+// are joined by or-shuffles into the segment's words (layout: kv_int4.cuh).
 // The two half warps take the K and the V row of the same token and head.
 //
 // Both kernels are bound by memory: 512 bytes in and 144 out per token and KV
@@ -91,16 +91,11 @@ kv_int4_append_kernel(const RowsParams p) {
             code[k] |= __shfl_xor_sync(0xffffffffu, code[k], 1);
             code[k] |= __shfl_xor_sync(0xffffffffu, code[k], 2);
         }
-        // word a = r / 2 (code[a]): lane q stores r = 2q and 2q + 1
+        // code[a] is the segment's 32-bit word of r = 2a, 2a + 1: lane q stores word q
         const uint32_t mine = q == 0 ? code[0] : q == 1 ? code[1] : q == 2 ? code[2] : code[3];
         if (!BI_IN_BOUNDS(row < p.c.num_blocks * p.c.Hkv * p.c.bs, p.status)) continue;
-        if (!is_v) {
-            *reinterpret_cast<uint32_t *>(p.c.kc + row * kI4Row + (4 * q + i) * 4) = mine;
-        } else {
-            uint16_t *d = reinterpret_cast<uint16_t *>(p.c.vc + row * kI4Row);
-            d[8 * q + i] = static_cast<uint16_t>(mine & 0xFFFFu);
-            d[8 * q + 4 + i] = static_cast<uint16_t>(mine >> 16);
-        }
+        const int at = i4_place(i, static_cast<int>(row % p.c.bs)) * 16 + 4 * q;
+        *reinterpret_cast<uint32_t *>((is_v ? p.c.vc : p.c.kc) + row * kI4Row + at) = mine;
         if (q == 0)
             (is_v ? p.c.vs : p.c.ks)[row * kI4Scales + i] = static_cast<uint16_t>(finite ? __float_as_uint(s) >> 16 : 0x7FFFu);
     }
@@ -117,23 +112,19 @@ kv_int4_read_kernel(const RowsParams p) {
         const int64_t t = w / p.c.Hkv;
         const int g = static_cast<int>(w % p.c.Hkv);
         const int64_t row = slot_row(p, t, g);
-        uint32_t word = 0, sc = 0;
+        uint4 seg = make_uint4(0u, 0u, 0u, 0u);
+        uint32_t sc = 0;
         if (row >= 0 && BI_IN_BOUNDS(row < p.c.num_blocks * p.c.Hkv * p.c.bs, p.status)) {
-            word = *reinterpret_cast<const uint32_t *>((is_v ? p.c.vc : p.c.kc) + row * kI4Row + (lane & 15) * 4);
+            seg = *reinterpret_cast<const uint4 *>((is_v ? p.c.vc : p.c.kc) + row * kI4Row +
+                                                   i4_place(i, static_cast<int>(row % p.c.bs)) * 16);
             sc = (is_v ? p.c.vs : p.c.ks)[row * kI4Scales + i];
         }
         const uint32_t s2 = sc | (sc << 16), c2 = mul_bf16x2(s2, kBf16x2_m136);
+        const uint32_t cw[4] = {seg.x, seg.y, seg.z, seg.w};
         uint32_t out[4];
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            // the word of r = 2a, 2a + 1 and group i: lane 4a + i of the K half warp holds it whole; of
-            // the V half warp, lanes 4a + i / 2 and 4a + 2 + i / 2 hold a half each
-            const uint32_t k = __shfl_sync(0xffffffffu, word, 4 * a + i, 16);
-            const uint32_t v0 = __shfl_sync(0xffffffffu, word, 4 * a + (i >> 1), 16);
-            const uint32_t v1 = __shfl_sync(0xffffffffu, word, 4 * a + 2 + (i >> 1), 16);
-            const uint32_t codes = is_v ? ((i & 1) ? zip16<1>(v0, v1) : zip16<0>(v0, v1)) : k;
-            out[a] = row < 0 ? 0u : fma_bf16x2(((codes >> (4 * q)) & 0x000F000Fu) | 0x43004300u, s2, c2);
-        }
+        for (int a = 0; a < 4; ++a)
+            out[a] = row < 0 ? 0u : fma_bf16x2(((cw[a] >> (4 * q)) & 0x000F000Fu) | 0x43004300u, s2, c2);
         uint16_t *dst = (is_v ? p.V + t * p.ldv : p.K + t * p.ldk) + g * kRowDims + 32 * i + 8 * q;
         *reinterpret_cast<uint4 *>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
     }

@@ -14,14 +14,16 @@
 // over the 4-bit cache multiplies the same operands as attention over a bf16
 // cache holding those values.
 //
-// Cache row of one token and KV head: 64 bytes of codes, 4 bf16 scales (one per
-// 32 dimensions). Dimension d = 32 i + 8 q + r (i, q in 0..3, r in 0..7) is
-// nibble q of the row's 16-bit word number
-//   K:  8 (r / 2) + 2 i + r % 2        V:  4 r + i
-// so that the lanes of a warp find their operands of the tensor-core products
-// in contiguous bytes: lane (row g, column pair c) of q.k takes the 16 bytes
-// r / 2 = c (all eight 16-dimension steps), lane (row g, column pair c) of p.v
-// the 8 bytes r = g (its row of all eight 16-dimension tiles).
+// Cache row of one token and KV head: 64 bytes of codes in four 16-byte
+// segments, one for each group of 32 dimensions, and 4 bf16 scales. Dimension
+// d = 32 i + 8 q + r (i, q in 0..3, r in 0..7) is nibble q of 16-bit word r of
+// segment i. That is the layout ldmatrix wants of both operands: of eight
+// tokens' segments i it gives lane (g, c) the word 2c, 2c + 1 of token g (keys:
+// dimension pairs of token g), or transposed the words g of tokens 2c, 2c + 1
+// (values: token pairs of dimension g), each time four operand pairs in one
+// register. Segment i stands at place i ^ (offset / 2 % 4), offset the token's
+// place in its block: eight consecutive tokens' segments i then lie in all the
+// shared-memory banks, also when a block is copied there as it is.
 #pragma once
 #include <cstdint>
 
@@ -61,5 +63,8 @@ __device__ __forceinline__ uint32_t dup16(uint32_t w) { return __byte_perm(w, 0,
 // (low halves of a and b) or (high halves): a's in the low half.
 template <int HI>
 __device__ __forceinline__ uint32_t zip16(uint32_t a, uint32_t b) { return __byte_perm(a, b, HI ? 0x7632 : 0x5410); }
+
+// Place of segment i in the code row of a token at this offset of its block.
+__device__ __forceinline__ int i4_place(int i, int offset) { return i ^ ((offset >> 1) & 3); }
 
 }  // namespace bi

@@ -25,13 +25,13 @@ def values(n, s):
     return (n.reshape(*s.shape, GROUP) * s[..., None]).reshape(n.shape)
 
 
-def pack(n, is_v):
-    """Codes of rows [..., 128] -> the cache's bytes [..., 64], from the documented position of each dimension."""
+def pack(n, offset):
+    """Codes of a token's rows [..., 128] at this offset of its block -> the cache's bytes [..., 64]."""
     words = np.zeros(n.shape[:-1] + (32,), np.uint16)
     u = (n + 8).astype(np.uint16)
     for d in range(128):
         i, q, r = d // 32, d // 8 % 4, d % 8
-        words[..., 4 * r + i if is_v else 8 * (r // 2) + 2 * i + r % 2] |= u[..., d] << (4 * q)
+        words[..., 8 * (i ^ (offset // 2 % 4)) + r] |= u[..., d] << (4 * q)
     return words.view(np.uint8)
 
 

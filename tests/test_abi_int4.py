@@ -27,7 +27,7 @@ def kv(**kw):
     (dict(T=-1), 1), (dict(T=1 << 31), 1), (dict(K=None), 1), (dict(slots=None), 1), (dict(vs=None), 1), (dict(nb=0), 1),
     (dict(Hkv=0), 1), (dict(bs=0), 1), (dict(ldk=1016), 1), (dict(D=64), 2), (dict(nb=1 << 40), 2),
     (dict(nb=1 << 25, bs=16, Hkv=8), 2), (dict(ldv=1028), 3), (dict(V=FAKE + 8), 3), (dict(kc=FAKE + 8), 3),
-    (dict(ks=FAKE + 4), 3), (dict(slots=FAKE + 4), 3), (dict(T=0), 0)])
+    (dict(ks=FAKE + 8), 3), (dict(slots=FAKE + 4), 3), (dict(T=0), 0)])
 def test_append_and_read(so, change, want):
     append, read = kv(**change)
     assert so.bi_kv_int4_append(*append) == want
@@ -40,14 +40,14 @@ def attn(**kw):
     cache = (a["kc"], a["ks"], a["vc"], a["vs"])
     mid = (a["table"], a["mb"], a["nb"], a["lens"], a["B"], a["Hq"], a["Hkv"], a["D"], a["bs"], a["L"])
     return ((a["Q"], *cache, *mid, a["scale"], a["ws"], a["wsb"], a["O"], None),
-            (a["Q"], a["cu"], a["T"], *cache, *mid, a["q"], a["scale"], a["O"], None))
+            (a["Q"], a["cu"], a["T"], *cache, *mid, a["q"], a["scale"], a["ws"], a["wsb"], a["O"], None))
 
 
 @pytest.mark.parametrize("change,want", [
     (dict(B=-1), 1), (dict(B=65536), 1), (dict(L=0), 1), (dict(L=(1 << 30) + 1), 1), (dict(mb=0), 1), (dict(nb=0), 1),
     (dict(scale=f(float("nan"))), 1), (dict(Q=None), 1), (dict(kc=None), 1), (dict(lens=None), 1), (dict(D=64), 2),
     (dict(Hkv=3), 2), (dict(Hq=48, Hkv=4), 2), (dict(Hq=24), 2), (dict(nb=1 << 40), 2), (dict(Q=FAKE + 8), 3),
-    (dict(vc=FAKE + 8), 3), (dict(vs=FAKE + 2), 3), (dict(table=FAKE + 2), 3), (dict(B=0), 0)])
+    (dict(vc=FAKE + 8), 3), (dict(vs=FAKE + 8), 3), (dict(table=FAKE + 2), 3), (dict(B=0), 0)])
 def test_attention(so, change, want):
     decode, extend = attn(**change)
     assert so.bi_attention_decode_int4(*decode) == want
@@ -61,6 +61,12 @@ def test_attention_own_arguments(so):
     assert so.bi_attention_extend_int4(*attn(q=0)[1]) == 1
     assert so.bi_attention_extend_int4(*attn(cu=FAKE + 2)[1]) == 3
     assert so.bi_attention_extend_int4(*attn(T=0)[1]) == 0
+    assert so.bi_attention_extend_int4(*attn(ws=FAKE + 8)[1]) == 3
+    size = so.bi_attention_extend_int4_workspace_size
+    assert size(80, 32, 8, 4000, 5) == so.bi_attention_decode_workspace_size(80, 32, 4000)
+    assert size(4096, 32, 8, 8192, 4096) == 0             # many rows: the tiled kernel
+    assert size(4, 32, 5, 128, 1) == size(4, 8, 32, 128, 1) == size(-1, 32, 8, 128, 1) == size(4, 32, 8, 0, 1) == -1
+    assert size(1 << 60, 32, 8, 1 << 30, 1) == -1
 
 
 @pytest.mark.parametrize("change,want", [

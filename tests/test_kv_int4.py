@@ -63,11 +63,11 @@ def test_append_matches_the_definition_and_touches_nothing_else(bi, T, Hkv, bs):
     scales = [bits_of(want[1]).copy(), bits_of(want[3]).copy()]
     for which, x in enumerate((K, V)):
         n, s = ref.held(x)
-        packed, sb = ref.pack(n, which == 1), syn.to_bf16_bits(np.nan_to_num(s, nan=0.0).astype(np.float32))
+        sb = syn.to_bf16_bits(np.nan_to_num(s, nan=0.0).astype(np.float32))
         sb = np.where(np.isnan(s), np.uint16(0x7FFF), sb)
         for t in range(T):
             if slots[t] >= 0:
-                codes[which][slots[t] // bs, :, slots[t] % bs] = packed[t]
+                codes[which][slots[t] // bs, :, slots[t] % bs] = ref.pack(n[t], int(slots[t] % bs))
                 scales[which][slots[t] // bs, :, slots[t] % bs] = sb[t]
     assert np.array_equal(c.k_codes.cpu().numpy(), codes[0]) and np.array_equal(c.v_codes.cpu().numpy(), codes[1])
     assert np.array_equal(bits_of(c.k_scales), scales[0]) and np.array_equal(bits_of(c.v_scales), scales[1])
@@ -173,7 +173,8 @@ def test_decode_long_and_many(bi):
 
 
 @pytest.mark.parametrize("Hq,Hkv,bs", [(4, 4, 16), (4, 2, 24), (32, 8, 16), (16, 2, 1)])
-@pytest.mark.parametrize("lens,qlens", [([1, 40, 300], [1, 40, 17]), ([129, 513, 128, 20], [1, 200, 128, 0])])
+@pytest.mark.parametrize("lens,qlens", [([1, 40, 300], [1, 40, 17]), ([129, 513, 128, 20], [1, 200, 128, 0]),
+                                        ([700, 5, 131, 4500], [5, 5, 3, 1])])     # few rows: split over the chunks
 def test_extend_is_bf16_extend_and_decode_of_cut_sequences(bi, Hq, Hkv, bs, lens, qlens):
     cu = np.concatenate([[0], np.cumsum(qlens)]).astype(np.int32)
     Q, c, Kh, Vh, table, ld = make(bi, lens, bs, Hq, Hkv, seed=60 + bs, q_rows=int(cu[-1]) + 3)
@@ -182,6 +183,8 @@ def test_extend_is_bf16_extend_and_decode_of_cut_sequences(bi, Hq, Hkv, bs, lens
     args = (table, ld, max(lens), max(qlens), SCALE)
     bi.attention_extend_int4(Q, to_dev(cu), c, *args, O=O)
     same = bi.attention_extend(Q, to_dev(cu), Kh, Vh, *args)
+    tiled = bi.attention_extend_int4(Q, to_dev(cu), c, *args, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert np.array_equal(bits_of(tiled[:cu[-1]]), bits_of(same[:cu[-1]]))
     assert np.array_equal(bits_of(O[:cu[-1]]), bits_of(same[:cu[-1]]))
     assert bool((O[cu[-1]:] == 7.0).all()), "rows behind the last sequence were written"
     for b in range(len(lens)):
@@ -222,9 +225,11 @@ def test_bad_lengths_and_blocks(bi):
         assert (np.abs(O[b].float().cpu().numpy() - want) <= tolerance(want, v)).all()
     cu = torch.arange(5, dtype=torch.int32, device="cuda")
     E = torch.full_like(Q, 7.0)
-    bi.attention_extend_int4(Q, cu, c, bad_tab, bad_len, 300, 1, SCALE, O=E)
-    assert bi.device_status() == bi.BI_ERR_INVALID_ARG
-    assert np.array_equal(bits_of(E), bits_of(O))
+    for ws in (None, torch.empty(16, dtype=torch.uint8, device="cuda")):      # split over the chunks, and tiled
+        E.fill_(7.0)
+        bi.attention_extend_int4(Q, cu, c, bad_tab, bad_len, 300, 1, SCALE, workspace=ws, O=E)
+        assert bi.device_status() == bi.BI_ERR_INVALID_ARG
+        assert np.array_equal(bits_of(E), bits_of(O))
 
 
 def test_non_finite_rows_show(bi):
