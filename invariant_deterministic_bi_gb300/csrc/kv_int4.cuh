@@ -47,7 +47,9 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 // (128 + u, 128 + u') of nibble Q of the word's two halves.
 template <int Q>
 __device__ __forceinline__ uint32_t i4_pair(uint32_t w) {
-    return ((w >> (4 * Q)) & 0x000F000Fu) | 0x43004300u;
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w >> (4 * Q)), "r"(0x000F000Fu), "r"(0x43004300u));
+    return d;
 }
 // The four pairs (u - 8) s of a word of eight codes; s2 the halves' scales,
 // c2 = -136 s2.
