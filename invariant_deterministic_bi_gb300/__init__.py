@@ -16,7 +16,6 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Any, NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # BI_LIBRARY=debug selects the debug build (bounds-checked kernels, same results)
@@ -54,6 +53,8 @@ class Plan(ctypes.Structure):
 def load() -> ctypes.CDLL:
     """Load libbi.so (built by ``__graft_entry__.build()``); raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -422,13 +423,30 @@ def attention_extend(Q, cu_q, K_cache, V_cache, block_table, seq_lens, max_seq_l
     return O
 
 
-class KVInt4Cache(NamedTuple):
+class KVInt4Cache:
     """One layer's paged 4-bit K/V cache (see bi.h): codes uint8 [blocks, Hkv,
-    block_size, 64], scales bfloat16 [blocks, Hkv, block_size, 4]."""
-    k_codes: Any
-    k_scales: Any
-    v_codes: Any
-    v_scales: Any
+    block_size, 64], scales bfloat16 [blocks, Hkv, block_size, 4], for keys and
+    for values; iterating gives the four tensors."""
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "_dims")
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales):
+        import torch
+        rows = None
+        for t, d, w, n in ((k_codes, torch.uint8, 64, "k_codes"), (k_scales, torch.bfloat16, 4, "k_scales"),
+                           (v_codes, torch.uint8, 64, "v_codes"), (v_scales, torch.bfloat16, 4, "v_scales")):
+            _dev(t, d, n)
+            rows = rows or tuple(t.shape[:3])
+            if tuple(t.shape) != rows + (w,) or not t.is_contiguous() or t.device != k_codes.device:
+                raise ValueError(f"{n} must be contiguous [blocks, Hkv, block_size, {w}], the same blocks, heads, block "
+                                 f"size and device for keys and values; got {tuple(t.shape)}")
+            object.__setattr__(self, n, t)
+        object.__setattr__(self, "_dims", rows + (k_codes.get_device(),))   # what the calls need of the checked tensors
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a KVInt4Cache's tensors are fixed; make a new one")
+
+    def __iter__(self):
+        return iter((self.k_codes, self.k_scales, self.v_codes, self.v_scales))
 
 
 def kv_int4_cache(num_blocks: int, block_size: int, Hkv: int, device="cuda") -> KVInt4Cache:
@@ -439,27 +457,22 @@ def kv_int4_cache(num_blocks: int, block_size: int, Hkv: int, device="cuda") -> 
                          for w, d in ((64, torch.uint8), (4, torch.bfloat16)) * 2))
 
 
-def _cache_args(cache):
-    """(num_blocks, Hkv, block_size) of a checked KVInt4Cache."""
-    import torch
-    kc, ks, vc, vs = cache
-    for t, d, n in ((kc, torch.uint8, "k_codes"), (ks, torch.bfloat16, "k_scales"), (vc, torch.uint8, "v_codes"),
-                    (vs, torch.bfloat16, "v_scales")):
-        _dev(t, d, n)
-        if t.dim() != 4 or not t.is_contiguous() or t.shape[:3] != kc.shape[:3]:
-            raise ValueError(f"{n} must be contiguous [blocks, Hkv, block_size, ...], the same for keys and values")
-    if kc.shape[3] != 64 or vc.shape[3] != 64 or ks.shape[3] != 4 or vs.shape[3] != 4:
-        raise ValueError("a cache row holds 64 bytes of codes and 4 scales")
-    return kc.shape[:3]
-
-
-def _one_device(*tensors):
-    """All tensors on the current device (the calls launch there)."""
+def _launch_on(cache, tensors, stream):
+    """(raw stream, cache arguments) for a call on the current device; the tensors and the cache have to be there."""
     import torch
     cur = torch.cuda.current_device()
+    if cache is not None:
+        if not isinstance(cache, KVInt4Cache):
+            raise TypeError("cache must be a KVInt4Cache")
+        if cache._dims[3] != cur:
+            raise ValueError(f"the cache must be on the current device cuda:{cur}, it is on cuda:{cache._dims[3]}")
     for t in tensors:
-        if t is not None and t.device.index != cur:
+        if t is not None and t.get_device() != cur:
             raise ValueError(f"tensors must be on the current device cuda:{cur}, got {t.device}")
+    raw = torch._C._cuda_getCurrentRawStream(cur) if stream is None else stream.cuda_stream
+    if cache is None:
+        return raw, ()
+    return raw, (cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr())
 
 
 def _new(shape, dtype, like, stream):
@@ -471,23 +484,36 @@ def _new(shape, dtype, like, stream):
     return t
 
 
+def _typed(t, dtype, name, contiguous=True):
+    """The tensor, of this type; contiguous if asked for (the device is checked by _launch_on)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
 def _kv_rows(t, T, Hkv, name):
     """Token stride of bf16 rows [T, Hkv, 128] whose heads are contiguous within a token."""
     import torch
-    _dev(t, torch.bfloat16, name)
-    if tuple(t.shape) != (T, Hkv, 128):
+    _typed(t, torch.bfloat16, name, contiguous=False)
+    if t.shape != (T, Hkv, 128):
         raise ValueError(f"{name} must be [T, Hkv, 128] = {(T, Hkv, 128)}, got {tuple(t.shape)}")
-    if t.numel() and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != 128)):
+    st = t.stride()
+    if T and (st[2] != 1 or (Hkv > 1 and st[1] != 128)):
         raise ValueError(f"{name}: the heads of a token must be contiguous (a token stride is allowed)")
-    return t.stride(0) if T > 1 else Hkv * 128
+    return st[0] if T > 1 else Hkv * 128
 
 
 def _slots(slots):
     import torch
-    _dev(slots, torch.int64, "slots")
-    if slots.dim() != 1 or not slots.is_contiguous():
-        raise ValueError("slots must be contiguous [T]")
-    return slots.numel()
+    _typed(slots, torch.int64, "slots")
+    if slots.dim() != 1:
+        raise ValueError("slots must be [T]")
+    return slots.shape[0]
 
 
 def kv_int4_append(K, V, slots, cache: KVInt4Cache, stream=None) -> KVInt4Cache:
@@ -496,47 +522,43 @@ def kv_int4_append(K, V, slots, cache: KVInt4Cache, stream=None) -> KVInt4Cache:
     K, V bf16 [T, Hkv, 128] (a token stride is allowed: slices of a fused
     projection); slots int64 [T]: block * block_size + offset, -1 to skip a
     token. The slots of one call must differ."""
-    nblk, Hkv, bs = _cache_args(cache)
     T = _slots(slots)
+    raw, c = _launch_on(cache, (K, V, slots), stream)
+    nblk, Hkv, bs, _ = cache._dims
     ldk, ldv = _kv_rows(K, T, Hkv, "K"), _kv_rows(V, T, Hkv, "V")
-    _one_device(K, V, slots, *cache)
-    _check(load().bi_kv_int4_append(_ptr(K), ldk, _ptr(V), ldv, T, _ptr(slots), *map(_ptr, cache), nblk, Hkv, 128, bs,
-                                    _stream(stream)), "bi_kv_int4_append")
+    _check(load().bi_kv_int4_append(K.data_ptr(), ldk, V.data_ptr(), ldv, T, slots.data_ptr(), *c, nblk, Hkv, 128, bs, raw),
+           "bi_kv_int4_append")
     return cache
 
 
 def kv_int4_read(cache: KVInt4Cache, slots, K=None, V=None, stream=None):
     """(K, V) bf16 [T, Hkv, 128]: the values held at `slots` (int64 [T]; -1 gives zeros)."""
     import torch
-    nblk, Hkv, bs = _cache_args(cache)
     T = _slots(slots)
-    _one_device(slots, K, V, *cache)
+    raw, c = _launch_on(cache, (slots, K, V), stream)
+    nblk, Hkv, bs, _ = cache._dims
     if K is None:
         K = _new((T, Hkv, 128), torch.bfloat16, slots, stream)
     if V is None:
         V = _new((T, Hkv, 128), torch.bfloat16, slots, stream)
     ldk, ldv = _kv_rows(K, T, Hkv, "K"), _kv_rows(V, T, Hkv, "V")
-    _check(load().bi_kv_int4_read(*map(_ptr, cache), nblk, Hkv, 128, bs, _ptr(slots), T, _ptr(K), ldk, _ptr(V), ldv,
-                                  _stream(stream)), "bi_kv_int4_read")
+    _check(load().bi_kv_int4_read(*c, nblk, Hkv, 128, bs, slots.data_ptr(), T, K.data_ptr(), ldk, V.data_ptr(), ldv, raw),
+           "bi_kv_int4_read")
     return K, V
 
 
-def _attention_int4_args(Q, cache, block_table, seq_lens, O):
-    """Checks shared by the 4-bit attention calls: (nblk, Hkv, block_size)."""
+def _attention_int4_args(Q, block_table, seq_lens, workspace, O):
+    """Checks shared by the 4-bit attention calls: Q's shape."""
     import torch
-    nblk, Hkv, bs = _cache_args(cache)
-    _dev(Q, torch.bfloat16, "Q"), _dev(block_table, torch.int32, "block_table"), _dev(seq_lens, torch.int32, "seq_lens")
-    for t, n in ((Q, "Q"), (block_table, "block_table"), (seq_lens, "seq_lens")):
-        if not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
-    if Q.dim() != 3 or Q.shape[2] != 128 or block_table.dim() != 2 or block_table.shape[0] != seq_lens.numel():
-        raise ValueError(f"shape mismatch Q{tuple(Q.shape)} block_table{tuple(block_table.shape)} "
-                         f"seq_lens{tuple(seq_lens.shape)}")
-    if O is not None:
-        _dev(O, torch.bfloat16, "O")
-        if O.shape != Q.shape or not O.is_contiguous():
-            raise ValueError("O must be contiguous, of Q's shape")
-    return nblk, Hkv, bs
+    _typed(Q, torch.bfloat16, "Q"), _typed(block_table, torch.int32, "block_table"), _typed(seq_lens, torch.int32, "seq_lens")
+    shape, tab = Q.shape, block_table.shape
+    if len(shape) != 3 or shape[2] != 128 or len(tab) != 2 or tab[0] != seq_lens.numel():
+        raise ValueError(f"shape mismatch Q{tuple(shape)} block_table{tuple(tab)} seq_lens{tuple(seq_lens.shape)}")
+    if workspace is not None:
+        _typed(workspace, torch.uint8, "workspace")
+    if O is not None and _typed(O, torch.bfloat16, "O").shape != shape:
+        raise ValueError("O must have Q's shape")
+    return shape
 
 
 def attention_decode_int4(Q, cache: KVInt4Cache, block_table, seq_lens, max_seq_len: int, scale: float,
@@ -547,21 +569,18 @@ def attention_decode_int4(Q, cache: KVInt4Cache, block_table, seq_lens, max_seq_
     The workspace (uint8, ``attention_decode_workspace_size`` bytes) is
     allocated with torch if not given."""
     import torch
-    nblk, Hkv, bs = _attention_int4_args(Q, cache, block_table, seq_lens, O)
-    B, Hq, D = Q.shape
-    if seq_lens.numel() != B:
-        raise ValueError("one query token a sequence: Q must have seq_lens.numel() rows")
-    _one_device(Q, block_table, seq_lens, workspace, O, *cache)
+    B, Hq, D = _attention_int4_args(Q, block_table, seq_lens, workspace, O)
+    raw, c = _launch_on(cache, (Q, block_table, seq_lens, workspace, O), stream)
+    nblk, Hkv, bs, _ = cache._dims
+    if seq_lens.shape != (B,):
+        raise ValueError("one query token a sequence: seq_lens must be [B], B the rows of Q")
     if workspace is None:
         workspace = _new(max(attention_decode_workspace_size(B, Hq, max_seq_len), 16), torch.uint8, Q, stream)
-    _dev(workspace, torch.uint8, "workspace")
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
     if O is None:
-        O = _new(Q.shape, Q.dtype, Q, stream)
-    _check(load().bi_attention_decode_int4(_ptr(Q), *map(_ptr, cache), _ptr(block_table), block_table.shape[1], nblk,
-                                           _ptr(seq_lens), B, Hq, Hkv, D, bs, max_seq_len, float(scale),
-                                           _ptr(workspace), workspace.numel(), _ptr(O), _stream(stream)),
+        O = _new((B, Hq, D), torch.bfloat16, Q, stream)
+    _check(load().bi_attention_decode_int4(Q.data_ptr(), *c, block_table.data_ptr(), block_table.shape[1], nblk,
+                                           seq_lens.data_ptr(), B, Hq, Hkv, D, bs, max_seq_len, scale,
+                                           workspace.data_ptr(), workspace.numel(), O.data_ptr(), raw),
            "bi_attention_decode_int4")
     return O
 
@@ -580,25 +599,22 @@ def attention_extend_int4(Q, cu_q, cache: KVInt4Cache, block_table, seq_lens, ma
     workspace (uint8, ``attention_extend_int4_workspace_size`` bytes) is
     allocated with torch if not given."""
     import torch
-    nblk, Hkv, bs = _attention_int4_args(Q, cache, block_table, seq_lens, O)
-    _dev(cu_q, torch.int32, "cu_q")
-    B = seq_lens.numel()
-    if cu_q.numel() != B + 1 or not cu_q.is_contiguous():
-        raise ValueError("cu_q must be contiguous [B + 1]")
-    _one_device(Q, cu_q, block_table, seq_lens, workspace, O, *cache)
-    T, Hq, D = Q.shape
+    T, Hq, D = _attention_int4_args(Q, block_table, seq_lens, workspace, O)
+    B = _typed(cu_q, torch.int32, "cu_q").numel() - 1
+    raw, c = _launch_on(cache, (Q, cu_q, block_table, seq_lens, workspace, O), stream)
+    nblk, Hkv, bs, _ = cache._dims
+    if seq_lens.shape != (B,):
+        raise ValueError("cu_q must have one entry more than seq_lens")
     if workspace is None:
-        workspace = _new(max(attention_extend_int4_workspace_size(T, Hq, Hkv, max_seq_len, max_q_len), 16), torch.uint8, Q,
-                         stream)
-    _dev(workspace, torch.uint8, "workspace")
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
+        need = attention_extend_int4_workspace_size(T, Hq, Hkv, max_seq_len, max_q_len)
+        workspace = _new(need, torch.uint8, Q, stream) if need > 0 else None
     if O is None:
-        O = _new(Q.shape, Q.dtype, Q, stream)
-    _check(load().bi_attention_extend_int4(_ptr(Q), _ptr(cu_q), T, *map(_ptr, cache), _ptr(block_table),
-                                           block_table.shape[1], nblk, _ptr(seq_lens), B, Hq, Hkv, D, bs, max_seq_len,
-                                           max_q_len, float(scale), _ptr(workspace), workspace.numel(), _ptr(O),
-                                           _stream(stream)), "bi_attention_extend_int4")
+        O = _new((T, Hq, D), torch.bfloat16, Q, stream)
+    _check(load().bi_attention_extend_int4(Q.data_ptr(), cu_q.data_ptr(), T, *c, block_table.data_ptr(),
+                                           block_table.shape[1], nblk, seq_lens.data_ptr(), B, Hq, Hkv, D, bs, max_seq_len,
+                                           max_q_len, scale, workspace.data_ptr() if workspace is not None else None,
+                                           workspace.numel() if workspace is not None else 0, O.data_ptr(), raw),
+           "bi_attention_extend_int4")
     return O
 
 
@@ -609,28 +625,25 @@ def gemm_int4(X, W, scales, zeros=None, Y=None, stream=None):
     byte, low nibble for even k; scales bf16 [N, K/g]; zeros uint8 [N, K/g] or
     None (8 throughout). A weight is (code - zero) * scale."""
     import torch
-    _dev(X, torch.bfloat16, "X"), _dev(W, torch.uint8, "W"), _dev(scales, torch.bfloat16, "scales")
-    if X.dim() != 2 or W.dim() != 2 or scales.dim() != 2 or X.shape[1] != 2 * W.shape[1] or scales.shape[0] != W.shape[0]:
-        raise ValueError(f"shape mismatch X{tuple(X.shape)} W{tuple(W.shape)} scales{tuple(scales.shape)}")
-    M, K = X.shape
-    N, groups = scales.shape
-    if X.stride(1) != 1 or not W.is_contiguous() or not scales.is_contiguous():
-        raise ValueError("X needs unit column stride; W and scales must be contiguous")
+    _typed(X, torch.bfloat16, "X", contiguous=False), _typed(W, torch.uint8, "W"), _typed(scales, torch.bfloat16, "scales")
+    xs, ws, ss = X.shape, W.shape, scales.shape
+    if len(xs) != 2 or len(ws) != 2 or len(ss) != 2 or xs[1] != 2 * ws[1] or ss[0] != ws[0]:
+        raise ValueError(f"shape mismatch X{tuple(xs)} W{tuple(ws)} scales{tuple(ss)}")
+    (M, K), (N, groups) = xs, ss
+    if X.stride(1) != 1:
+        raise ValueError("X needs unit column stride")
     if groups < 1 or K % groups:
         raise ValueError("scales must divide K into groups")
-    if zeros is not None:
-        _dev(zeros, torch.uint8, "zeros")
-        if zeros.shape != scales.shape or not zeros.is_contiguous():
-            raise ValueError("zeros must be contiguous, of scales' shape")
-    _one_device(X, W, scales, zeros, Y)
+    if zeros is not None and _typed(zeros, torch.uint8, "zeros").shape != ss:
+        raise ValueError("zeros must have scales' shape")
+    raw, _ = _launch_on(None, (X, W, scales, zeros, Y), stream)
     if Y is None:
         Y = _new((M, N), torch.bfloat16, X, stream)
-    _dev(Y, torch.bfloat16, "Y")
-    if Y.shape != (M, N) or Y.stride(1) != 1:
+    elif _typed(Y, torch.bfloat16, "Y", contiguous=False).shape != (M, N) or Y.stride(1) != 1:
         raise ValueError("Y must be [M, N] with unit column stride")
-    _check(load().bi_gemm_int4(_ptr(X), X.stride(0) if M > 1 else K, _ptr(W), _ptr(scales),
-                               _ptr(zeros) if zeros is not None else None, _ptr(Y), Y.stride(0) if M > 1 else N, M, N, K,
-                               K // groups, _stream(stream)), "bi_gemm_int4")
+    _check(load().bi_gemm_int4(X.data_ptr(), X.stride(0) if M > 1 else K, W.data_ptr(), scales.data_ptr(),
+                               zeros.data_ptr() if zeros is not None else None, Y.data_ptr(), Y.stride(0) if M > 1 else N,
+                               M, N, K, K // groups, raw), "bi_gemm_int4")
     return Y
 
 

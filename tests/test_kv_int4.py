@@ -264,9 +264,13 @@ def test_refusals():
     with pytest.raises(ValueError):
         bi.kv_int4_append(K.transpose(0, 1).contiguous().transpose(0, 1), K, s, c)     # heads apart
     with pytest.raises(ValueError):
-        bi.kv_int4_append(K, K, s, bi.KVInt4Cache(c.k_codes[..., :32].contiguous(), *c[1:]))
-    with pytest.raises(TypeError):
+        bi.KVInt4Cache(c.k_codes[..., :32].contiguous(), c.k_scales, c.v_codes, c.v_scales)
+    with pytest.raises((TypeError, ValueError)):
         bi.kv_int4_append(K.cpu(), K, s, c)
+    with pytest.raises(TypeError):
+        bi.kv_int4_append(K, K, s, tuple(c))
+    with pytest.raises(AttributeError):
+        c.k_codes = c.v_codes
     base = torch.zeros(3 * 2 * D + 4, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(bi.BiError) as e:
         bi.kv_int4_append(base[4:].view(3, 2, D), K, s, c)                           # 8-byte aligned rows
