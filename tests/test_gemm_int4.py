@@ -56,6 +56,17 @@ def test_rows_do_not_depend_on_the_batch(bi, K, g):
     assert np.array_equal(bits_of(run(bi, X[perm], W, S, Z)), full[perm])
 
 
+@pytest.mark.parametrize("M,N,K,g", [(2500, 2048, 1024, 128), (1290, 4104, 1056, 32)])
+def test_many_tiles(bi, M, N, K, g):
+    """More tiles than the GPU holds at once: the same bits as the rows alone, and parity on some of them."""
+    a = X, W, S, Z = inputs(M, N, K, g, True, seed=11)
+    full = run(bi, *a)
+    for rows in (slice(0, 1), slice(M - 5, M), slice(60, 76), slice(100, 140)):
+        part = run(bi, X[rows], W, S, Z)
+        assert np.array_equal(bits_of(part), bits_of(full[rows])), rows
+    check(full[-5:], X[-5:], W, S, Z)
+
+
 def test_strided_rows(bi):
     """X and Y as column slices of wider buffers: nothing outside Y's slice is written."""
     import torch
