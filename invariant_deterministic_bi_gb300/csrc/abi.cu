@@ -474,7 +474,7 @@ bi_status bi_gemm_int4(const void *X, int64_t ldx, const uint8_t *W, const void 
     if (!X || !W || !scales || !Y || ldx < K || ldy < N) return BI_ERR_INVALID_ARG;
     if (!(group == 32 || group == 64 || group % 128 == 0) || K % group != 0 || N % 8 != 0) return BI_ERR_UNSUPPORTED;
     if (ldx % 8 != 0 || ldy % 8 != 0 || !aligned16(X) || !aligned16(W) || !aligned16(Y) ||
-        (reinterpret_cast<uintptr_t>(scales) & 1u))
+        !aligned16(scales) || !aligned16(zeros))
         return BI_ERR_MISALIGNED;
     const bi_status st = require_device();
     if (st != BI_OK) return st;

@@ -17,11 +17,11 @@
 // blocks into S segments; a segment's groups are added in ascending order, and
 // the segments' sums in order. The number of rows decides only who computes
 // what:
-//   - few rows (gemm_int4_rows_kernel, M <= 16): a warp a segment, the CTA's
+//   - few rows (gemm_int4_rows_kernel, M <= 8): a warp a segment, the CTA's
 //     warps share 16 or 32 weight rows; every warp has its own ring of TMA
 //     copies and nobody waits for anybody before the final sum;
-//   - more (gemm_int4_tile_kernel): a CTA a tile of 128 weight rows x 64 rows of
-//     X, both staged by TMA for all warps; it walks the segments, or, where the
+//   - more (gemm_int4_tile_kernel): a CTA a tile of 128 weight rows x 16, 32 or 64
+//     rows of X, both staged by TMA for all warps; it walks the segments, or, where the
 //     tiles would not fill the GPU, the CTAs of a cluster take one each.
 #include "attn_common.cuh"
 #include "bi_internal.h"
@@ -35,23 +35,68 @@ constexpr int kBlockK = 128;                   // k of a staged block
 constexpr int kMaxSegments = 8;
 
 struct GemmI4Params {
-    const uint16_t *S;       // [N][groups] bf16
-    const uint8_t *Z;        // [N][groups] or null
+    const uint32_t *S;       // [N][groups] bf16, as words
+    const uint32_t *Z;       // [N][groups] bytes, as words, or null
     uint16_t *Y;             // [M][ldy]
-    int64_t ldy, M, N, K, group, groups, blocks;
-    int32_t segments;
+    int64_t ldy, M, N, K, groups;
+    int32_t group, blocks, segments;
     unsigned *status;
 };
 
-// (scale as fp32, -(128 + z) as a bf16 pair) of weight row n's group at k.
-__device__ __forceinline__ uint2 load_scale(const GemmI4Params &p, int64_t n, int64_t k) {
-    uint2 v = make_uint2(0u, 0xC308C308u);
-    if (n < p.N && k < p.K) {
-        const int64_t gi = n * p.groups + k / p.group;
-        v.x = static_cast<uint32_t>(p.S[gi]) << 16;
-        if (p.Z) v.y = 0xC300C300u | ((p.Z[gi] & 15u) * 0x00010001u);
+// The scales and zeros of a staged block, GS k a scale: for each weight row the
+// 32-bit words that hold them (their place in the first word depends on the row).
+template <int GS>
+struct ScaleTile {
+    static constexpr int kSub = kBlockK / GS;                     // groups of a block
+    static constexpr int kSWords = (kSub + 1) / 2 + (kSub > 1);   // words of kSub 16-bit scales at any halfword
+    static constexpr int kZWords = kSub > 1 ? 2 : 1;              // words of kSub bytes at any byte
+    static constexpr int bytes(int rows) { return rows * (kSWords + kZWords) * 4; }
+};
+
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// First group of a block.
+template <int GS>
+__device__ __forceinline__ int first_group(const GemmI4Params &p, int blk) {
+    return GS < kBlockK ? blk * (kBlockK / GS) : static_cast<int>(static_cast<unsigned>(blk) / static_cast<unsigned>(p.group / kBlockK));
+}
+
+// Starts the copies of a block's scales and zeros for `rows` weight rows from n0 by
+// `threads` threads, each of which arrives on the barrier once its copies have
+// landed. Words past the arrays (rows past N, groups past K) repeat the last one.
+template <int GS>
+__device__ __forceinline__ void stage_scales(const GemmI4Params &p, uint32_t dst, uint64_t *bar, int64_t n0, int rows, int blk,
+                                             int thread, int threads) {
+    using T = ScaleTile<GS>;
+    const int64_t e0 = n0 * p.groups + first_group<GS>(p, blk), total = p.N * p.groups;
+    for (int v = thread; v < rows * T::kSWords; v += threads) {
+        const int r = v / T::kSWords, w = v % T::kSWords;
+        const int64_t word = (e0 + r * p.groups) / 2 + w;
+        cp_async_4(dst + v * 4, p.S + (word < total / 2 ? word : total / 2 - 1));
     }
-    return v;
+    if (p.Z) {
+        for (int v = thread; v < rows * T::kZWords; v += threads) {
+            const int r = v / T::kZWords, w = v % T::kZWords;
+            const int64_t word = (e0 + r * p.groups) / 4 + w;
+            cp_async_4(dst + (rows * T::kSWords + v) * 4, p.Z + (word < total / 4 ? word : total / 4 - 1));
+        }
+    }
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// (scale as fp32, -(128 + z) as a bf16 pair) of a staged row (of `rows`, the tile's first one n0) and group.
+template <int GS>
+__device__ __forceinline__ void read_scale(const GemmI4Params &p, const uint8_t *tile, int64_t n0, int rows, int row, int blk,
+                                           int sub, float &s, uint32_t &z2) {
+    using T = ScaleTile<GS>;
+    const uint32_t e = static_cast<uint32_t>(n0 + row) * static_cast<uint32_t>(p.groups) + first_group<GS>(p, blk);   // modulo 4 is exact
+    const bool in = GS == kBlockK || blk * kBlockK + sub * GS < p.K;
+    const uint32_t bits = *reinterpret_cast<const uint16_t *>(tile + row * T::kSWords * 4 + (e & 1) * 2 + sub * 2);
+    s = in ? __uint_as_float(bits << 16) : 0.0f;
+    z2 = 0xC308C308u;
+    if (p.Z) z2 = 0xC300C300u | ((tile[(rows * T::kSWords + row * T::kZWords) * 4 + (e & 3) + sub] & 15u) * 0x00010001u);
 }
 
 // Where lane (g, c) finds its operands of a block, GS k a scale: word j of group
@@ -83,24 +128,27 @@ __device__ __forceinline__ void expand_weights(uint32_t w, uint32_t z2, uint32_t
     a[3] = fma_bf16x2(i4_pair<3>(w), 0x3F803F80u, z2);
 }
 
-// acc += the block's groups, each scaled, for 16 MR weight rows x 8 NT rows of X.
-// `sc`: [16 MR][groups of the block] scales.
+// acc += the block's groups, each scaled, for weight rows row0 .. row0 + 16 MR - 1
+// of the staged `rows` and 8 NT rows of X from x_row0 of the staged x_rows.
 template <int GS, int MR, int NT>
-__device__ __forceinline__ void block_product(uint32_t w_tile, uint32_t x_tile, int x_rows, int x_row0, const uint2 *sc,
-                                              int gq, int cq, float (&acc)[MR][NT][4]) {
+__device__ __forceinline__ void block_product(const GemmI4Params &p, const uint8_t *w_tile, const uint8_t *x_tile,
+                                              const uint8_t *sc, int64_t n0, int rows, int row0, int blk, int x_rows,
+                                              int x_row0, int gq, int cq, float (&acc)[MR][NT][4]) {
+    const uint32_t w_at = smem_u32(w_tile), x_at = smem_u32(x_tile);
     constexpr int kSub = kBlockK / GS;
 #pragma unroll
     for (int sub = 0; sub < kSub; ++sub) {
         uint32_t w[MR][2][GS / 32];
-        uint2 s[MR][2];
+        float s[MR][2];
+        uint32_t z2[MR][2];
         float part[MR][NT][4];
 #pragma unroll
         for (int m = 0; m < MR; ++m) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int row = 16 * m + 8 * h + gq;
-                load_words<GS>(w_tile + row * (kBlockK / 2), row, sub, cq, w[m][h]);
-                s[m][h] = sc[row * kSub + sub];
+                const int row = row0 + 16 * m + 8 * h + gq;
+                load_words<GS>(w_at + row * (kBlockK / 2), row, sub, cq, w[m][h]);
+                read_scale<GS>(p, sc, n0, rows, row, blk, sub, s[m][h], z2[m][h]);
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -113,11 +161,11 @@ __device__ __forceinline__ void block_product(uint32_t w_tile, uint32_t x_tile, 
 #pragma unroll
             for (int m = 0; m < MR; ++m)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) expand_weights(w[m][h][j], s[m][h].y, a[m][h]);
+                for (int h = 0; h < 2; ++h) expand_weights(w[m][h][j], z2[m][h], a[m][h]);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 uint32_t b[4];
-                load_x<GS>(x_tile, x_rows, x_row0 + 8 * t + gq, sub, cq, j, b);
+                load_x<GS>(x_at, x_rows, x_row0 + 8 * t + gq, sub, cq, j, b);
 #pragma unroll
                 for (int m = 0; m < MR; ++m)
                     mma_16816(part[m][t], a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], b[0], b[1]);
@@ -132,7 +180,7 @@ __device__ __forceinline__ void block_product(uint32_t w_tile, uint32_t x_tile, 
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    acc[m][t][e] = __fmaf_rn(__uint_as_float(s[m][e >> 1].x), part[m][t][e], acc[m][t][e]);
+                    acc[m][t][e] = __fmaf_rn(s[m][e >> 1], part[m][t][e], acc[m][t][e]);
     }
 }
 
@@ -143,26 +191,35 @@ __device__ __forceinline__ void store_y(const GemmI4Params &p, int64_t m, int64_
 
 // ---------------------------------------------------------------- few rows ---
 
-constexpr int kRing = 3;                       // blocks of a warp in shared memory
+// blocks of a warp in shared memory, such that two CTAs fit an SM
+template <int MR>
+constexpr int rows_ring() { return MR == 1 ? 3 : 2; }
 template <int MR, int NT>
 constexpr int rows_stage() { return MR * 16 * (kBlockK / 2) + NT * 8 * kBlockK * 2; }   // W, X
+template <int MR, int NT>
+constexpr int rows_sums() { return 16 * MR * (8 * NT + 1); }   // floats of a warp's sums
 template <int GS, int MR, int NT>
-constexpr int rows_warp() { return kRing * rows_stage<MR, NT>() + 2 * 16 * MR * (kBlockK / GS) * 8; }
+constexpr int rows_warp() {
+    return rows_ring<MR>() * (rows_stage<MR, NT>() + ScaleTile<GS>::bytes(16 * MR)) + 2 * rows_sums<MR, NT>() * 4;
+}
 
+// CTAs walk the tiles of 16 MR weight rows; a warp's ring runs on from one tile to the next.
 template <int GS, int MR, int NT>
 __global__ void __launch_bounds__(32 * kMaxSegments)
 gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmI4Params p) {
-    constexpr int kSub = kBlockK / GS, kStage = rows_stage<MR, NT>(), kWBytes = MR * 16 * (kBlockK / 2);
-    constexpr int kScales = 16 * MR * kSub, kPer = (kScales + 31) / 32;
+    constexpr int kRing = rows_ring<MR>(), kStage = rows_stage<MR, NT>(), kScaleBytes = ScaleTile<GS>::bytes(16 * MR);
+    constexpr int kWBytes = MR * 16 * (kBlockK / 2), kXBytes = NT * 8 * kBlockK * 2;
+    constexpr int kSums = rows_sums<MR, NT>(), kCols = 8 * NT + 1;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ uint64_t full[kMaxSegments][kRing];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, cq = lane & 3;
     uint8_t *ring = smem + warp * kRing * kStage;
-    uint2 *scales = reinterpret_cast<uint2 *>(smem + p.segments * kRing * kStage) + warp * 2 * kScales;
+    uint8_t *scales = smem + p.segments * kRing * kStage + warp * kRing * kScaleBytes;
+    float *sums = reinterpret_cast<float *>(smem + p.segments * kRing * (kStage + kScaleBytes));   // [2][segments][kSums]
     if (lane == 0) {
-        for (int k = 0; k < kRing; ++k) mbar_init(&full[warp][k], 1);
+        for (int k = 0; k < kRing; ++k) mbar_init(&full[warp][k], 33);   // 32 lanes' scale copies, and the TMA's bytes
         fence_mbar_init();
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmX);
@@ -170,102 +227,102 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     __syncwarp();
     grid_dep_wait();      // earlier work of the stream is complete and visible
     grid_dep_launch();
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * MR);
-    const int b0 = static_cast<int>(warp * p.blocks / p.segments), b1 = static_cast<int>((warp + 1) * p.blocks / p.segments);
-    auto issue = [&](int blk) {                            // one lane
-        const int slot = (blk - b0) % kRing;
-        uint8_t *dst = ring + slot * kStage;
-        uint64_t *bar = &full[warp][slot];
-        mbar_arrive_expect_tx(bar, kStage);
-        tma_load_2d(dst, &tmW, bar, blk * (kBlockK / 2), static_cast<int32_t>(n0));
-        tma_load_2d(dst + kWBytes, &tmX, bar, blk * kBlockK, 0);
-        tma_load_2d(dst + kWBytes + NT * 8 * 128, &tmX, bar, blk * kBlockK + 64, 0);
-    };
-    uint2 sv[kPer];
-    auto fetch_scales = [&](int blk) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int v = lane + 32 * i;
-            sv[i] = v < kScales ? load_scale(p, n0 + v / kSub, static_cast<int64_t>(blk) * kBlockK + v % kSub * GS) : make_uint2(0u, 0u);
+    const int tiles = static_cast<int>((p.N + 16 * MR - 1) / (16 * MR));
+    const int b0 = static_cast<int>(static_cast<int64_t>(warp) * p.blocks / p.segments);
+    const int b1 = static_cast<int>(static_cast<int64_t>(warp + 1) * p.blocks / p.segments);
+    // the next block to be copied, and its slot
+    int ft = blockIdx.x, fb = b0, fs = 0;
+    auto fill = [&]() {
+        if (ft >= tiles) return;
+        uint8_t *dst = ring + fs * kStage;
+        uint64_t *bar = &full[warp][fs];
+        const int64_t n0 = static_cast<int64_t>(ft) * (16 * MR);
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar, kWBytes + kXBytes);
+            tma_load_2d(dst, &tmW, bar, fb * (kBlockK / 2), static_cast<int32_t>(n0));
+            tma_load_2d(dst + kWBytes, &tmX, bar, fb * kBlockK, 0);
+            tma_load_2d(dst + kWBytes + kXBytes / 2, &tmX, bar, fb * kBlockK + 64, 0);
         }
+        stage_scales<GS>(p, smem_u32(scales + fs * kScaleBytes), bar, n0, 16 * MR, fb, lane, 32);
+        if (++fs == kRing) fs = 0;
+        if (++fb == b1) fb = b0, ft += gridDim.x;
     };
-    if (lane == 0)
-        for (int blk = b0; blk < b1 && blk < b0 + kRing; ++blk) issue(blk);
-    float acc[MR][NT][4];
-#pragma unroll
-    for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[m][t][e] = 0.0f;
-    fetch_scales(b0);
+    for (int k = 0; k < kRing; ++k) fill();
+    int slot = 0, buf = 0;
+    uint32_t parity = 0;
     bool ok = true;
-    for (int blk = b0; blk < b1; ++blk) {
-        const int i = blk - b0, slot = i % kRing;
-        uint2 *sc = scales + (i & 1) * kScales;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+        const int64_t n0 = static_cast<int64_t>(tile) * (16 * MR);
+        float acc[MR][NT][4];
 #pragma unroll
-        for (int k = 0; k < kPer; ++k)
-            if (lane + 32 * k < kScales) sc[lane + 32 * k] = sv[k];
-        if (blk + 1 < b1) fetch_scales(blk + 1);
-        ok = mbar_wait(&full[warp][slot], (i / kRing) & 1, nullptr);
-        __syncwarp();
-        if (!__all_sync(0xffffffffu, ok)) {                // ran out: report; the copies in flight get another limit
-            if (lane == 0) {
-                atomicOr(p.status, kDevTimeout);
-                for (int k = 0; k < kRing && blk + k < b1; ++k) mbar_wait(&full[warp][(i + k) % kRing], ((i + k) / kRing) & 1, nullptr);
-            }
-            break;
+        for (int m = 0; m < MR; ++m)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[m][t][e] = 0.0f;
+        for (int blk = b0; blk < b1 && ok; ++blk) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][slot], parity, nullptr));
+            __syncwarp();
+            if (!ok) break;
+            const uint8_t *st = ring + slot * kStage;
+            block_product<GS, MR, NT>(p, st, st + kWBytes, scales + slot * kScaleBytes, n0, 16 * MR, 0, blk, 8 * NT, 0, gq, cq, acc);
+            __syncwarp();                                  // every lane has read the slot
+            fill();
+            if (++slot == kRing) slot = 0, parity ^= 1;
         }
-        const uint32_t w_tile = smem_u32(ring + slot * kStage);
-        block_product<GS, MR, NT>(w_tile, w_tile + kWBytes, 8 * NT, 0, sc, gq, cq, acc);
-        __syncwarp();                                      // every lane has read the slot
-        if (lane == 0 && blk + kRing < b1) issue(blk + kRing);
+        // the segments' sums, added in order
+        float *mine = sums + (buf * p.segments + warp) * kSums;
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mine[(16 * m + gq + 8 * (e >> 1)) * kCols + 8 * t + 2 * cq + (e & 1)] = acc[m][t][e];
+        if (__syncthreads_or(!ok)) break;                  // (two buffers: the one before last has been read)
+        for (int i = threadIdx.x; i < 16 * MR * 8 * NT; i += blockDim.x) {
+            const int r = i % (16 * MR), t = i / (16 * MR);
+            if (t >= p.M) break;
+            const float *v = sums + buf * p.segments * kSums + r * kCols + t;
+            float y = v[0];
+            for (int s = 1; s < p.segments; ++s) y += v[s * kSums];
+            store_y(p, t, n0 + r, y);
+        }
     }
-    // the segments' sums, added in order (the rings are done with: each warp's sums lie in its own)
-    constexpr int kCols = 8 * NT + 1;
-    float *red = reinterpret_cast<float *>(ring);
-    static_assert(16 * MR * kCols * 4 <= kRing * kStage, "the sums fit the ring");
-    __syncwarp();
-#pragma unroll
-    for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) red[(16 * m + gq + 8 * (e >> 1)) * kCols + 8 * t + 2 * cq + (e & 1)] = acc[m][t][e];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * MR * 8 * NT; i += blockDim.x) {
-        const int r = i % (16 * MR), t = i / (16 * MR);
-        if (t >= p.M) break;
-        const float *v = reinterpret_cast<const float *>(smem) + r * kCols + t;
-        float y = v[0];
-        for (int s = 1; s < p.segments; ++s) y += v[s * (kRing * kStage / 4)];
-        store_y(p, t, n0 + r, y);
+    if (!ok && lane == 0) {                                // a wait ran out: report; the copies in flight get another limit
+        atomicOr(p.status, kDevTimeout);
+        for (int k = 0; k < kRing; ++k) {
+            mbar_wait(&full[warp][slot], parity, nullptr);
+            if (++slot == kRing) slot = 0, parity ^= 1;
+        }
     }
 }
 
 // -------------------------------------------------------------------- tiles ---
 
-constexpr int kTileN = 128, kTileM = 64;       // weight rows, rows of X of a CTA
-constexpr int kTileThreads = 256;              // warps: four of 32 weight rows x two of 32 rows of X
-constexpr int kTileStages = 3;
-constexpr int kTileW = kTileN * (kBlockK / 2), kTileStage = kTileW + kTileM * kBlockK * 2;   // 24 KB
-template <int GS>
-constexpr int tile_smem() { return 1024 + kTileStages * kTileStage + 2 * kTileN * (kBlockK / GS) * 8; }
-static_assert(kTileN * kTileM * 4 <= kTileStages * kTileStage, "a segment's sums fit the stages");
+constexpr int kTileN = 128;                    // weight rows of a CTA
+constexpr int kTileThreads = 256;              // warps: 8 / WM of 16 WM weight rows x WM of TM / WM rows of X
+constexpr int kTileW = kTileN * (kBlockK / 2); // 8 KB a stage
+template <int TM>
+constexpr int tile_stage() { return kTileW + TM * kBlockK * 2; }
+template <int TM>
+constexpr int tile_stages() { return TM == 64 ? 3 : 5; }
+template <int GS, int TM>
+constexpr int tile_smem() { return 1024 + tile_stages<TM>() * (tile_stage<TM>() + ScaleTile<GS>::bytes(kTileN)); }
 
 // One segment a CTA (a cluster's ranks in segment order), or all segments in turn (SPLIT false).
-template <int GS, bool SPLIT>
-__global__ void __launch_bounds__(kTileThreads, SPLIT ? 2 : 1)
+template <int GS, int TM, bool SPLIT>
+__global__ void __launch_bounds__(kTileThreads, TM == 64 && !SPLIT ? 1 : 2)
 gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmI4Params p) {
-    constexpr int kSub = kBlockK / GS, kScales = kTileN * kSub, kPer = (kScales + kTileThreads - 1) / kTileThreads;
+    constexpr int kScaleBytes = ScaleTile<GS>::bytes(kTileN), kTileStage = tile_stage<TM>(), kTileStages = tile_stages<TM>();
+    constexpr int kTileM = TM, WM = TM == 16 ? 1 : 2, MR = WM, NT = TM / 8 / WM;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint2 *scales = reinterpret_cast<uint2 *>(smem + kTileStages * kTileStage);
+    uint8_t *scales = smem + kTileStages * kTileStage;
     __shared__ uint64_t full[kTileStages];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int gq = lane >> 2, cq = lane & 3, wn = warp & 3, wm = warp >> 2;
+    const int gq = lane >> 2, cq = lane & 3, wn = warp % (8 / WM), wm = warp / (8 / WM);
     if (tid == 0) {
-        for (int k = 0; k < kTileStages; ++k) mbar_init(&full[k], 1);
+        for (int k = 0; k < kTileStages; ++k) mbar_init(&full[k], kTileThreads + 1);   // scale copies, the TMA's bytes
         fence_mbar_init();
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmX);
@@ -278,49 +335,37 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     const int64_t tile = SPLIT ? blockIdx.x / p.segments : blockIdx.x;
     const int64_t tiles_m = (p.M + kTileM - 1) / kTileM;
     const int64_t m0 = tile % tiles_m * kTileM, n0 = tile / tiles_m * kTileN;
-    const int first = SPLIT ? static_cast<int>(rank * p.blocks / p.segments) : 0;
-    const int last = SPLIT ? static_cast<int>((rank + 1) * p.blocks / p.segments) : static_cast<int>(p.blocks);
-    auto issue = [&](int blk) {                            // thread 0
+    const int first = SPLIT ? static_cast<int>(static_cast<int64_t>(rank) * p.blocks / p.segments) : 0;
+    const int last = SPLIT ? static_cast<int>(static_cast<int64_t>(rank + 1) * p.blocks / p.segments) : p.blocks;
+    auto fill = [&](int blk) {
         const int slot = (blk - first) % kTileStages;
         uint8_t *dst = smem + slot * kTileStage;
-        mbar_arrive_expect_tx(&full[slot], kTileStage);
-        tma_load_2d(dst, &tmW, &full[slot], blk * (kBlockK / 2), static_cast<int32_t>(n0));
-        tma_load_2d(dst + kTileW, &tmX, &full[slot], blk * kBlockK, static_cast<int32_t>(m0));
-        tma_load_2d(dst + kTileW + kTileM * 128, &tmX, &full[slot], blk * kBlockK + 64, static_cast<int32_t>(m0));
-    };
-    uint2 sv[kPer];
-    auto fetch_scales = [&](int blk) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int v = tid + kTileThreads * i;
-            sv[i] = v < kScales ? load_scale(p, n0 + v / kSub, static_cast<int64_t>(blk) * kBlockK + v % kSub * GS) : make_uint2(0u, 0u);
+        if (tid == 0) {
+            mbar_arrive_expect_tx(&full[slot], kTileStage);
+            tma_load_2d(dst, &tmW, &full[slot], blk * (kBlockK / 2), static_cast<int32_t>(n0));
+            tma_load_2d(dst + kTileW, &tmX, &full[slot], blk * kBlockK, static_cast<int32_t>(m0));
+            tma_load_2d(dst + kTileW + kTileM * 128, &tmX, &full[slot], blk * kBlockK + 64, static_cast<int32_t>(m0));
         }
+        stage_scales<GS>(p, smem_u32(scales + slot * kScaleBytes), &full[slot], n0, kTileN, blk, tid, kTileThreads);
     };
-    if (tid == 0)
-        for (int blk = first; blk < last && blk < first + kTileStages - 1; ++blk) issue(blk);
-    float acc[2][4][4], tot[2][4][4];
-    auto clear = [&](float (&v)[2][4][4]) {
+    for (int blk = first; blk < last && blk < first + kTileStages - 1; ++blk) fill(blk);
+    float acc[MR][NT][4], tot[MR][NT][4];
+    auto clear = [&](float (&v)[MR][NT][4]) {
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < MR; ++m)
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[m][t][e] = 0.0f;
     };
     clear(acc);
-    fetch_scales(first);
     int seg = 0;                                           // SPLIT false: the segment at work, and its end
-    int seg_end = static_cast<int>(p.blocks / p.segments);
+    int seg_end = p.blocks / p.segments;
     bool ok = true;
     for (int blk = first; blk < last; ++blk) {
         const int i = blk - first, slot = i % kTileStages;
-        uint2 *sc = scales + (i & 1) * kScales;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k)
-            if (tid + kTileThreads * k < kScales) sc[tid + kTileThreads * k] = sv[k];
-        if (blk + 1 < last) fetch_scales(blk + 1);
         ok = mbar_wait(&full[slot], (i / kTileStages) & 1, nullptr);
-        if (__syncthreads_or(!ok)) {                       // (and: the scales are written, block i - 1 is done with)
+        if (__syncthreads_or(!ok)) {                       // (and: block i - 1 is done with)
             if (tid == 0) {                                // ran out: report; the copies in flight get another limit
                 atomicOr(p.status, kDevTimeout);
                 for (int k = 0; k < kTileStages - 1 && blk + k < last; ++k)
@@ -328,19 +373,20 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
             }
             break;
         }
-        if (tid == 0 && blk + kTileStages - 1 < last) issue(blk + kTileStages - 1);
-        const uint32_t w_tile = smem_u32(smem + slot * kTileStage);
-        block_product<GS, 2, 4>(w_tile + wn * 32 * (kBlockK / 2), w_tile + kTileW, kTileM, 32 * wm, sc + wn * 32 * kSub, gq, cq, acc);
+        if (blk + kTileStages - 1 < last) fill(blk + kTileStages - 1);
+        const uint8_t *st = smem + slot * kTileStage;
+        block_product<GS, MR, NT>(p, st, st + kTileW, scales + slot * kScaleBytes, n0, kTileN, 16 * MR * wn, blk, kTileM, 8 * NT * wm, gq, cq,
+                                  acc);
         if (!SPLIT && blk + 1 == seg_end) {
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < MR; ++m)
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) tot[m][t][e] = seg == 0 ? acc[m][t][e] : tot[m][t][e] + acc[m][t][e];
             clear(acc);
             ++seg;
-            seg_end = static_cast<int>((seg + 1) * p.blocks / p.segments);
+            seg_end = static_cast<int>(static_cast<int64_t>(seg + 1) * p.blocks / p.segments);
         }
     }
     // the tile's sums through shared memory, [row of X][weight row] with the rows four apart in banks
@@ -349,12 +395,12 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     float *red = reinterpret_cast<float *>(smem);
     __syncthreads();
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < MR; ++m)
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                red[(32 * wm + 8 * t + 2 * cq + (e & 1)) * kLd + 32 * wn + 16 * m + gq + 8 * (e >> 1)] =
+                red[(8 * NT * wm + 8 * t + 2 * cq + (e & 1)) * kLd + 16 * MR * wn + 16 * m + gq + 8 * (e >> 1)] =
                     SPLIT ? acc[m][t][e] : tot[m][t][e];
     if (SPLIT)
         cluster_sync();
@@ -392,28 +438,32 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
 // ----------------------------------------------------------------- launches ---
 
 template <int GS, int MR, int NT>
-bi_status launch_rows(const CUtensorMap &tmW, const CUtensorMap &tmX, const GemmI4Params &p, cudaStream_t s) {
+bi_status launch_rows(const CUtensorMap &tmW, const CUtensorMap &tmX, const GemmI4Params &p, int sms, cudaStream_t s) {
     static unsigned long long configured = 0;
     constexpr int most = 1024 + kMaxSegments * rows_warp<GS, MR, NT>();
     static_assert(most <= 232448 - 1024, "one CTA's shared memory");
     if (ensure_smem_attr(reinterpret_cast<const void *>(gemm_int4_rows_kernel<GS, MR, NT>), most, &configured) != BI_OK)
         return BI_ERR_CUDA;
-    const int64_t grid = (p.N + 16 * MR - 1) / (16 * MR);
-    return launch_pdl(gemm_int4_rows_kernel<GS, MR, NT>, dim3(static_cast<unsigned>(grid)), dim3(32 * p.segments),
-                      1024 + p.segments * rows_warp<GS, MR, NT>(), s, tmW, tmX, p);
+    // as many CTAs as the shared memory of the SMs takes at once
+    const int64_t tiles = (p.N + 16 * MR - 1) / (16 * MR);
+    const int smem = 1024 + p.segments * rows_warp<GS, MR, NT>(), fit = 232448 / (smem + 2048);
+    const int64_t most_ctas = static_cast<int64_t>(sms) * (fit > 16 ? 16 : fit);
+    return launch_pdl(gemm_int4_rows_kernel<GS, MR, NT>, dim3(static_cast<unsigned>(tiles < most_ctas ? tiles : most_ctas)),
+                      dim3(32 * p.segments), smem, s, tmW, tmX, p);
 }
 
-template <int GS, bool SPLIT>
-bi_status launch_tiles(const CUtensorMap &tmW, const CUtensorMap &tmX, const GemmI4Params &p, int64_t tiles, cudaStream_t s) {
+template <int GS, int TM, bool SPLIT>
+bi_status launch_tile_kernel(const CUtensorMap &tmW, const CUtensorMap &tmX, const GemmI4Params &p, int64_t tiles,
+                       cudaStream_t s) {
     static unsigned long long configured = 0;
-    if (ensure_smem_attr(reinterpret_cast<const void *>(gemm_int4_tile_kernel<GS, SPLIT>), tile_smem<GS>(), &configured) != BI_OK)
+    if (ensure_smem_attr(reinterpret_cast<const void *>(gemm_int4_tile_kernel<GS, TM, SPLIT>), tile_smem<GS, TM>(), &configured) != BI_OK)
         return BI_ERR_CUDA;
     const int64_t grid = tiles * (SPLIT ? p.segments : 1);
     if (grid > 0x7FFFFFFF) return BI_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kTileThreads);
-    cfg.dynamicSmemBytes = tile_smem<GS>();
+    cfg.dynamicSmemBytes = tile_smem<GS, TM>();
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -424,31 +474,35 @@ bi_status launch_tiles(const CUtensorMap &tmW, const CUtensorMap &tmX, const Gem
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = SPLIT ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, gemm_int4_tile_kernel<GS, SPLIT>, tmW, tmX, p) == cudaSuccess) return BI_OK;
+    if (cudaLaunchKernelEx(&cfg, gemm_int4_tile_kernel<GS, TM, SPLIT>, tmW, tmX, p) == cudaSuccess) return BI_OK;
     cudaGetLastError();
     return BI_ERR_CUDA;
 }
 
+template <int GS, int TM>
+bi_status launch_tiles(const CUtensorMap &tmW, const CUtensorMap &tmX, const GemmI4Params &p, int sms, cudaStream_t s) {
+    // a CTA a segment while the tiles alone would leave SMs without one
+    const int64_t tiles = (p.N + kTileN - 1) / kTileN * ((p.M + TM - 1) / TM);
+    if (p.segments > 1 && tiles < sms) return launch_tile_kernel<GS, TM, true>(tmW, tmX, p, tiles, s);
+    return launch_tile_kernel<GS, TM, false>(tmW, tmX, p, tiles, s);
+}
+
 template <int GS>
 bi_status launch_group(const void *X, int64_t ldx, const uint8_t *W, GemmI4Params &p, int sms, cudaStream_t s) {
-    const bool rows = p.M <= 16;
-    const int nt = p.M <= 8 ? 1 : 2;
+    const bool rows = p.M <= 8;
+    const int tm = p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64;
     // 32 weight rows a CTA halve the reads of X; 16 where that would leave SMs without a CTA
-    const int mr = p.M > 4 && p.N >= 32 * 2 * static_cast<int64_t>(sms) ? 2 : 1;
+    const int mr = p.N >= 32 * 2 * static_cast<int64_t>(sms) ? 2 : 1;
     CUtensorMap tmW{}, tmX{};
     if (make_tmap_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, p.K / 2, p.N, p.K / 2, kBlockK / 2, rows ? 16 * mr : kTileN,
                      CU_TENSOR_MAP_SWIZZLE_64B) != BI_OK ||
-        make_tmap_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, p.K, p.M, ldx * 2, 64, rows ? 8 * nt : kTileM,
+        make_tmap_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, p.K, p.M, ldx * 2, 64, rows ? 8 : tm,
                      CU_TENSOR_MAP_SWIZZLE_128B) != BI_OK)
         return BI_ERR_CUDA;
-    if (rows) {
-        if (mr == 1) return nt == 1 ? launch_rows<GS, 1, 1>(tmW, tmX, p, s) : launch_rows<GS, 1, 2>(tmW, tmX, p, s);
-        return nt == 1 ? launch_rows<GS, 2, 1>(tmW, tmX, p, s) : launch_rows<GS, 2, 2>(tmW, tmX, p, s);
-    }
-    // one CTA a segment while the tiles alone would not keep two CTAs an SM at work
-    const int64_t tiles = (p.N + kTileN - 1) / kTileN * ((p.M + kTileM - 1) / kTileM);
-    if (p.segments > 1 && tiles < 4 * static_cast<int64_t>(sms)) return launch_tiles<GS, true>(tmW, tmX, p, tiles, s);
-    return launch_tiles<GS, false>(tmW, tmX, p, tiles, s);
+    if (rows) return mr == 1 ? launch_rows<GS, 1, 1>(tmW, tmX, p, sms, s) : launch_rows<GS, 2, 1>(tmW, tmX, p, sms, s);
+    if (tm == 16) return launch_tiles<GS, 16>(tmW, tmX, p, sms, s);
+    if (tm == 32) return launch_tiles<GS, 32>(tmW, tmX, p, sms, s);
+    return launch_tiles<GS, 64>(tmW, tmX, p, sms, s);
 }
 
 }  // namespace
@@ -459,9 +513,17 @@ bi_status launch_gemm_int4(const void *X, int64_t ldx, const uint8_t *W, const v
     const DeviceInfo *info = nullptr;
     const bi_status st = current_device(&dev, &info);
     if (st != BI_OK) return st;
-    GemmI4Params p{static_cast<const uint16_t *>(scales), zeros, static_cast<uint16_t *>(Y), ldy, M, N, K, group, K / group,
-                   (K + kBlockK - 1) / kBlockK, 0, device_status_word()};
-    p.segments = static_cast<int32_t>(p.blocks < 4 ? 1 : p.blocks / 4 > kMaxSegments ? kMaxSegments : p.blocks / 4);
+    GemmI4Params p{};
+    p.S = static_cast<const uint32_t *>(scales);
+    p.Z = reinterpret_cast<const uint32_t *>(zeros);
+    p.Y = static_cast<uint16_t *>(Y);
+    p.ldy = ldy;
+    p.M = M, p.N = N, p.K = K;
+    p.groups = K / group;
+    p.group = static_cast<int32_t>(group);
+    p.blocks = static_cast<int32_t>((K + kBlockK - 1) / kBlockK);
+    p.segments = p.blocks < 4 ? 1 : p.blocks / 4 > kMaxSegments ? kMaxSegments : p.blocks / 4;
+    p.status = device_status_word();
     if (group == 32) return launch_group<32>(X, ldx, W, p, info->sm_count, s);
     if (group == 64) return launch_group<64>(X, ldx, W, p, info->sm_count, s);
     return launch_group<128>(X, ldx, W, p, info->sm_count, s);

@@ -72,7 +72,7 @@ def test_attention_own_arguments(so):
 @pytest.mark.parametrize("change,want", [
     (dict(M=-1), 1), (dict(K=0), 1), (dict(g=0), 1), (dict(X=None), 1), (dict(S=None), 1), (dict(ldx=100), 1), (dict(ldy=100), 1),
     (dict(g=16), 2), (dict(g=96), 2), (dict(g=192), 2), (dict(N=500), 2), (dict(ldx=260), 3), (dict(W=FAKE + 8), 3),
-    (dict(X=FAKE + 8), 3), (dict(S=FAKE + 1), 3), (dict(M=0), 0), (dict(N=0), 0)])
+    (dict(X=FAKE + 8), 3), (dict(S=FAKE + 8), 3), (dict(Z=FAKE + 4), 3), (dict(M=0), 0), (dict(N=0), 0)])
 def test_gemm(so, change, want):
     a = dict(dict(X=FAKE, ldx=256, W=FAKE, S=FAKE, Z=None, Y=FAKE, ldy=512, M=4, N=512, K=256, g=64), **change)
     assert so.bi_gemm_int4(a["X"], a["ldx"], a["W"], a["S"], a["Z"], a["Y"], a["ldy"], a["M"], a["N"], a["K"], a["g"], None) == want
