@@ -38,8 +38,8 @@ struct GemmI4Params {
     const uint32_t *S;       // [N][groups] bf16, as words
     const uint32_t *Z;       // [N][groups] bytes, as words, or null
     uint16_t *Y;             // [M][ldy]
-    int64_t ldy, M, N, K, groups;
-    int32_t group, blocks, segments;
+    int64_t ldy, M, N, K, s_last, z_last;   // last words of S and Z
+    int32_t groups, group, blocks, segments;
     unsigned *status;
 };
 
@@ -57,46 +57,45 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// First group of a block.
-template <int GS>
-__device__ __forceinline__ int first_group(const GemmI4Params &p, int blk) {
-    return GS < kBlockK ? blk * (kBlockK / GS) : static_cast<int>(static_cast<unsigned>(blk) / static_cast<unsigned>(p.group / kBlockK));
-}
-
-// Starts the copies of a block's scales and zeros for `rows` weight rows from n0 by
-// `threads` threads, each of which arrives on the barrier once its copies have
-// landed. Words past the arrays (rows past N, groups past K) repeat the last one.
-template <int GS>
-__device__ __forceinline__ void stage_scales(const GemmI4Params &p, uint32_t dst, uint64_t *bar, int64_t n0, int rows, int blk,
-                                             int thread, int threads) {
+// Starts the copies of a block's scales and zeros for ROWS weight rows by THREADS
+// threads, each of which arrives on the barrier once its copies have landed.
+// e0: element (row n0, the block's first group) of the arrays. Words past the
+// arrays (rows past N, groups past K) repeat the last one.
+template <int GS, int ROWS, int THREADS, bool ZEROS>
+__device__ __forceinline__ void stage_scales(const GemmI4Params &p, uint32_t dst, uint64_t *bar, int64_t e0, int thread) {
     using T = ScaleTile<GS>;
-    const int64_t e0 = n0 * p.groups + first_group<GS>(p, blk), total = p.N * p.groups;
-    for (int v = thread; v < rows * T::kSWords; v += threads) {
-        const int r = v / T::kSWords, w = v % T::kSWords;
-        const int64_t word = (e0 + r * p.groups) / 2 + w;
-        cp_async_4(dst + v * 4, p.S + (word < total / 2 ? word : total / 2 - 1));
+#pragma unroll
+    for (int i = 0; i < (ROWS * T::kSWords + THREADS - 1) / THREADS; ++i) {
+        const int v = thread + i * THREADS, r = v / T::kSWords, w = v % T::kSWords;
+        if (v < ROWS * T::kSWords) cp_async_4(dst + v * 4, p.S + min(((e0 + r * p.groups) >> 1) + w, p.s_last));
     }
-    if (p.Z) {
-        for (int v = thread; v < rows * T::kZWords; v += threads) {
-            const int r = v / T::kZWords, w = v % T::kZWords;
-            const int64_t word = (e0 + r * p.groups) / 4 + w;
-            cp_async_4(dst + (rows * T::kSWords + v) * 4, p.Z + (word < total / 4 ? word : total / 4 - 1));
+    if (ZEROS) {
+#pragma unroll
+        for (int i = 0; i < (ROWS * T::kZWords + THREADS - 1) / THREADS; ++i) {
+            const int v = thread + i * THREADS, r = v / T::kZWords, w = v % T::kZWords;
+            if (v < ROWS * T::kZWords)
+                cp_async_4(dst + (ROWS * T::kSWords + v) * 4, p.Z + min(((e0 + r * p.groups) >> 2) + w, p.z_last));
         }
     }
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// (scale as fp32, -(128 + z) as a bf16 pair) of a staged row (of `rows`, the tile's first one n0) and group.
-template <int GS>
-__device__ __forceinline__ void read_scale(const GemmI4Params &p, const uint8_t *tile, int64_t n0, int rows, int row, int blk,
-                                           int sub, float &s, uint32_t &z2) {
+// (scale as fp32, -(128 + z) as a bf16 pair) of a staged row and group. `e` is the element of (row, the
+// block's first group) modulo 4: tiles begin at multiples of 16 rows, so row * groups + group will do.
+template <int GS, int ROWS, bool ZEROS>
+__device__ __forceinline__ void read_scale(const uint8_t *tile, int row, int e, int sub, bool in, float &s, uint32_t &z2) {
     using T = ScaleTile<GS>;
-    const uint32_t e = static_cast<uint32_t>(n0 + row) * static_cast<uint32_t>(p.groups) + first_group<GS>(p, blk);   // modulo 4 is exact
-    const bool in = GS == kBlockK || blk * kBlockK + sub * GS < p.K;
     const uint32_t bits = *reinterpret_cast<const uint16_t *>(tile + row * T::kSWords * 4 + (e & 1) * 2 + sub * 2);
     s = in ? __uint_as_float(bits << 16) : 0.0f;
-    z2 = 0xC308C308u;
-    if (p.Z) z2 = 0xC300C300u | ((tile[(rows * T::kSWords + row * T::kZWords) * 4 + (e & 3) + sub] & 15u) * 0x00010001u);
+    z2 = kBf16x2_m136;
+    if (ZEROS) z2 = 0xC300C300u | ((tile[(ROWS * T::kSWords + row * T::kZWords) * 4 + (e & 3) + sub] & 15u) * 0x00010001u);
+}
+
+// The first product of a chain: D = A B.
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // Where lane (g, c) finds its operands of a block, GS k a scale: word j of group
@@ -129,12 +128,11 @@ __device__ __forceinline__ void expand_weights(uint32_t w, uint32_t z2, uint32_t
 }
 
 // acc += the block's groups, each scaled, for weight rows row0 .. row0 + 16 MR - 1
-// of the staged `rows` and 8 NT rows of X from x_row0 of the staged x_rows.
-template <int GS, int MR, int NT>
-__device__ __forceinline__ void block_product(const GemmI4Params &p, const uint8_t *w_tile, const uint8_t *x_tile,
-                                              const uint8_t *sc, int64_t n0, int rows, int row0, int blk, int x_rows,
-                                              int x_row0, int gq, int cq, float (&acc)[MR][NT][4]) {
-    const uint32_t w_at = smem_u32(w_tile), x_at = smem_u32(x_tile);
+// of the staged ROWS and 8 NT rows of X from x_row0 of the staged X_ROWS. `group`:
+// the block's first group; k_left: k from the block's start to K's end.
+template <int GS, int MR, int NT, int ROWS, int X_ROWS, bool ZEROS>
+__device__ __forceinline__ void block_product(uint32_t w_tile, uint32_t x_tile, const uint8_t *sc, int row0, int x_row0, int groups,
+                                              int group, int64_t k_left, int gq, int cq, float (&acc)[MR][NT][4]) {
     constexpr int kSub = kBlockK / GS;
 #pragma unroll
     for (int sub = 0; sub < kSub; ++sub) {
@@ -147,13 +145,9 @@ __device__ __forceinline__ void block_product(const GemmI4Params &p, const uint8
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int row = row0 + 16 * m + 8 * h + gq;
-                load_words<GS>(w_at + row * (kBlockK / 2), row, sub, cq, w[m][h]);
-                read_scale<GS>(p, sc, n0, rows, row, blk, sub, s[m][h], z2[m][h]);
+                load_words<GS>(w_tile + row * (kBlockK / 2), row, sub, cq, w[m][h]);
+                read_scale<GS, ROWS, ZEROS>(sc, row, row * groups + group, sub, kSub == 1 || sub * GS < k_left, s[m][h], z2[m][h]);
             }
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) part[m][t][e] = 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < GS / 32; ++j) {
@@ -165,10 +159,14 @@ __device__ __forceinline__ void block_product(const GemmI4Params &p, const uint8
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 uint32_t b[4];
-                load_x<GS>(x_at, x_rows, x_row0 + 8 * t + gq, sub, cq, j, b);
+                load_x<GS>(x_tile, X_ROWS, x_row0 + 8 * t + gq, sub, cq, j, b);
 #pragma unroll
-                for (int m = 0; m < MR; ++m)
-                    mma_16816(part[m][t], a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], b[0], b[1]);
+                for (int m = 0; m < MR; ++m) {
+                    if (j == 0)
+                        mma_first(part[m][t], a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], b[0], b[1]);
+                    else
+                        mma_16816(part[m][t], a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], b[0], b[1]);
+                }
 #pragma unroll
                 for (int m = 0; m < MR; ++m)
                     mma_16816(part[m][t], a[m][0][2], a[m][1][2], a[m][0][3], a[m][1][3], b[2], b[3]);
@@ -179,10 +177,26 @@ __device__ __forceinline__ void block_product(const GemmI4Params &p, const uint8
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[m][t][e] = __fmaf_rn(s[m][e >> 1], part[m][t][e], acc[m][t][e]);
+                for (int e = 0; e < 4; ++e) acc[m][t][e] = __fmaf_rn(s[m][e >> 1], part[m][t][e], acc[m][t][e]);
     }
 }
+
+// Block -> its first group, and on to the next: a block has several groups, or a group several blocks.
+template <int GS>
+struct GroupCursor {
+    int group, left;         // left: blocks of the group still to come, this one included
+    __device__ __forceinline__ GroupCursor(const GemmI4Params &p, int blk) {
+        const int per = GS < kBlockK ? 1 : p.group / kBlockK;
+        group = GS < kBlockK ? blk * (kBlockK / GS) : blk / per;
+        left = per - (GS < kBlockK ? 0 : blk % per);
+    }
+    __device__ __forceinline__ void next(const GemmI4Params &p) {
+        if (GS < kBlockK)
+            group += kBlockK / GS;
+        else if (--left == 0)
+            ++group, left = p.group / kBlockK;
+    }
+};
 
 __device__ __forceinline__ void store_y(const GemmI4Params &p, int64_t m, int64_t n, float y) {
     if (m < p.M && n < p.N && BI_IN_BOUNDS(m * p.ldy + n < (p.M - 1) * p.ldy + p.N, p.status))
@@ -204,7 +218,7 @@ constexpr int rows_warp() {
 }
 
 // CTAs walk the tiles of 16 MR weight rows; a warp's ring runs on from one tile to the next.
-template <int GS, int MR, int NT>
+template <int GS, int MR, int NT, bool ZEROS>
 __global__ void __launch_bounds__(32 * kMaxSegments)
 gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmI4Params p) {
     constexpr int kRing = rows_ring<MR>(), kStage = rows_stage<MR, NT>(), kScaleBytes = ScaleTile<GS>::bytes(16 * MR);
@@ -230,22 +244,26 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     const int tiles = static_cast<int>((p.N + 16 * MR - 1) / (16 * MR));
     const int b0 = static_cast<int>(static_cast<int64_t>(warp) * p.blocks / p.segments);
     const int b1 = static_cast<int>(static_cast<int64_t>(warp + 1) * p.blocks / p.segments);
-    // the next block to be copied, and its slot
+    const GroupCursor<GS> g0(p, b0);
+    // the next block to be copied, its group, and its slot
     int ft = blockIdx.x, fb = b0, fs = 0;
+    GroupCursor<GS> fg = g0;
+    int64_t row_e = static_cast<int64_t>(ft) * (16 * MR) * p.groups;   // element (the tile's first row, group 0)
+    const int64_t step_e = static_cast<int64_t>(gridDim.x) * (16 * MR) * p.groups;
     auto fill = [&]() {
         if (ft >= tiles) return;
         uint8_t *dst = ring + fs * kStage;
         uint64_t *bar = &full[warp][fs];
-        const int64_t n0 = static_cast<int64_t>(ft) * (16 * MR);
         if (lane == 0) {
             mbar_arrive_expect_tx(bar, kWBytes + kXBytes);
-            tma_load_2d(dst, &tmW, bar, fb * (kBlockK / 2), static_cast<int32_t>(n0));
+            tma_load_2d(dst, &tmW, bar, fb * (kBlockK / 2), ft * (16 * MR));
             tma_load_2d(dst + kWBytes, &tmX, bar, fb * kBlockK, 0);
             tma_load_2d(dst + kWBytes + kXBytes / 2, &tmX, bar, fb * kBlockK + 64, 0);
         }
-        stage_scales<GS>(p, smem_u32(scales + fs * kScaleBytes), bar, n0, 16 * MR, fb, lane, 32);
+        stage_scales<GS, 16 * MR, 32, ZEROS>(p, smem_u32(scales + fs * kScaleBytes), bar, row_e + fg.group, lane);
         if (++fs == kRing) fs = 0;
-        if (++fb == b1) fb = b0, ft += gridDim.x;
+        fg.next(p);
+        if (++fb == b1) fb = b0, fg = g0, ft += gridDim.x, row_e += step_e;
     };
     for (int k = 0; k < kRing; ++k) fill();
     int slot = 0, buf = 0;
@@ -260,12 +278,15 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[m][t][e] = 0.0f;
+        GroupCursor<GS> g = g0;
         for (int blk = b0; blk < b1 && ok; ++blk) {
             ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][slot], parity, nullptr));
             __syncwarp();
             if (!ok) break;
-            const uint8_t *st = ring + slot * kStage;
-            block_product<GS, MR, NT>(p, st, st + kWBytes, scales + slot * kScaleBytes, n0, 16 * MR, 0, blk, 8 * NT, 0, gq, cq, acc);
+            const uint32_t st = smem_u32(ring + slot * kStage);
+            block_product<GS, MR, NT, 16 * MR, 8 * NT, ZEROS>(st, st + kWBytes, scales + slot * kScaleBytes, 0, 0, p.groups, g.group,
+                                                              p.K - static_cast<int64_t>(blk) * kBlockK, gq, cq, acc);
+            g.next(p);
             __syncwarp();                                  // every lane has read the slot
             fill();
             if (++slot == kRing) slot = 0, parity ^= 1;
@@ -310,7 +331,7 @@ template <int GS, int TM>
 constexpr int tile_smem() { return 1024 + tile_stages<TM>() * (tile_stage<TM>() + ScaleTile<GS>::bytes(kTileN)); }
 
 // One segment a CTA (a cluster's ranks in segment order), or all segments in turn (SPLIT false).
-template <int GS, int TM, bool SPLIT>
+template <int GS, int TM, bool SPLIT, bool ZEROS>
 __global__ void __launch_bounds__(kTileThreads, TM == 64 && !SPLIT ? 1 : 2)
 gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmI4Params p) {
     constexpr int kScaleBytes = ScaleTile<GS>::bytes(kTileN), kTileStage = tile_stage<TM>(), kTileStages = tile_stages<TM>();
@@ -337,6 +358,7 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     const int64_t m0 = tile % tiles_m * kTileM, n0 = tile / tiles_m * kTileN;
     const int first = SPLIT ? static_cast<int>(static_cast<int64_t>(rank) * p.blocks / p.segments) : 0;
     const int last = SPLIT ? static_cast<int>(static_cast<int64_t>(rank + 1) * p.blocks / p.segments) : p.blocks;
+    GroupCursor<GS> g(p, first), fg = g;                   // of the block at work, of the next to be copied
     auto fill = [&](int blk) {
         const int slot = (blk - first) % kTileStages;
         uint8_t *dst = smem + slot * kTileStage;
@@ -346,7 +368,8 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
             tma_load_2d(dst + kTileW, &tmX, &full[slot], blk * kBlockK, static_cast<int32_t>(m0));
             tma_load_2d(dst + kTileW + kTileM * 128, &tmX, &full[slot], blk * kBlockK + 64, static_cast<int32_t>(m0));
         }
-        stage_scales<GS>(p, smem_u32(scales + slot * kScaleBytes), &full[slot], n0, kTileN, blk, tid, kTileThreads);
+        stage_scales<GS, kTileN, kTileThreads, ZEROS>(p, smem_u32(scales + slot * kScaleBytes), &full[slot], n0 * p.groups + fg.group, tid);
+        fg.next(p);
     };
     for (int blk = first; blk < last && blk < first + kTileStages - 1; ++blk) fill(blk);
     float acc[MR][NT][4], tot[MR][NT][4];
@@ -374,9 +397,10 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
             break;
         }
         if (blk + kTileStages - 1 < last) fill(blk + kTileStages - 1);
-        const uint8_t *st = smem + slot * kTileStage;
-        block_product<GS, MR, NT>(p, st, st + kTileW, scales + slot * kScaleBytes, n0, kTileN, 16 * MR * wn, blk, kTileM, 8 * NT * wm, gq, cq,
-                                  acc);
+        const uint32_t st = smem_u32(smem + slot * kTileStage);
+        block_product<GS, MR, NT, kTileN, kTileM, ZEROS>(st, st + kTileW, scales + slot * kScaleBytes, 16 * MR * wn, 8 * NT * wm, p.groups,
+                                                         g.group, p.K - static_cast<int64_t>(blk) * kBlockK, gq, cq, acc);
+        g.next(p);
         if (!SPLIT && blk + 1 == seg_end) {
 #pragma unroll
             for (int m = 0; m < MR; ++m)
@@ -437,26 +461,26 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
 
 // ----------------------------------------------------------------- launches ---
 
-template <int GS, int MR, int NT>
+template <int GS, int MR, int NT, bool ZEROS>
 bi_status launch_rows(const CUtensorMap &tmW, const CUtensorMap &tmX, const GemmI4Params &p, int sms, cudaStream_t s) {
     static unsigned long long configured = 0;
     constexpr int most = 1024 + kMaxSegments * rows_warp<GS, MR, NT>();
     static_assert(most <= 232448 - 1024, "one CTA's shared memory");
-    if (ensure_smem_attr(reinterpret_cast<const void *>(gemm_int4_rows_kernel<GS, MR, NT>), most, &configured) != BI_OK)
+    if (ensure_smem_attr(reinterpret_cast<const void *>(gemm_int4_rows_kernel<GS, MR, NT, ZEROS>), most, &configured) != BI_OK)
         return BI_ERR_CUDA;
     // as many CTAs as the shared memory of the SMs takes at once
     const int64_t tiles = (p.N + 16 * MR - 1) / (16 * MR);
     const int smem = 1024 + p.segments * rows_warp<GS, MR, NT>(), fit = 232448 / (smem + 2048);
     const int64_t most_ctas = static_cast<int64_t>(sms) * (fit > 16 ? 16 : fit);
-    return launch_pdl(gemm_int4_rows_kernel<GS, MR, NT>, dim3(static_cast<unsigned>(tiles < most_ctas ? tiles : most_ctas)),
+    return launch_pdl(gemm_int4_rows_kernel<GS, MR, NT, ZEROS>, dim3(static_cast<unsigned>(tiles < most_ctas ? tiles : most_ctas)),
                       dim3(32 * p.segments), smem, s, tmW, tmX, p);
 }
 
-template <int GS, int TM, bool SPLIT>
+template <int GS, int TM, bool SPLIT, bool ZEROS>
 bi_status launch_tile_kernel(const CUtensorMap &tmW, const CUtensorMap &tmX, const GemmI4Params &p, int64_t tiles,
                        cudaStream_t s) {
     static unsigned long long configured = 0;
-    if (ensure_smem_attr(reinterpret_cast<const void *>(gemm_int4_tile_kernel<GS, TM, SPLIT>), tile_smem<GS, TM>(), &configured) != BI_OK)
+    if (ensure_smem_attr(reinterpret_cast<const void *>(gemm_int4_tile_kernel<GS, TM, SPLIT, ZEROS>), tile_smem<GS, TM>(), &configured) != BI_OK)
         return BI_ERR_CUDA;
     const int64_t grid = tiles * (SPLIT ? p.segments : 1);
     if (grid > 0x7FFFFFFF) return BI_ERR_UNSUPPORTED;
@@ -474,20 +498,20 @@ bi_status launch_tile_kernel(const CUtensorMap &tmW, const CUtensorMap &tmX, con
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = SPLIT ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, gemm_int4_tile_kernel<GS, TM, SPLIT>, tmW, tmX, p) == cudaSuccess) return BI_OK;
+    if (cudaLaunchKernelEx(&cfg, gemm_int4_tile_kernel<GS, TM, SPLIT, ZEROS>, tmW, tmX, p) == cudaSuccess) return BI_OK;
     cudaGetLastError();
     return BI_ERR_CUDA;
 }
 
-template <int GS, int TM>
+template <int GS, int TM, bool ZEROS>
 bi_status launch_tiles(const CUtensorMap &tmW, const CUtensorMap &tmX, const GemmI4Params &p, int sms, cudaStream_t s) {
     // a CTA a segment while the tiles alone would leave SMs without one
     const int64_t tiles = (p.N + kTileN - 1) / kTileN * ((p.M + TM - 1) / TM);
-    if (p.segments > 1 && tiles < sms) return launch_tile_kernel<GS, TM, true>(tmW, tmX, p, tiles, s);
-    return launch_tile_kernel<GS, TM, false>(tmW, tmX, p, tiles, s);
+    if (p.segments > 1 && tiles < sms) return launch_tile_kernel<GS, TM, true, ZEROS>(tmW, tmX, p, tiles, s);
+    return launch_tile_kernel<GS, TM, false, ZEROS>(tmW, tmX, p, tiles, s);
 }
 
-template <int GS>
+template <int GS, bool ZEROS>
 bi_status launch_group(const void *X, int64_t ldx, const uint8_t *W, GemmI4Params &p, int sms, cudaStream_t s) {
     const bool rows = p.M <= 8;
     const int tm = p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64;
@@ -499,10 +523,10 @@ bi_status launch_group(const void *X, int64_t ldx, const uint8_t *W, GemmI4Param
         make_tmap_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, p.K, p.M, ldx * 2, 64, rows ? 8 : tm,
                      CU_TENSOR_MAP_SWIZZLE_128B) != BI_OK)
         return BI_ERR_CUDA;
-    if (rows) return mr == 1 ? launch_rows<GS, 1, 1>(tmW, tmX, p, sms, s) : launch_rows<GS, 2, 1>(tmW, tmX, p, sms, s);
-    if (tm == 16) return launch_tiles<GS, 16>(tmW, tmX, p, sms, s);
-    if (tm == 32) return launch_tiles<GS, 32>(tmW, tmX, p, sms, s);
-    return launch_tiles<GS, 64>(tmW, tmX, p, sms, s);
+    if (rows) return mr == 1 ? launch_rows<GS, 1, 1, ZEROS>(tmW, tmX, p, sms, s) : launch_rows<GS, 2, 1, ZEROS>(tmW, tmX, p, sms, s);
+    if (tm == 16) return launch_tiles<GS, 16, ZEROS>(tmW, tmX, p, sms, s);
+    if (tm == 32) return launch_tiles<GS, 32, ZEROS>(tmW, tmX, p, sms, s);
+    return launch_tiles<GS, 64, ZEROS>(tmW, tmX, p, sms, s);
 }
 
 }  // namespace
@@ -519,14 +543,16 @@ bi_status launch_gemm_int4(const void *X, int64_t ldx, const uint8_t *W, const v
     p.Y = static_cast<uint16_t *>(Y);
     p.ldy = ldy;
     p.M = M, p.N = N, p.K = K;
-    p.groups = K / group;
+    p.groups = static_cast<int32_t>(K / group);
+    p.s_last = N * p.groups / 2 - 1, p.z_last = N * p.groups / 4 - 1;   // (N % 8 == 0)
     p.group = static_cast<int32_t>(group);
     p.blocks = static_cast<int32_t>((K + kBlockK - 1) / kBlockK);
     p.segments = p.blocks < 4 ? 1 : p.blocks / 4 > kMaxSegments ? kMaxSegments : p.blocks / 4;
     p.status = device_status_word();
-    if (group == 32) return launch_group<32>(X, ldx, W, p, info->sm_count, s);
-    if (group == 64) return launch_group<64>(X, ldx, W, p, info->sm_count, s);
-    return launch_group<128>(X, ldx, W, p, info->sm_count, s);
+    const int sms = info->sm_count;
+    if (group == 32) return zeros ? launch_group<32, true>(X, ldx, W, p, sms, s) : launch_group<32, false>(X, ldx, W, p, sms, s);
+    if (group == 64) return zeros ? launch_group<64, true>(X, ldx, W, p, sms, s) : launch_group<64, false>(X, ldx, W, p, sms, s);
+    return zeros ? launch_group<128, true>(X, ldx, W, p, sms, s) : launch_group<128, false>(X, ldx, W, p, sms, s);
 }
 
 }  // namespace bi
