@@ -13,9 +13,9 @@
 // lane takes its k as whole 32-bit words of the weight row (eight codes, two
 // steps), and the nibbles q and q + 4 of a word are one operand pair.
 //
-// The sum's order is fixed by (K, group): K is cut into blocks of 128 and the
-// blocks into S segments; a segment's groups are added in ascending order, and
-// the segments' sums in order. The number of rows decides only who computes
+// The sum's order is fixed by (K, group): K is cut into units of 256 and the
+// units into S segments; a segment's groups (of longer ones, each 128 k) are added
+// in ascending order, and the segments' sums in order. The number of rows decides only who computes
 // what:
 //   - few rows (gemm_int4_rows_kernel, M <= 8): a warp a segment, the CTA's
 //     warps share 16 or 32 weight rows; every warp has its own ring of TMA
@@ -31,7 +31,8 @@
 namespace bi {
 namespace {
 
-constexpr int kBlockK = 128;                   // k of a staged block
+constexpr int kBlockK = 128;                   // a group's longest product chain
+constexpr int kUnitK = 256;                    // k of which segments are made
 constexpr int kMaxSegments = 8;
 
 struct GemmI4Params {
@@ -39,17 +40,18 @@ struct GemmI4Params {
     const uint32_t *Z;       // [N][groups] bytes, as words, or null
     uint16_t *Y;             // [M][ldy]
     int64_t ldy, M, N, K, s_last, z_last;   // last words of S and Z
-    int32_t groups, group, blocks, segments;
+    int32_t groups, group, blocks, units, segments;   // blocks: of kBlockK; units: of kUnitK
+    int32_t x_rows;          // rows kernel: staged rows of X (1, 2, 4 or 8)
     unsigned *status;
 };
 
-// The scales and zeros of a staged block, GS k a scale: for each weight row the
+// The scales and zeros of KB staged k, GS k a scale: for each weight row the
 // 32-bit words that hold them (their place in the first word depends on the row).
-template <int GS>
+template <int GS, int KB>
 struct ScaleTile {
-    static constexpr int kSub = kBlockK / GS;                     // groups of a block
+    static constexpr int kSub = KB / GS;                          // groups (or a longer group's 128 k each)
     static constexpr int kSWords = (kSub + 1) / 2 + (kSub > 1);   // words of kSub 16-bit scales at any halfword
-    static constexpr int kZWords = kSub > 1 ? 2 : 1;              // words of kSub bytes at any byte
+    static constexpr int kZWords = (kSub + 3) / 4 + (kSub > 1);   // words of kSub bytes at any byte
     static constexpr int bytes(int rows) { return rows * (kSWords + kZWords) * 4; }
 };
 
@@ -59,11 +61,11 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src) {
 
 // Starts the copies of a block's scales and zeros for ROWS weight rows by THREADS
 // threads, each of which arrives on the barrier once its copies have landed.
-// e0: element (row n0, the block's first group) of the arrays. Words past the
+// e0: element (row n0, the first group) of the arrays. Words past the
 // arrays (rows past N, groups past K) repeat the last one.
-template <int GS, int ROWS, int THREADS, bool ZEROS>
+template <int GS, int KB, int ROWS, int THREADS, bool ZEROS>
 __device__ __forceinline__ void stage_scales(const GemmI4Params &p, uint32_t dst, uint64_t *bar, int64_t e0, int thread) {
-    using T = ScaleTile<GS>;
+    using T = ScaleTile<GS, KB>;
 #pragma unroll
     for (int i = 0; i < (ROWS * T::kSWords + THREADS - 1) / THREADS; ++i) {
         const int v = thread + i * THREADS, r = v / T::kSWords, w = v % T::kSWords;
@@ -80,15 +82,15 @@ __device__ __forceinline__ void stage_scales(const GemmI4Params &p, uint32_t dst
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// (scale as fp32, -(128 + z) as a bf16 pair) of a staged row and group. `e` is the element of (row, the
-// block's first group) modulo 4: tiles begin at multiples of 16 rows, so row * groups + group will do.
-template <int GS, int ROWS, bool ZEROS>
-__device__ __forceinline__ void read_scale(const uint8_t *tile, int row, int e, int sub, bool in, float &s, uint32_t &z2) {
-    using T = ScaleTile<GS>;
-    const uint32_t bits = *reinterpret_cast<const uint16_t *>(tile + row * T::kSWords * 4 + (e & 1) * 2 + sub * 2);
+// (scale as fp32, -(128 + z) as a bf16 pair) of a staged row and its `at`-th staged group. `e` is the element of
+// (row, the first staged group) modulo 4: tiles begin at multiples of 16 rows, so row * groups + group will do.
+template <int GS, int KB, int ROWS, bool ZEROS>
+__device__ __forceinline__ void read_scale(const uint8_t *tile, int row, int e, int at, bool in, float &s, uint32_t &z2) {
+    using T = ScaleTile<GS, KB>;
+    const uint32_t bits = *reinterpret_cast<const uint16_t *>(tile + row * T::kSWords * 4 + (e & 1) * 2 + at * 2);
     s = in ? __uint_as_float(bits << 16) : 0.0f;
     z2 = kBf16x2_m136;
-    if (ZEROS) z2 = 0xC300C300u | ((tile[(ROWS * T::kSWords + row * T::kZWords) * 4 + (e & 3) + sub] & 15u) * 0x00010001u);
+    if (ZEROS) z2 = 0xC300C300u | ((tile[(ROWS * T::kSWords + row * T::kZWords) * 4 + (e & 3) + at] & 15u) * 0x00010001u);
 }
 
 // The first product of a chain: D = A B.
@@ -98,13 +100,14 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// Where lane (g, c) finds its operands of a block, GS k a scale: word j of group
-// `sub` holds k = GS sub + (GS / 4) c + 8 j and the seven after it. Weight rows
-// are 64 bytes a block (64-byte swizzle), rows of X two boxes of 64 k (128-byte swizzle).
-template <int GS>
+// Where lane (g, c) finds its operands among KB staged k, GS k a scale: word j of
+// group `sub` holds k = GS sub + (GS / 4) c + 8 j and the seven after it. Weight
+// rows are KB / 2 bytes with the TMA's swizzle of that width, rows of X boxes of 64 k,
+// swizzled (X_SWIZZLED) or as they are.
+template <int GS, int KB>
 __device__ __forceinline__ void load_words(uint32_t w_row, int row, int sub, int cq, uint32_t (&w)[GS / 32]) {
     const int byte = GS / 2 * sub + GS / 8 * cq;
-    const uint32_t at = w_row + ((((byte >> 4) ^ (row >> 1)) & 3) << 4) + (byte & 15);
+    const uint32_t at = w_row + (((byte >> 4) ^ (KB == 256 ? row & 7 : (row >> 1) & 3)) << 4) + (byte & 15);
     if constexpr (GS == 128)
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
     else if constexpr (GS == 64)
@@ -113,11 +116,11 @@ __device__ __forceinline__ void load_words(uint32_t w_row, int row, int sub, int
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at));
 }
 // The B operands of word j: (b0, b1) of its two steps. `rows` rows of X a box.
-template <int GS>
+template <int GS, bool X_SWIZZLED>
 __device__ __forceinline__ void load_x(uint32_t x_tile, int rows, int row, int sub, int cq, int j, uint32_t (&b)[4]) {
     const int k = GS * sub + GS / 4 * cq + 8 * j;
     uint32_t x0, x1, x2, x3;
-    ld_shared_v4(x_tile + ((k >> 6) * rows + row) * 128 + ((((k >> 3) ^ row) & 7) << 4), x0, x1, x2, x3);
+    ld_shared_v4(x_tile + ((k >> 6) * rows + row) * 128 + ((((k >> 3) ^ (X_SWIZZLED ? row : 0)) & 7) << 4), x0, x1, x2, x3);
     b[0] = zip16<0>(x0, x2), b[1] = zip16<1>(x0, x2), b[2] = zip16<0>(x1, x3), b[3] = zip16<1>(x1, x3);
 }
 __device__ __forceinline__ void expand_weights(uint32_t w, uint32_t z2, uint32_t (&a)[4]) {
@@ -127,13 +130,32 @@ __device__ __forceinline__ void expand_weights(uint32_t w, uint32_t z2, uint32_t
     a[3] = fma_bf16x2(i4_pair<3>(w), 0x3F803F80u, z2);
 }
 
-// acc += the block's groups, each scaled, for weight rows row0 .. row0 + 16 MR - 1
-// of the staged ROWS and 8 NT rows of X from x_row0 of the staged X_ROWS. `group`:
-// the block's first group; k_left: k from the block's start to K's end.
-template <int GS, int MR, int NT, int ROWS, int X_ROWS, bool ZEROS>
-__device__ __forceinline__ void block_product(uint32_t w_tile, uint32_t x_tile, const uint8_t *sc, int row0, int x_row0, int groups,
-                                              int group, int64_t k_left, int gq, int cq, float (&acc)[MR][NT][4]) {
-    constexpr int kSub = kBlockK / GS;
+// Block -> its first group, and on to the next: a block has several groups, or a group several blocks.
+template <int GS>
+struct GroupCursor {
+    int group, left;         // left: blocks of the group still to come, this one included
+    __device__ __forceinline__ GroupCursor(const GemmI4Params &p, int blk) {
+        const int per = GS < kBlockK ? 1 : p.group / kBlockK;
+        group = GS < kBlockK ? blk * (kBlockK / GS) : blk / per;
+        left = per - (GS < kBlockK ? 0 : blk % per);
+    }
+    __device__ __forceinline__ void next(const GemmI4Params &p) {
+        if (GS < kBlockK)
+            group += kBlockK / GS;
+        else if (--left == 0)
+            ++group, left = p.group / kBlockK;
+    }
+};
+
+// acc += KB staged k, each group scaled, for weight rows row0 .. row0 + 16 MR - 1 of
+// the staged ROWS and 8 NT rows of X from x_row0 of the staged x_rows (x_mask: rows
+// that are not there repeat others; their columns are not stored). `g`: the first
+// group; k_left: k from the first one to K's end.
+template <int GS, int KB, int MR, int NT, int ROWS, bool X_SWIZZLED, bool ZEROS>
+__device__ __forceinline__ void product(uint32_t w_tile, uint32_t x_tile, const uint8_t *sc, int row0, int x_rows, int x_row0, int x_mask,
+                                        int groups, const GroupCursor<GS> &g, int64_t k_left, int gq, int cq,
+                                        float (&acc)[MR][NT][4]) {
+    constexpr int kSub = KB / GS;
 #pragma unroll
     for (int sub = 0; sub < kSub; ++sub) {
         uint32_t w[MR][2][GS / 32];
@@ -145,8 +167,10 @@ __device__ __forceinline__ void block_product(uint32_t w_tile, uint32_t x_tile, 
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int row = row0 + 16 * m + 8 * h + gq;
-                load_words<GS>(w_tile + row * (kBlockK / 2), row, sub, cq, w[m][h]);
-                read_scale<GS, ROWS, ZEROS>(sc, row, row * groups + group, sub, kSub == 1 || sub * GS < k_left, s[m][h], z2[m][h]);
+                load_words<GS, KB>(w_tile + row * (KB / 2), row, sub, cq, w[m][h]);
+                // a group of more than 128 k: the second 128 are the next group's only where the first one's is done
+                const int at = GS < kBlockK || sub == 0 ? sub : g.left == 1;
+                read_scale<GS, KB, ROWS, ZEROS>(sc, row, row * groups + g.group, at, kSub == 1 || sub * GS < k_left, s[m][h], z2[m][h]);
             }
         }
 #pragma unroll
@@ -159,7 +183,7 @@ __device__ __forceinline__ void block_product(uint32_t w_tile, uint32_t x_tile, 
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 uint32_t b[4];
-                load_x<GS>(x_tile, X_ROWS, x_row0 + 8 * t + gq, sub, cq, j, b);
+                load_x<GS, X_SWIZZLED>(x_tile, x_rows, x_row0 + 8 * t + (gq & x_mask), sub, cq, j, b);
 #pragma unroll
                 for (int m = 0; m < MR; ++m) {
                     if (j == 0)
@@ -181,23 +205,6 @@ __device__ __forceinline__ void block_product(uint32_t w_tile, uint32_t x_tile, 
     }
 }
 
-// Block -> its first group, and on to the next: a block has several groups, or a group several blocks.
-template <int GS>
-struct GroupCursor {
-    int group, left;         // left: blocks of the group still to come, this one included
-    __device__ __forceinline__ GroupCursor(const GemmI4Params &p, int blk) {
-        const int per = GS < kBlockK ? 1 : p.group / kBlockK;
-        group = GS < kBlockK ? blk * (kBlockK / GS) : blk / per;
-        left = per - (GS < kBlockK ? 0 : blk % per);
-    }
-    __device__ __forceinline__ void next(const GemmI4Params &p) {
-        if (GS < kBlockK)
-            group += kBlockK / GS;
-        else if (--left == 0)
-            ++group, left = p.group / kBlockK;
-    }
-};
-
 __device__ __forceinline__ void store_y(const GemmI4Params &p, int64_t m, int64_t n, float y) {
     if (m < p.M && n < p.N && BI_IN_BOUNDS(m * p.ldy + n < (p.M - 1) * p.ldy + p.N, p.status))
         p.Y[m * p.ldy + n] = static_cast<uint16_t>(pack_bf16x2(__float_as_uint(y), 0u) & 0xFFFFu);
@@ -205,33 +212,27 @@ __device__ __forceinline__ void store_y(const GemmI4Params &p, int64_t m, int64_
 
 // ---------------------------------------------------------------- few rows ---
 
-// blocks of a warp in shared memory, such that two CTAs fit an SM
-template <int MR>
-constexpr int rows_ring() { return MR == 1 ? 3 : 2; }
-template <int MR, int NT>
-constexpr int rows_stage() { return MR * 16 * (kBlockK / 2) + NT * 8 * kBlockK * 2; }   // W, X
-template <int MR, int NT>
-constexpr int rows_sums() { return 16 * MR * (8 * NT + 1); }   // floats of a warp's sums
-template <int GS, int MR, int NT>
-constexpr int rows_warp() {
-    return rows_ring<MR>() * (rows_stage<MR, NT>() + ScaleTile<GS>::bytes(16 * MR)) + 2 * rows_sums<MR, NT>() * 4;
-}
+// CTAs of 32 weight rows walk the tiles; a warp's ring of kUnitK k runs on from one tile to the next. A wide
+// stage and two row tiles a warp spread the waits, the copies' issue and the operands of X over 64 operand words.
+constexpr int kRowsN = 32, kRing = 2;          // (two CTAs fit an SM)
+constexpr int kRowsW = kRowsN * (kUnitK / 2), kRowsCols = 9, kRowsSums = kRowsN * kRowsCols;   // sums: floats of a warp
+template <int GS>
+constexpr int rows_stage(int x_rows) { return kRowsW + (x_rows * kUnitK * 2 + ScaleTile<GS, kUnitK>::bytes(kRowsN) + 1023) / 1024 * 1024; }
+template <int GS>
+constexpr int rows_warp(int x_rows) { return kRing * rows_stage<GS>(x_rows) + 2 * kRowsSums * 4; }
 
-// CTAs walk the tiles of 16 MR weight rows; a warp's ring runs on from one tile to the next.
-template <int GS, int MR, int NT, bool ZEROS>
+template <int GS, bool ZEROS>
 __global__ void __launch_bounds__(32 * kMaxSegments)
 gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmI4Params p) {
-    constexpr int kRing = rows_ring<MR>(), kStage = rows_stage<MR, NT>(), kScaleBytes = ScaleTile<GS>::bytes(16 * MR);
-    constexpr int kWBytes = MR * 16 * (kBlockK / 2), kXBytes = NT * 8 * kBlockK * 2;
-    constexpr int kSums = rows_sums<MR, NT>(), kCols = 8 * NT + 1;
+    constexpr int kCols = kRowsCols, kSums = kRowsSums;
+    const int x_bytes = p.x_rows * kUnitK * 2, stage_bytes = rows_stage<GS>(p.x_rows);
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ uint64_t full[kMaxSegments][kRing];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, cq = lane & 3;
-    uint8_t *ring = smem + warp * kRing * kStage;
-    uint8_t *scales = smem + p.segments * kRing * kStage + warp * kRing * kScaleBytes;
-    float *sums = reinterpret_cast<float *>(smem + p.segments * kRing * (kStage + kScaleBytes));   // [2][segments][kSums]
+    uint8_t *ring = smem + warp * kRing * stage_bytes;                                     // a stage: W, X, scales
+    float *sums = reinterpret_cast<float *>(smem + p.segments * kRing * stage_bytes);   // [2][segments][kSums]
     if (lane == 0) {
         for (int k = 0; k < kRing; ++k) mbar_init(&full[warp][k], 33);   // 32 lanes' scale copies, and the TMA's bytes
         fence_mbar_init();
@@ -241,27 +242,29 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     __syncwarp();
     grid_dep_wait();      // earlier work of the stream is complete and visible
     grid_dep_launch();
-    const int tiles = static_cast<int>((p.N + 16 * MR - 1) / (16 * MR));
-    const int b0 = static_cast<int>(static_cast<int64_t>(warp) * p.blocks / p.segments);
-    const int b1 = static_cast<int>(static_cast<int64_t>(warp + 1) * p.blocks / p.segments);
-    const GroupCursor<GS> g0(p, b0);
-    // the next block to be copied, its group, and its slot
+    const int tiles = static_cast<int>((p.N + kRowsN - 1) / kRowsN);
+    const int b0 = static_cast<int>(static_cast<int64_t>(warp) * p.units / p.segments);
+    const int b1 = static_cast<int>(static_cast<int64_t>(warp + 1) * p.units / p.segments);
+    const GroupCursor<GS> g0(p, 2 * b0);
+    // the next unit to be copied, its group, and its slot
     int ft = blockIdx.x, fb = b0, fs = 0;
     GroupCursor<GS> fg = g0;
-    int64_t row_e = static_cast<int64_t>(ft) * (16 * MR) * p.groups;   // element (the tile's first row, group 0)
-    const int64_t step_e = static_cast<int64_t>(gridDim.x) * (16 * MR) * p.groups;
+    int64_t row_e = static_cast<int64_t>(ft) * kRowsN * p.groups;   // element (the tile's first row, group 0)
+    const int64_t step_e = static_cast<int64_t>(gridDim.x) * kRowsN * p.groups;
     auto fill = [&]() {
         if (ft >= tiles) return;
-        uint8_t *dst = ring + fs * kStage;
+        uint8_t *dst = ring + fs * stage_bytes;
         uint64_t *bar = &full[warp][fs];
         if (lane == 0) {
-            mbar_arrive_expect_tx(bar, kWBytes + kXBytes);
-            tma_load_2d(dst, &tmW, bar, fb * (kBlockK / 2), ft * (16 * MR));
-            tma_load_2d(dst + kWBytes, &tmX, bar, fb * kBlockK, 0);
-            tma_load_2d(dst + kWBytes + kXBytes / 2, &tmX, bar, fb * kBlockK + 64, 0);
+            mbar_arrive_expect_tx(bar, kRowsW + x_bytes);
+            tma_load_2d(dst, &tmW, bar, fb * (kUnitK / 2), ft * kRowsN);
+#pragma unroll
+            for (int k = 0; k < kUnitK / 64; ++k)
+                tma_load_2d(dst + kRowsW + k * (x_bytes / (kUnitK / 64)), &tmX, bar, fb * kUnitK + 64 * k, 0);
         }
-        stage_scales<GS, 16 * MR, 32, ZEROS>(p, smem_u32(scales + fs * kScaleBytes), bar, row_e + fg.group, lane);
+        stage_scales<GS, kUnitK, kRowsN, 32, ZEROS>(p, smem_u32(dst + kRowsW + x_bytes), bar, row_e + fg.group, lane);
         if (++fs == kRing) fs = 0;
+        fg.next(p);
         fg.next(p);
         if (++fb == b1) fb = b0, fg = g0, ft += gridDim.x, row_e += step_e;
     };
@@ -270,22 +273,22 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     uint32_t parity = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
-        const int64_t n0 = static_cast<int64_t>(tile) * (16 * MR);
-        float acc[MR][NT][4];
+        const int64_t n0 = static_cast<int64_t>(tile) * kRowsN;
+        float acc[2][1][4];
 #pragma unroll
-        for (int m = 0; m < MR; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[m][t][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) acc[m][0][e] = 0.0f;
         GroupCursor<GS> g = g0;
         for (int blk = b0; blk < b1 && ok; ++blk) {
             ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][slot], parity, nullptr));
             __syncwarp();
             if (!ok) break;
-            const uint32_t st = smem_u32(ring + slot * kStage);
-            block_product<GS, MR, NT, 16 * MR, 8 * NT, ZEROS>(st, st + kWBytes, scales + slot * kScaleBytes, 0, 0, p.groups, g.group,
-                                                              p.K - static_cast<int64_t>(blk) * kBlockK, gq, cq, acc);
+            const uint8_t *st = ring + slot * stage_bytes;
+            product<GS, kUnitK, 2, 1, kRowsN, false, ZEROS>(smem_u32(st), smem_u32(st) + kRowsW, st + kRowsW + x_bytes, 0, p.x_rows, 0,
+                                                            p.x_rows - 1, p.groups, g, p.K - static_cast<int64_t>(blk) * kUnitK, gq, cq,
+                                                            acc);
+            g.next(p);
             g.next(p);
             __syncwarp();                                  // every lane has read the slot
             fill();
@@ -294,14 +297,12 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         // the segments' sums, added in order
         float *mine = sums + (buf * p.segments + warp) * kSums;
 #pragma unroll
-        for (int m = 0; m < MR; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mine[(16 * m + gq + 8 * (e >> 1)) * kCols + 8 * t + 2 * cq + (e & 1)] = acc[m][t][e];
+            for (int e = 0; e < 4; ++e) mine[(16 * m + gq + 8 * (e >> 1)) * kCols + 2 * cq + (e & 1)] = acc[m][0][e];
         if (__syncthreads_or(!ok)) break;                  // (two buffers: the one before last has been read)
-        for (int i = threadIdx.x; i < 16 * MR * 8 * NT; i += blockDim.x) {
-            const int r = i % (16 * MR), t = i / (16 * MR);
+        for (int i = threadIdx.x; i < kRowsN * 8; i += blockDim.x) {
+            const int r = i % kRowsN, t = i / kRowsN;
             if (t >= p.M) break;
             const float *v = sums + buf * p.segments * kSums + r * kCols + t;
             float y = v[0];
@@ -328,13 +329,13 @@ constexpr int tile_stage() { return kTileW + TM * kBlockK * 2; }
 template <int TM>
 constexpr int tile_stages() { return TM == 64 ? 3 : 5; }
 template <int GS, int TM>
-constexpr int tile_smem() { return 1024 + tile_stages<TM>() * (tile_stage<TM>() + ScaleTile<GS>::bytes(kTileN)); }
+constexpr int tile_smem() { return 1024 + tile_stages<TM>() * (tile_stage<TM>() + ScaleTile<GS, kBlockK>::bytes(kTileN)); }
 
 // One segment a CTA (a cluster's ranks in segment order), or all segments in turn (SPLIT false).
 template <int GS, int TM, bool SPLIT, bool ZEROS>
 __global__ void __launch_bounds__(kTileThreads, TM == 64 && !SPLIT ? 1 : 2)
 gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmI4Params p) {
-    constexpr int kScaleBytes = ScaleTile<GS>::bytes(kTileN), kTileStage = tile_stage<TM>(), kTileStages = tile_stages<TM>();
+    constexpr int kScaleBytes = ScaleTile<GS, kBlockK>::bytes(kTileN), kTileStage = tile_stage<TM>(), kTileStages = tile_stages<TM>();
     constexpr int kTileM = TM, WM = TM == 16 ? 1 : 2, MR = WM, NT = TM / 8 / WM;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -356,8 +357,8 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     const int64_t tile = SPLIT ? blockIdx.x / p.segments : blockIdx.x;
     const int64_t tiles_m = (p.M + kTileM - 1) / kTileM;
     const int64_t m0 = tile % tiles_m * kTileM, n0 = tile / tiles_m * kTileN;
-    const int first = SPLIT ? static_cast<int>(static_cast<int64_t>(rank) * p.blocks / p.segments) : 0;
-    const int last = SPLIT ? static_cast<int>(static_cast<int64_t>(rank + 1) * p.blocks / p.segments) : p.blocks;
+    const int first = SPLIT ? 2 * static_cast<int>(static_cast<int64_t>(rank) * p.units / p.segments) : 0;
+    const int last = SPLIT ? min(p.blocks, 2 * static_cast<int>(static_cast<int64_t>(rank + 1) * p.units / p.segments)) : p.blocks;
     GroupCursor<GS> g(p, first), fg = g;                   // of the block at work, of the next to be copied
     auto fill = [&](int blk) {
         const int slot = (blk - first) % kTileStages;
@@ -368,7 +369,7 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
             tma_load_2d(dst + kTileW, &tmX, &full[slot], blk * kBlockK, static_cast<int32_t>(m0));
             tma_load_2d(dst + kTileW + kTileM * 128, &tmX, &full[slot], blk * kBlockK + 64, static_cast<int32_t>(m0));
         }
-        stage_scales<GS, kTileN, kTileThreads, ZEROS>(p, smem_u32(scales + slot * kScaleBytes), &full[slot], n0 * p.groups + fg.group, tid);
+        stage_scales<GS, kBlockK, kTileN, kTileThreads, ZEROS>(p, smem_u32(scales + slot * kScaleBytes), &full[slot], n0 * p.groups + fg.group, tid);
         fg.next(p);
     };
     for (int blk = first; blk < last && blk < first + kTileStages - 1; ++blk) fill(blk);
@@ -383,7 +384,7 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     };
     clear(acc);
     int seg = 0;                                           // SPLIT false: the segment at work, and its end
-    int seg_end = p.blocks / p.segments;
+    int seg_end = min(p.blocks, 2 * (p.units / p.segments));
     bool ok = true;
     for (int blk = first; blk < last; ++blk) {
         const int i = blk - first, slot = i % kTileStages;
@@ -398,8 +399,8 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         }
         if (blk + kTileStages - 1 < last) fill(blk + kTileStages - 1);
         const uint32_t st = smem_u32(smem + slot * kTileStage);
-        block_product<GS, MR, NT, kTileN, kTileM, ZEROS>(st, st + kTileW, scales + slot * kScaleBytes, 16 * MR * wn, 8 * NT * wm, p.groups,
-                                                         g.group, p.K - static_cast<int64_t>(blk) * kBlockK, gq, cq, acc);
+        product<GS, kBlockK, MR, NT, kTileN, true, ZEROS>(st, st + kTileW, scales + slot * kScaleBytes, 16 * MR * wn, kTileM, 8 * NT * wm, 7,
+                                                          p.groups, g, p.K - static_cast<int64_t>(blk) * kBlockK, gq, cq, acc);
         g.next(p);
         if (!SPLIT && blk + 1 == seg_end) {
 #pragma unroll
@@ -410,7 +411,7 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                     for (int e = 0; e < 4; ++e) tot[m][t][e] = seg == 0 ? acc[m][t][e] : tot[m][t][e] + acc[m][t][e];
             clear(acc);
             ++seg;
-            seg_end = static_cast<int>(static_cast<int64_t>(seg + 1) * p.blocks / p.segments);
+            seg_end = min(p.blocks, 2 * static_cast<int>(static_cast<int64_t>(seg + 1) * p.units / p.segments));
         }
     }
     // the tile's sums through shared memory, [row of X][weight row] with the rows four apart in banks
@@ -461,18 +462,18 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
 
 // ----------------------------------------------------------------- launches ---
 
-template <int GS, int MR, int NT, bool ZEROS>
+template <int GS, bool ZEROS>
 bi_status launch_rows(const CUtensorMap &tmW, const CUtensorMap &tmX, const GemmI4Params &p, int sms, cudaStream_t s) {
     static unsigned long long configured = 0;
-    constexpr int most = 1024 + kMaxSegments * rows_warp<GS, MR, NT>();
+    constexpr int most = 1024 + kMaxSegments * rows_warp<GS>(8);
     static_assert(most <= 232448 - 1024, "one CTA's shared memory");
-    if (ensure_smem_attr(reinterpret_cast<const void *>(gemm_int4_rows_kernel<GS, MR, NT, ZEROS>), most, &configured) != BI_OK)
+    if (ensure_smem_attr(reinterpret_cast<const void *>(gemm_int4_rows_kernel<GS, ZEROS>), most, &configured) != BI_OK)
         return BI_ERR_CUDA;
     // as many CTAs as the shared memory of the SMs takes at once
-    const int64_t tiles = (p.N + 16 * MR - 1) / (16 * MR);
-    const int smem = 1024 + p.segments * rows_warp<GS, MR, NT>(), fit = 232448 / (smem + 2048);
-    const int64_t most_ctas = static_cast<int64_t>(sms) * (fit > 16 ? 16 : fit);
-    return launch_pdl(gemm_int4_rows_kernel<GS, MR, NT, ZEROS>, dim3(static_cast<unsigned>(tiles < most_ctas ? tiles : most_ctas)),
+    const int64_t tiles = (p.N + kRowsN - 1) / kRowsN;
+    const int smem = 1024 + p.segments * rows_warp<GS>(p.x_rows), fit = 232448 / (smem + 2048);
+    const int64_t most_ctas = static_cast<int64_t>(sms) * (fit > 8 ? 8 : fit);
+    return launch_pdl(gemm_int4_rows_kernel<GS, ZEROS>, dim3(static_cast<unsigned>(tiles < most_ctas ? tiles : most_ctas)),
                       dim3(32 * p.segments), smem, s, tmW, tmX, p);
 }
 
@@ -515,15 +516,14 @@ template <int GS, bool ZEROS>
 bi_status launch_group(const void *X, int64_t ldx, const uint8_t *W, GemmI4Params &p, int sms, cudaStream_t s) {
     const bool rows = p.M <= 8;
     const int tm = p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64;
-    // 32 weight rows a CTA halve the reads of X; 16 where that would leave SMs without a CTA
-    const int mr = p.N >= 32 * 2 * static_cast<int64_t>(sms) ? 2 : 1;
+    p.x_rows = p.M <= 2 ? static_cast<int>(p.M) : p.M <= 4 ? 4 : 8;
     CUtensorMap tmW{}, tmX{};
-    if (make_tmap_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, p.K / 2, p.N, p.K / 2, kBlockK / 2, rows ? 16 * mr : kTileN,
-                     CU_TENSOR_MAP_SWIZZLE_64B) != BI_OK ||
-        make_tmap_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, p.K, p.M, ldx * 2, 64, rows ? 8 : tm,
-                     CU_TENSOR_MAP_SWIZZLE_128B) != BI_OK)
+    if (make_tmap_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, p.K / 2, p.N, p.K / 2, (rows ? kUnitK : kBlockK) / 2, rows ? kRowsN : kTileN,
+                     rows ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) != BI_OK ||
+        make_tmap_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, p.K, p.M, ldx * 2, 64, rows ? p.x_rows : tm,
+                     rows ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B) != BI_OK)
         return BI_ERR_CUDA;
-    if (rows) return mr == 1 ? launch_rows<GS, 1, 1, ZEROS>(tmW, tmX, p, sms, s) : launch_rows<GS, 2, 1, ZEROS>(tmW, tmX, p, sms, s);
+    if (rows) return launch_rows<GS, ZEROS>(tmW, tmX, p, sms, s);
     if (tm == 16) return launch_tiles<GS, 16, ZEROS>(tmW, tmX, p, sms, s);
     if (tm == 32) return launch_tiles<GS, 32, ZEROS>(tmW, tmX, p, sms, s);
     return launch_tiles<GS, 64, ZEROS>(tmW, tmX, p, sms, s);
@@ -547,7 +547,8 @@ bi_status launch_gemm_int4(const void *X, int64_t ldx, const uint8_t *W, const v
     p.s_last = N * p.groups / 2 - 1, p.z_last = N * p.groups / 4 - 1;   // (N % 8 == 0)
     p.group = static_cast<int32_t>(group);
     p.blocks = static_cast<int32_t>((K + kBlockK - 1) / kBlockK);
-    p.segments = p.blocks < 4 ? 1 : p.blocks / 4 > kMaxSegments ? kMaxSegments : p.blocks / 4;
+    p.units = static_cast<int32_t>((K + kUnitK - 1) / kUnitK);
+    p.segments = p.units < 4 ? 1 : p.units / 2 > kMaxSegments ? kMaxSegments : p.units / 2;
     p.status = device_status_word();
     const int sms = info->sm_count;
     if (group == 32) return zeros ? launch_group<32, true>(X, ldx, W, p, sms, s) : launch_group<32, false>(X, ldx, W, p, sms, s);
