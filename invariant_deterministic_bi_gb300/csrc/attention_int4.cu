@@ -35,7 +35,9 @@ constexpr int kHalfBytes = kCodeBytes + kScaleBytes;   // a chunk's K (or V): 9 
 constexpr int kWarpBytes = 2 * kHalfBytes;
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 constexpr int kRecord = kD + 2;                // floats of a chunk result: m, l, o
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 128;             // and a warp that loads
+constexpr int kMergeTile = 32, kMergeRing = 8; // chunk results of a tile, tiles on the way at most
+constexpr int kMergeStage = (kMergeTile * kRecord * 4 + 16 + 15) / 16 * 16;
 // Extend takes this split for at most so many query rows (tokens x shared heads) a sequence, and chunk results of
 // at most so many bytes.
 constexpr int kFewRows = 64;
@@ -454,70 +456,112 @@ attn_split_int4_kernel(const SplitParams p) {
     }
 }
 
-// Merges the chunk results of one (query token, query head) in chunk order, thread d its dimension d. The chunks come
-// in tiles of 32, the next tile's loads in flight while one is merged. The running maximum before a chunk is a
-// prefix maximum (exact in any order), so warp 0 prepares the tile's factors in parallel; what is left in order is
-// one product and one fused multiply-add a chunk.
+// Merges the chunk results of one (query token, query head) in chunk order, thread d its dimension d (warps 0 .. 3).
+// The records of a head lie one after the other: warp 4 keeps up to `ring` tiles of 32 on the way to shared memory.
+// The running maximum before a chunk is a prefix maximum (exact in any order), so it also prepares the next tile's
+// factors in parallel, while the others merge: one product and one fused multiply-add a chunk in order. With a long
+// sequence's loads so far ahead, its merge is bound by those operations and not by a tile's load latency.
 template <bool EXT>
-__global__ void __launch_bounds__(kMergeThreads)
-attn_merge_int4_kernel(const SplitParams p) {
+__global__ void __launch_bounds__(kMergeThreads + 32)
+attn_merge_int4_kernel(const SplitParams p, int ring) {
+    constexpr int kTile = kMergeTile;
+    extern __shared__ __align__(16) uint8_t tiles[];       // [ring][kMergeStage]
+    __shared__ float fa[2][kTile], fb[2][kTile], fl[2][kTile];   // alpha, beta, l of a tile's chunks
+    __shared__ uint64_t full[kMergeRing];
+    __shared__ int failed;
+    const int d = threadIdx.x, lane = d & 31;
+    const bool loader = d >= kMergeThreads;
+    if (d == kMergeThreads) {
+        for (int k = 0; k < ring; ++k) mbar_init(&full[k], 1);
+        fence_mbar_init();
+        failed = 0;
+    }
+    __syncthreads();
     grid_dep_wait();      // earlier work of the stream is complete and visible
     grid_dep_launch();
-    constexpr int kTile = 32;
-    __shared__ float fa[2][kTile], fb[2][kTile], fl[2][kTile];   // alpha, beta, l of a tile's chunks
-    const int h = blockIdx.x % p.Hq, d = threadIdx.x;
+    const int h = blockIdx.x % p.Hq;
     const int64_t y = blockIdx.x / p.Hq, b = EXT ? y / p.max_q : y;
     const int i = EXT ? static_cast<int>(y % p.max_q) : 0;
     int64_t row;
     int qlen, len0;
     if (!sequence<EXT>(p, b, row, qlen, len0, false) || i >= qlen) return;
     row += i;
-    const int nc = (len0 + i + kChunk - 1) / kChunk;
+    const int nc = (len0 + i + kChunk - 1) / kChunk, nt = (nc + kTile - 1) / kTile;
     if (!BI_IN_BOUNDS(nc <= p.chunks && row < (EXT ? p.total_q : p.batch), p.status)) return;
     const float *w = p.ws + (row * p.Hq + h) * static_cast<int64_t>(p.chunks) * kRecord;
-    float o = 0.0f, l = 0.0f, m_run = -INFINITY;           // m_run: warp 0's running maximum
-    float ov[kTile], mc = -INFINITY, lc = 0.0f;
-    auto load_tile = [&](int c0, float (&v)[kTile], float &tm, float &tl) {
-        const int nt = min(kTile, nc - c0);
-        const float *t = w + static_cast<int64_t>(c0) * kRecord;
-#pragma unroll
-        for (int c = 0; c < kTile; ++c) v[c] = c < nt ? t[c * kRecord + 2 + d] : 0.0f;
-        tm = d < nt ? t[d * kRecord] : -INFINITY;          // read by warp 0 only (nt <= 32)
-        tl = d < nt ? t[d * kRecord + 1] : 0.0f;
+    const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(w) & 15u) / 4);   // copies begin at 16 bytes
+    // floats of tile t's stage; where they end inside 16 bytes, the last two are not part of the copy (it would read
+    // past the workspace) but loaded by hand
+    auto floats = [&](int t) { return min(kTile, nc - t * kTile) * kRecord + skew; };
+    auto fill = [&](int t) {                               // one lane
+        const uint32_t bytes = static_cast<uint32_t>(floats(t) & ~3) * 4;
+        mbar_arrive_expect_tx(&full[t % ring], bytes);
+        bulk_load(tiles + t % ring * kMergeStage, w - skew + static_cast<int64_t>(t) * kTile * kRecord, bytes, &full[t % ring]);
     };
-    load_tile(0, ov, mc, lc);
-    for (int c0 = 0, buf = 0; c0 < nc; c0 += kTile, buf ^= 1) {
-        const int nt = min(kTile, nc - c0);
-        if (d < 32) {
-            float incl = mc;                               // max(m_c0 .. m_c) over the tile
+    auto tile_at = [&](int t) { return reinterpret_cast<const float *>(tiles + t % ring * kMergeStage) + skew; };
+    float m_run = -INFINITY;                               // the loader's running maximum
+    auto factors = [&](int t) {                            // warp 4: tile t's factors, once it has landed
+        if (!mbar_wait(&full[t % ring], (t / ring) & 1, nullptr)) failed = 1;
+        __syncwarp();
+        const int n = floats(t);
+        if ((n & 2) && lane < 2)
+            reinterpret_cast<float *>(tiles + t % ring * kMergeStage)[n - 2 + lane] =
+                w[static_cast<int64_t>(t) * kTile * kRecord + n - 2 + lane - skew];
+        const float *rec = tile_at(t) + lane * kRecord;
+        const bool in = t * kTile + lane < nc;
+        const float mc = in ? rec[0] : -INFINITY, lc = in ? rec[1] : 0.0f;
+        float incl = mc;                                   // max(m_c0 .. m_c) over the tile
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const float v = __shfl_up_sync(0xffffffffu, incl, off);
-                if (d >= off) incl = fmaxf(incl, v);
-            }
-            float before = __shfl_up_sync(0xffffffffu, incl, 1);
-            before = d == 0 ? m_run : fmaxf(m_run, before);
-            float mn, a, bt;
-            merge_factors(before, mc, mn, a, bt);
-            if (d < nt) fa[buf][d] = a, fb[buf][d] = bt, fl[buf][d] = lc;
-            m_run = fmaxf(m_run, __shfl_sync(0xffffffffu, incl, 31));
+        for (int off = 1; off < 32; off <<= 1) {
+            const float v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl = fmaxf(incl, v);
         }
-        __syncthreads();                                   // (two buffers: the one before last is free)
-        float nv[kTile];
-        const bool more = c0 + kTile < nc;
-        if (more) load_tile(c0 + kTile, nv, mc, lc);
-#pragma unroll
-        for (int c = 0; c < kTile; ++c)
-            if (c < nt) {
-                o = merge_value(o, ov[c], fa[buf][c], fb[buf][c]);
-                l = merge_value(l, fl[buf][c], fa[buf][c], fb[buf][c]);
+        float before = __shfl_up_sync(0xffffffffu, incl, 1);
+        before = lane == 0 ? m_run : fmaxf(m_run, before);
+        float mn, a, bt;
+        merge_factors(before, mc, mn, a, bt);
+        fa[t & 1][lane] = a, fb[t & 1][lane] = bt, fl[t & 1][lane] = lc;
+        m_run = fmaxf(m_run, __shfl_sync(0xffffffffu, incl, 31));
+    };
+    if (loader) {
+        if (lane == 0)
+            for (int t = 0; t < nt && t < ring; ++t) fill(t);
+        __syncwarp();
+        factors(0);
+    }
+    float o = 0.0f, l = 0.0f;
+    for (int t = 0; t < nt; ++t) {
+        __syncthreads();                                   // tile t's factors are there, tile t - 1 is merged
+        if (failed) {                                      // a wait ran out: report; the copies in flight get another limit
+            if (d == kMergeThreads) {
+                atomicOr(p.status, kDevTimeout);
+                for (int k = t; k < nt && k < t + ring; ++k) mbar_wait(&full[k % ring], (k / ring) & 1, nullptr);
             }
-        if (more) {
+            return;
+        }
+        if (loader) {
+            if (lane == 0 && t > 0 && t - 1 + ring < nt) fill(t - 1 + ring);
+            __syncwarp();
+            if (t + 1 < nt) factors(t + 1);
+        } else {
+            const float *rec = tile_at(t) + 2 + d;
+            const int n = min(kTile, nc - t * kTile);
+            if (n == kTile) {
 #pragma unroll
-            for (int c = 0; c < kTile; ++c) ov[c] = nv[c];
+                for (int c = 0; c < kTile; ++c) {
+                    o = merge_value(o, rec[c * kRecord], fa[t & 1][c], fb[t & 1][c]);
+                    l = merge_value(l, fl[t & 1][c], fa[t & 1][c], fb[t & 1][c]);
+                }
+            } else {
+                for (int c = 0; c < n; ++c) {
+                    o = merge_value(o, rec[c * kRecord], fa[t & 1][c], fb[t & 1][c]);
+                    l = merge_value(l, fl[t & 1][c], fa[t & 1][c], fb[t & 1][c]);
+                }
+            }
         }
     }
-    p.O[(row * p.Hq + h) * kD + d] = static_cast<uint16_t>(pack_bf16x2(__float_as_uint(__fdiv_rn(o, l)), 0u) & 0xFFFFu);
+    if (!loader)
+        p.O[(row * p.Hq + h) * kD + d] = static_cast<uint16_t>(pack_bf16x2(__float_as_uint(__fdiv_rn(o, l)), 0u) & 0xFFFFu);
 }
 
 template <int G, bool EXT, bool BLOCKS>
@@ -558,7 +602,12 @@ bi_status launch_few(SplitParams &p, cudaStream_t s) {
     }
 #undef BI_SPLIT
     if (st != BI_OK) return st;
-    return launch_pdl(attn_merge_int4_kernel<EXT>, dim3(static_cast<unsigned>(merges)), dim3(kMergeThreads), 0, s, p);
+    static unsigned long long configured = 0;
+    if (ensure_smem_attr(reinterpret_cast<const void *>(attn_merge_int4_kernel<EXT>), kMergeRing * kMergeStage, &configured) != BI_OK)
+        return BI_ERR_CUDA;
+    const int tiles = (p.chunks + kMergeTile - 1) / kMergeTile, ring = tiles < kMergeRing ? tiles : kMergeRing;
+    return launch_pdl(attn_merge_int4_kernel<EXT>, dim3(static_cast<unsigned>(merges)), dim3(kMergeThreads + 32), ring * kMergeStage, s,
+                      p, ring);
 }
 
 }  // namespace
