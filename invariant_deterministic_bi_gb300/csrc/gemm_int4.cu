@@ -17,10 +17,10 @@
 // units into S segments; a segment's groups (of longer ones, each 128 k) are added
 // in ascending order, and the segments' sums in order. The number of rows decides only who computes
 // what:
-//   - few rows (gemm_int4_rows_kernel, M <= 8): a warp a segment, the CTA's
-//     warps share 16 or 32 weight rows; every warp has its own ring of TMA
+//   - few rows (gemm_int4_rows_kernel, M <= 16): a warp a segment, the CTA's
+//     warps share 32 weight rows; every warp has its own ring of TMA
 //     copies and nobody waits for anybody before the final sum;
-//   - more (gemm_int4_tile_kernel): a CTA a tile of 128 weight rows x 16, 32 or 64
+//   - more (gemm_int4_tile_kernel): a CTA a tile of 128 weight rows x 32 or 64
 //     rows of X, both staged by TMA for all warps; it walks the segments, or, where the
 //     tiles would not fill the GPU, the CTAs of a cluster take one each.
 #include "attn_common.cuh"
@@ -212,20 +212,28 @@ __device__ __forceinline__ void store_y(const GemmI4Params &p, int64_t m, int64_
 
 // ---------------------------------------------------------------- few rows ---
 
-// CTAs of 32 weight rows walk the tiles; a warp's ring of kUnitK k runs on from one tile to the next. A wide
-// stage and two row tiles a warp spread the waits, the copies' issue and the operands of X over 64 operand words.
+// CTAs of 32 weight rows walk the tiles; a warp's ring of kRing stages runs on from one tile to the next. Two row
+// tiles a warp, and KB = 256 k a stage where X has at most eight rows, spread the waits, the copies' issue and the
+// operands of X over more weights.
 constexpr int kRowsN = 32, kRing = 2;          // (two CTAs fit an SM)
-constexpr int kRowsW = kRowsN * (kUnitK / 2), kRowsCols = 9, kRowsSums = kRowsN * kRowsCols;   // sums: floats of a warp
-template <int GS>
-constexpr int rows_stage(int x_rows) { return kRowsW + (x_rows * kUnitK * 2 + ScaleTile<GS, kUnitK>::bytes(kRowsN) + 1023) / 1024 * 1024; }
-template <int GS>
-constexpr int rows_warp(int x_rows) { return kRing * rows_stage<GS>(x_rows) + 2 * kRowsSums * 4; }
+template <int NT>
+constexpr int rows_kb() { return NT == 1 ? 256 : 128; }
+template <int NT>
+constexpr int rows_w() { return kRowsN * (rows_kb<NT>() / 2); }
+template <int NT>
+constexpr int rows_sums() { return kRowsN * (8 * NT + 1); }   // floats of a warp's sums
+template <int GS, int NT>
+constexpr int rows_stage(int x_rows) {
+    return rows_w<NT>() + (x_rows * rows_kb<NT>() * 2 + ScaleTile<GS, rows_kb<NT>()>::bytes(kRowsN) + 1023) / 1024 * 1024;
+}
+template <int GS, int NT>
+constexpr int rows_warp(int x_rows) { return kRing * rows_stage<GS, NT>(x_rows) + 2 * rows_sums<NT>() * 4; }
 
-template <int GS, bool ZEROS>
-__global__ void __launch_bounds__(32 * kMaxSegments)
+template <int GS, int NT, bool ZEROS>
+__global__ void __launch_bounds__(32 * kMaxSegments, 2)
 gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmI4Params p) {
-    constexpr int kCols = kRowsCols, kSums = kRowsSums;
-    const int x_bytes = p.x_rows * kUnitK * 2, stage_bytes = rows_stage<GS>(p.x_rows);
+    constexpr int KB = rows_kb<NT>(), kBlocks = KB / kBlockK, kW = rows_w<NT>(), kCols = 8 * NT + 1, kSums = rows_sums<NT>();
+    const int x_bytes = p.x_rows * KB * 2, stage_bytes = rows_stage<GS, NT>(p.x_rows);
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ uint64_t full[kMaxSegments][kRing];
@@ -243,10 +251,12 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     grid_dep_wait();      // earlier work of the stream is complete and visible
     grid_dep_launch();
     const int tiles = static_cast<int>((p.N + kRowsN - 1) / kRowsN);
-    const int b0 = static_cast<int>(static_cast<int64_t>(warp) * p.units / p.segments);
-    const int b1 = static_cast<int>(static_cast<int64_t>(warp + 1) * p.units / p.segments);
-    const GroupCursor<GS> g0(p, 2 * b0);
-    // the next unit to be copied, its group, and its slot
+    // the warp's stages of KB k
+    const int b0 = static_cast<int>(static_cast<int64_t>(warp) * p.units / p.segments) * (kUnitK / KB);
+    const int u1 = static_cast<int>(static_cast<int64_t>(warp + 1) * p.units / p.segments);
+    const int b1 = KB == kUnitK ? u1 : min(p.blocks, 2 * u1);
+    const GroupCursor<GS> g0(p, b0 * kBlocks);
+    // the next stage to be copied, its group, and its slot
     int ft = blockIdx.x, fb = b0, fs = 0;
     GroupCursor<GS> fg = g0;
     int64_t row_e = static_cast<int64_t>(ft) * kRowsN * p.groups;   // element (the tile's first row, group 0)
@@ -256,16 +266,15 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         uint8_t *dst = ring + fs * stage_bytes;
         uint64_t *bar = &full[warp][fs];
         if (lane == 0) {
-            mbar_arrive_expect_tx(bar, kRowsW + x_bytes);
-            tma_load_2d(dst, &tmW, bar, fb * (kUnitK / 2), ft * kRowsN);
+            mbar_arrive_expect_tx(bar, kW + x_bytes);
+            tma_load_2d(dst, &tmW, bar, fb * (KB / 2), ft * kRowsN);
 #pragma unroll
-            for (int k = 0; k < kUnitK / 64; ++k)
-                tma_load_2d(dst + kRowsW + k * (x_bytes / (kUnitK / 64)), &tmX, bar, fb * kUnitK + 64 * k, 0);
+            for (int k = 0; k < KB / 64; ++k)
+                tma_load_2d(dst + kW + k * (x_bytes / (KB / 64)), &tmX, bar, fb * KB + 64 * k, 0);
         }
-        stage_scales<GS, kUnitK, kRowsN, 32, ZEROS>(p, smem_u32(dst + kRowsW + x_bytes), bar, row_e + fg.group, lane);
+        stage_scales<GS, KB, kRowsN, 32, ZEROS>(p, smem_u32(dst + kW + x_bytes), bar, row_e + fg.group, lane);
         if (++fs == kRing) fs = 0;
-        fg.next(p);
-        fg.next(p);
+        for (int k = 0; k < kBlocks; ++k) fg.next(p);
         if (++fb == b1) fb = b0, fg = g0, ft += gridDim.x, row_e += step_e;
     };
     for (int k = 0; k < kRing; ++k) fill();
@@ -274,22 +283,23 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     bool ok = true;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
         const int64_t n0 = static_cast<int64_t>(tile) * kRowsN;
-        float acc[2][1][4];
+        float acc[2][NT][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[m][0][e] = 0.0f;
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[m][t][e] = 0.0f;
         GroupCursor<GS> g = g0;
         for (int blk = b0; blk < b1 && ok; ++blk) {
             ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][slot], parity, nullptr));
             __syncwarp();
             if (!ok) break;
             const uint8_t *st = ring + slot * stage_bytes;
-            product<GS, kUnitK, 2, 1, kRowsN, false, ZEROS>(smem_u32(st), smem_u32(st) + kRowsW, st + kRowsW + x_bytes, 0, p.x_rows, 0,
-                                                            p.x_rows - 1, p.groups, g, p.K - static_cast<int64_t>(blk) * kUnitK, gq, cq,
-                                                            acc);
-            g.next(p);
-            g.next(p);
+            product<GS, KB, 2, NT, kRowsN, false, ZEROS>(smem_u32(st), smem_u32(st) + kW, st + kW + x_bytes, 0, p.x_rows, 0,
+                                                         NT == 1 ? p.x_rows - 1 : 7, p.groups, g,
+                                                         p.K - static_cast<int64_t>(blk) * KB, gq, cq, acc);
+            for (int k = 0; k < kBlocks; ++k) g.next(p);
             __syncwarp();                                  // every lane has read the slot
             fill();
             if (++slot == kRing) slot = 0, parity ^= 1;
@@ -299,9 +309,11 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mine[(16 * m + gq + 8 * (e >> 1)) * kCols + 2 * cq + (e & 1)] = acc[m][0][e];
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mine[(16 * m + gq + 8 * (e >> 1)) * kCols + 8 * t + 2 * cq + (e & 1)] = acc[m][t][e];
         if (__syncthreads_or(!ok)) break;                  // (two buffers: the one before last has been read)
-        for (int i = threadIdx.x; i < kRowsN * 8; i += blockDim.x) {
+        for (int i = threadIdx.x; i < kRowsN * 8 * NT; i += blockDim.x) {
             const int r = i % kRowsN, t = i / kRowsN;
             if (t >= p.M) break;
             const float *v = sums + buf * p.segments * kSums + r * kCols + t;
@@ -322,7 +334,7 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
 // -------------------------------------------------------------------- tiles ---
 
 constexpr int kTileN = 128;                    // weight rows of a CTA
-constexpr int kTileThreads = 256;              // warps: 8 / WM of 16 WM weight rows x WM of TM / WM rows of X
+constexpr int kTileThreads = 256;              // warps: four of 32 weight rows x two of TM / 2 rows of X
 constexpr int kTileW = kTileN * (kBlockK / 2); // 8 KB a stage
 template <int TM>
 constexpr int tile_stage() { return kTileW + TM * kBlockK * 2; }
@@ -336,7 +348,7 @@ template <int GS, int TM, bool SPLIT, bool ZEROS>
 __global__ void __launch_bounds__(kTileThreads, TM == 64 && !SPLIT ? 1 : 2)
 gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmI4Params p) {
     constexpr int kScaleBytes = ScaleTile<GS, kBlockK>::bytes(kTileN), kTileStage = tile_stage<TM>(), kTileStages = tile_stages<TM>();
-    constexpr int kTileM = TM, WM = TM == 16 ? 1 : 2, MR = WM, NT = TM / 8 / WM;
+    constexpr int kTileM = TM, WM = 2, MR = 2, NT = TM / 16;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *scales = smem + kTileStages * kTileStage;
@@ -462,18 +474,18 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
 
 // ----------------------------------------------------------------- launches ---
 
-template <int GS, bool ZEROS>
+template <int GS, int NT, bool ZEROS>
 bi_status launch_rows(const CUtensorMap &tmW, const CUtensorMap &tmX, const GemmI4Params &p, int sms, cudaStream_t s) {
     static unsigned long long configured = 0;
-    constexpr int most = 1024 + kMaxSegments * rows_warp<GS>(8);
+    constexpr int most = 1024 + kMaxSegments * rows_warp<GS, NT>(8 * NT);
     static_assert(most <= 232448 - 1024, "one CTA's shared memory");
-    if (ensure_smem_attr(reinterpret_cast<const void *>(gemm_int4_rows_kernel<GS, ZEROS>), most, &configured) != BI_OK)
+    if (ensure_smem_attr(reinterpret_cast<const void *>(gemm_int4_rows_kernel<GS, NT, ZEROS>), most, &configured) != BI_OK)
         return BI_ERR_CUDA;
     // as many CTAs as the shared memory of the SMs takes at once
     const int64_t tiles = (p.N + kRowsN - 1) / kRowsN;
-    const int smem = 1024 + p.segments * rows_warp<GS>(p.x_rows), fit = 232448 / (smem + 2048);
+    const int smem = 1024 + p.segments * rows_warp<GS, NT>(p.x_rows), fit = 232448 / (smem + 2048);
     const int64_t most_ctas = static_cast<int64_t>(sms) * (fit > 8 ? 8 : fit);
-    return launch_pdl(gemm_int4_rows_kernel<GS, ZEROS>, dim3(static_cast<unsigned>(tiles < most_ctas ? tiles : most_ctas)),
+    return launch_pdl(gemm_int4_rows_kernel<GS, NT, ZEROS>, dim3(static_cast<unsigned>(tiles < most_ctas ? tiles : most_ctas)),
                       dim3(32 * p.segments), smem, s, tmW, tmX, p);
 }
 
@@ -514,17 +526,16 @@ bi_status launch_tiles(const CUtensorMap &tmW, const CUtensorMap &tmX, const Gem
 
 template <int GS, bool ZEROS>
 bi_status launch_group(const void *X, int64_t ldx, const uint8_t *W, GemmI4Params &p, int sms, cudaStream_t s) {
-    const bool rows = p.M <= 8;
-    const int tm = p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64;
-    p.x_rows = p.M <= 2 ? static_cast<int>(p.M) : p.M <= 4 ? 4 : 8;
+    const bool rows = p.M <= 16;
+    const int tm = p.M <= 32 ? 32 : 64, kb = p.M <= 8 ? rows_kb<1>() : rows_kb<2>();
+    p.x_rows = p.M <= 2 ? static_cast<int>(p.M) : p.M <= 4 ? 4 : p.M <= 8 ? 8 : 16;
     CUtensorMap tmW{}, tmX{};
-    if (make_tmap_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, p.K / 2, p.N, p.K / 2, (rows ? kUnitK : kBlockK) / 2, rows ? kRowsN : kTileN,
-                     rows ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) != BI_OK ||
+    if (make_tmap_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, p.K / 2, p.N, p.K / 2, (rows ? kb : kBlockK) / 2, rows ? kRowsN : kTileN,
+                     rows && kb == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) != BI_OK ||
         make_tmap_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, p.K, p.M, ldx * 2, 64, rows ? p.x_rows : tm,
                      rows ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B) != BI_OK)
         return BI_ERR_CUDA;
-    if (rows) return launch_rows<GS, ZEROS>(tmW, tmX, p, sms, s);
-    if (tm == 16) return launch_tiles<GS, 16, ZEROS>(tmW, tmX, p, sms, s);
+    if (rows) return p.M <= 8 ? launch_rows<GS, 1, ZEROS>(tmW, tmX, p, sms, s) : launch_rows<GS, 2, ZEROS>(tmW, tmX, p, sms, s);
     if (tm == 32) return launch_tiles<GS, 32, ZEROS>(tmW, tmX, p, sms, s);
     return launch_tiles<GS, 64, ZEROS>(tmW, tmX, p, sms, s);
 }
