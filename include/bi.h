@@ -505,7 +505,7 @@ BI_API bi_status bi_attention_extend_int4(const void *Q, const int32_t *cu_q, in
  *   Y[i][j] = bf16( sum_g s[j][g] * sum_{k in group g} X[i][k] * (u[j][k] - z[j][g]) )
  * The weights enter the products as the exact integers u - z; each group's (or
  * each 128 k of a longer group's) sum is fp32, scaled and added in fp32. K is
- * cut into blocks of 128, the blocks into segments fixed by K alone; groups are
+ * cut into units of 256, the units into segments fixed by K alone; groups are
  * added in ascending order within a segment and the segments' sums in segment
  * order. Row i of Y does not depend on M or on the other rows, bit for bit.
  *   X       bf16 [M][ldx]
@@ -514,7 +514,7 @@ BI_API bi_status bi_attention_extend_int4(const void *Q, const int32_t *cu_q, in
  *   zeros   u8   [N][K/group]  0..15 (the low four bits count); NULL: 8 throughout
  *   Y       bf16 [M][ldy]
  * Made for few rows, where the weights' bytes bound it; any M is computed.
- * Requirements: group 32, 64 or a multiple of 128; K % group == 0; N % 8 == 0;
+ * Requirements: group 32, 64 or a multiple of 128; K % group == 0; K <= 2^28; N % 8 == 0;
  * ldx, ldy multiples of 8, ldx >= K, ldy >= N.
  */
 BI_API bi_status bi_gemm_int4(const void *X, int64_t ldx, const uint8_t *W, const void *scales, const uint8_t *zeros,

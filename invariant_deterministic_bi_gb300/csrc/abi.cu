@@ -472,7 +472,8 @@ bi_status bi_gemm_int4(const void *X, int64_t ldx, const uint8_t *W, const void 
     if (M < 0 || N < 0 || K <= 0 || M >= kI32Max || N >= kI32Max || K >= kI32Max || group < 1) return BI_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return BI_OK;
     if (!X || !W || !scales || !Y || ldx < K || ldy < N) return BI_ERR_INVALID_ARG;
-    if (!(group == 32 || group == 64 || group % 128 == 0) || K % group != 0 || N % 8 != 0) return BI_ERR_UNSUPPORTED;
+    if (!(group == 32 || group == 64 || group % 128 == 0) || K % group != 0 || N % 8 != 0 || K > (1 << 28))
+        return BI_ERR_UNSUPPORTED;
     if (ldx % 8 != 0 || ldy % 8 != 0 || !aligned16(X) || !aligned16(W) || !aligned16(Y) ||
         !aligned16(scales) || !aligned16(zeros))
         return BI_ERR_MISALIGNED;

@@ -39,7 +39,8 @@ struct GemmI4Params {
     const uint32_t *S;       // [N][groups] bf16, as words
     const uint32_t *Z;       // [N][groups] bytes, as words, or null
     uint16_t *Y;             // [M][ldy]
-    int64_t ldy, M, N, K, s_last, z_last;   // last words of S and Z
+    int64_t ldy, M, N, s_last, z_last;       // last words of S and Z
+    int32_t K;
     int32_t groups, group, blocks, units, segments;   // blocks: of kBlockK; units: of kUnitK
     int32_t x_rows;          // rows kernel: staged rows of X (1, 2, 4 or 8)
     unsigned *status;
@@ -153,7 +154,7 @@ struct GroupCursor {
 // group; k_left: k from the first one to K's end.
 template <int GS, int KB, int MR, int NT, int ROWS, bool X_SWIZZLED, bool ZEROS>
 __device__ __forceinline__ void product(uint32_t w_tile, uint32_t x_tile, const uint8_t *sc, int row0, int x_rows, int x_row0, int x_mask,
-                                        int groups, const GroupCursor<GS> &g, int64_t k_left, int gq, int cq,
+                                        int groups, const GroupCursor<GS> &g, int k_left, int gq, int cq,
                                         float (&acc)[MR][NT][4]) {
     constexpr int kSub = KB / GS;
 #pragma unroll
@@ -212,77 +213,90 @@ __device__ __forceinline__ void store_y(const GemmI4Params &p, int64_t m, int64_
 
 // ---------------------------------------------------------------- few rows ---
 
-// CTAs of 32 weight rows walk the tiles; a warp's ring of kRing stages runs on from one tile to the next. Two row
-// tiles a warp, and KB = 256 k a stage where X has at most eight rows, spread the waits, the copies' issue and the
-// operands of X over more weights.
-constexpr int kRowsN = 32, kRing = 2;          // (two CTAs fit an SM)
+// CTAs walk the tiles of 32 weight rows a warp; a segment's ring of kRing stages runs on from one tile to the next.
+// Two row tiles a warp, and KB = 256 k a stage where X has at most eight rows, spread the waits, the copies' issue and
+// the operands of X over more weights; with up to 16 rows of X, two warps (of 64 weight rows) share a segment's stages,
+// so that 16 warps fit an SM either way.
+constexpr int kRing = 2;
+template <int NT>
+constexpr int rows_n() { return 32 * NT; }     // weight rows of a CTA: NT warps a segment
 template <int NT>
 constexpr int rows_kb() { return NT == 1 ? 256 : 128; }
 template <int NT>
-constexpr int rows_w() { return kRowsN * (rows_kb<NT>() / 2); }
+constexpr int rows_w() { return rows_n<NT>() * (rows_kb<NT>() / 2); }
 template <int NT>
-constexpr int rows_sums() { return kRowsN * (8 * NT + 1); }   // floats of a warp's sums
+constexpr int rows_sums() { return rows_n<NT>() * (8 * NT + 1); }   // floats of a segment's sums
 template <int GS, int NT>
 constexpr int rows_stage(int x_rows) {
-    return rows_w<NT>() + (x_rows * rows_kb<NT>() * 2 + ScaleTile<GS, rows_kb<NT>()>::bytes(kRowsN) + 1023) / 1024 * 1024;
+    return rows_w<NT>() + (x_rows * rows_kb<NT>() * 2 + ScaleTile<GS, rows_kb<NT>()>::bytes(rows_n<NT>()) + 1023) / 1024 * 1024;
 }
+template <int NT>
+constexpr int rows_buffers() { return NT == 1 ? 2 : 1; }       // of the sums
 template <int GS, int NT>
-constexpr int rows_warp(int x_rows) { return kRing * rows_stage<GS, NT>(x_rows) + 2 * rows_sums<NT>() * 4; }
+constexpr int rows_segment(int x_rows) { return kRing * rows_stage<GS, NT>(x_rows) + rows_buffers<NT>() * rows_sums<NT>() * 4; }
 
 template <int GS, int NT, bool ZEROS>
-__global__ void __launch_bounds__(32 * kMaxSegments, 2)
+__global__ void __launch_bounds__(32 * kMaxSegments * NT, NT == 1 ? 2 : 1)
 gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmI4Params p) {
     constexpr int KB = rows_kb<NT>(), kBlocks = KB / kBlockK, kW = rows_w<NT>(), kCols = 8 * NT + 1, kSums = rows_sums<NT>();
+    constexpr int kN = rows_n<NT>(), kBuffers = rows_buffers<NT>();
     const int x_bytes = p.x_rows * KB * 2, stage_bytes = rows_stage<GS, NT>(p.x_rows);
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ uint64_t full[kMaxSegments][kRing];
+    __shared__ uint64_t full[kMaxSegments][kRing], empty[kMaxSegments][kRing];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int gq = lane >> 2, cq = lane & 3;
-    uint8_t *ring = smem + warp * kRing * stage_bytes;                                     // a stage: W, X, scales
-    float *sums = reinterpret_cast<float *>(smem + p.segments * kRing * stage_bytes);   // [2][segments][kSums]
-    if (lane == 0) {
-        for (int k = 0; k < kRing; ++k) mbar_init(&full[warp][k], 33);   // 32 lanes' scale copies, and the TMA's bytes
+    const int gq = lane >> 2, cq = lane & 3, seg = warp / NT, wn = warp % NT;
+    uint8_t *ring = smem + seg * kRing * stage_bytes;                                      // a stage: W, X, scales
+    float *sums = reinterpret_cast<float *>(smem + p.segments * kRing * stage_bytes);   // [kBuffers][segments][kSums]
+    if (wn == 0 && lane == 0) {
+        for (int k = 0; k < kRing; ++k) {
+            mbar_init(&full[seg][k], 33);                  // 32 lanes' scale copies, and the TMA's bytes
+            mbar_init(&empty[seg][k], NT);
+        }
         fence_mbar_init();
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmX);
     }
-    __syncwarp();
+    if (NT == 1)
+        __syncwarp();
+    else
+        __syncthreads();
     grid_dep_wait();      // earlier work of the stream is complete and visible
     grid_dep_launch();
-    const int tiles = static_cast<int>((p.N + kRowsN - 1) / kRowsN);
-    // the warp's stages of KB k
-    const int b0 = static_cast<int>(static_cast<int64_t>(warp) * p.units / p.segments) * (kUnitK / KB);
-    const int u1 = static_cast<int>(static_cast<int64_t>(warp + 1) * p.units / p.segments);
+    const int tiles = static_cast<int>((p.N + kN - 1) / kN);
+    // the segment's stages of KB k
+    const int b0 = static_cast<int>(static_cast<int64_t>(seg) * p.units / p.segments) * (kUnitK / KB);
+    const int u1 = static_cast<int>(static_cast<int64_t>(seg + 1) * p.units / p.segments);
     const int b1 = KB == kUnitK ? u1 : min(p.blocks, 2 * u1);
     const GroupCursor<GS> g0(p, b0 * kBlocks);
-    // the next stage to be copied, its group, and its slot
+    // the next stage to be copied (by the segment's first warp), its group, and its slot
     int ft = blockIdx.x, fb = b0, fs = 0;
     GroupCursor<GS> fg = g0;
-    int64_t row_e = static_cast<int64_t>(ft) * kRowsN * p.groups;   // element (the tile's first row, group 0)
-    const int64_t step_e = static_cast<int64_t>(gridDim.x) * kRowsN * p.groups;
+    int64_t row_e = static_cast<int64_t>(ft) * kN * p.groups;   // element (the tile's first row, group 0)
+    const int64_t step_e = static_cast<int64_t>(gridDim.x) * kN * p.groups;
     auto fill = [&]() {
         if (ft >= tiles) return;
         uint8_t *dst = ring + fs * stage_bytes;
-        uint64_t *bar = &full[warp][fs];
+        uint64_t *bar = &full[seg][fs];
         if (lane == 0) {
             mbar_arrive_expect_tx(bar, kW + x_bytes);
-            tma_load_2d(dst, &tmW, bar, fb * (KB / 2), ft * kRowsN);
+            tma_load_2d(dst, &tmW, bar, fb * (KB / 2), ft * kN);
 #pragma unroll
             for (int k = 0; k < KB / 64; ++k)
                 tma_load_2d(dst + kW + k * (x_bytes / (KB / 64)), &tmX, bar, fb * KB + 64 * k, 0);
         }
-        stage_scales<GS, KB, kRowsN, 32, ZEROS>(p, smem_u32(dst + kW + x_bytes), bar, row_e + fg.group, lane);
+        stage_scales<GS, KB, kN, 32, ZEROS>(p, smem_u32(dst + kW + x_bytes), bar, row_e + fg.group, lane);
         if (++fs == kRing) fs = 0;
         for (int k = 0; k < kBlocks; ++k) fg.next(p);
         if (++fb == b1) fb = b0, fg = g0, ft += gridDim.x, row_e += step_e;
     };
-    for (int k = 0; k < kRing; ++k) fill();
+    if (wn == 0)
+        for (int k = 0; k < kRing; ++k) fill();
     int slot = 0, buf = 0;
     uint32_t parity = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
-        const int64_t n0 = static_cast<int64_t>(tile) * kRowsN;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf = (buf + 1) % kBuffers) {
+        const int64_t n0 = static_cast<int64_t>(tile) * kN;
         float acc[2][NT][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -292,20 +306,23 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                 for (int e = 0; e < 4; ++e) acc[m][t][e] = 0.0f;
         GroupCursor<GS> g = g0;
         for (int blk = b0; blk < b1 && ok; ++blk) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][slot], parity, nullptr));
+            ok = __all_sync(0xffffffffu, mbar_wait(&full[seg][slot], parity, nullptr));
             __syncwarp();
             if (!ok) break;
             const uint8_t *st = ring + slot * stage_bytes;
-            product<GS, KB, 2, NT, kRowsN, false, ZEROS>(smem_u32(st), smem_u32(st) + kW, st + kW + x_bytes, 0, p.x_rows, 0,
-                                                         NT == 1 ? p.x_rows - 1 : 7, p.groups, g,
-                                                         p.K - static_cast<int64_t>(blk) * KB, gq, cq, acc);
+            product<GS, KB, 2, NT, kN, false, ZEROS>(smem_u32(st), smem_u32(st) + kW, st + kW + x_bytes, 32 * wn, p.x_rows, 0,
+                                                     NT == 1 ? p.x_rows - 1 : 7, p.groups, g, p.K - blk * KB, gq, cq, acc);
             for (int k = 0; k < kBlocks; ++k) g.next(p);
             __syncwarp();                                  // every lane has read the slot
-            fill();
+            if (NT > 1) {
+                if (lane == 0) mbar_arrive(&empty[seg][slot]);
+                if (wn == 0) ok = __all_sync(0xffffffffu, mbar_wait(&empty[seg][slot], parity, nullptr));
+            }
+            if (wn == 0 && ok) fill();
             if (++slot == kRing) slot = 0, parity ^= 1;
         }
         // the segments' sums, added in order
-        float *mine = sums + (buf * p.segments + warp) * kSums;
+        float *mine = sums + (buf * p.segments + seg) * kSums + 32 * wn * kCols;
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -313,19 +330,20 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mine[(16 * m + gq + 8 * (e >> 1)) * kCols + 8 * t + 2 * cq + (e & 1)] = acc[m][t][e];
         if (__syncthreads_or(!ok)) break;                  // (two buffers: the one before last has been read)
-        for (int i = threadIdx.x; i < kRowsN * 8 * NT; i += blockDim.x) {
-            const int r = i % kRowsN, t = i / kRowsN;
+        for (int i = threadIdx.x; i < kN * 8 * NT; i += blockDim.x) {
+            const int r = i % kN, t = i / kN;
             if (t >= p.M) break;
             const float *v = sums + buf * p.segments * kSums + r * kCols + t;
             float y = v[0];
             for (int s = 1; s < p.segments; ++s) y += v[s * kSums];
             store_y(p, t, n0 + r, y);
         }
+        if (kBuffers == 1) __syncthreads();
     }
-    if (!ok && lane == 0) {                                // a wait ran out: report; the copies in flight get another limit
-        atomicOr(p.status, kDevTimeout);
+    if (!ok && wn == 0) {                                  // a wait ran out: report; the copies in flight get another limit
+        if (lane == 0) atomicOr(p.status, kDevTimeout);
         for (int k = 0; k < kRing; ++k) {
-            mbar_wait(&full[warp][slot], parity, nullptr);
+            mbar_wait(&full[seg][slot], parity, nullptr);
             if (++slot == kRing) slot = 0, parity ^= 1;
         }
     }
@@ -412,7 +430,7 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         if (blk + kTileStages - 1 < last) fill(blk + kTileStages - 1);
         const uint32_t st = smem_u32(smem + slot * kTileStage);
         product<GS, kBlockK, MR, NT, kTileN, true, ZEROS>(st, st + kTileW, scales + slot * kScaleBytes, 16 * MR * wn, kTileM, 8 * NT * wm, 7,
-                                                          p.groups, g, p.K - static_cast<int64_t>(blk) * kBlockK, gq, cq, acc);
+                                                          p.groups, g, p.K - blk * kBlockK, gq, cq, acc);
         g.next(p);
         if (!SPLIT && blk + 1 == seg_end) {
 #pragma unroll
@@ -477,16 +495,16 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
 template <int GS, int NT, bool ZEROS>
 bi_status launch_rows(const CUtensorMap &tmW, const CUtensorMap &tmX, const GemmI4Params &p, int sms, cudaStream_t s) {
     static unsigned long long configured = 0;
-    constexpr int most = 1024 + kMaxSegments * rows_warp<GS, NT>(8 * NT);
+    constexpr int most = 1024 + kMaxSegments * rows_segment<GS, NT>(8 * NT);
     static_assert(most <= 232448 - 1024, "one CTA's shared memory");
     if (ensure_smem_attr(reinterpret_cast<const void *>(gemm_int4_rows_kernel<GS, NT, ZEROS>), most, &configured) != BI_OK)
         return BI_ERR_CUDA;
     // as many CTAs as the shared memory of the SMs takes at once
-    const int64_t tiles = (p.N + kRowsN - 1) / kRowsN;
-    const int smem = 1024 + p.segments * rows_warp<GS, NT>(p.x_rows), fit = 232448 / (smem + 2048);
-    const int64_t most_ctas = static_cast<int64_t>(sms) * (fit > 8 ? 8 : fit);
+    const int64_t tiles = (p.N + rows_n<NT>() - 1) / rows_n<NT>();
+    const int smem = 1024 + p.segments * rows_segment<GS, NT>(p.x_rows), fit = 232448 / (smem + 2048);
+    const int64_t most_ctas = static_cast<int64_t>(sms) * (fit > 4 ? 4 : fit);
     return launch_pdl(gemm_int4_rows_kernel<GS, NT, ZEROS>, dim3(static_cast<unsigned>(tiles < most_ctas ? tiles : most_ctas)),
-                      dim3(32 * p.segments), smem, s, tmW, tmX, p);
+                      dim3(32 * NT * p.segments), smem, s, tmW, tmX, p);
 }
 
 template <int GS, int TM, bool SPLIT, bool ZEROS>
@@ -530,7 +548,7 @@ bi_status launch_group(const void *X, int64_t ldx, const uint8_t *W, GemmI4Param
     const int tm = p.M <= 32 ? 32 : 64, kb = p.M <= 8 ? rows_kb<1>() : rows_kb<2>();
     p.x_rows = p.M <= 2 ? static_cast<int>(p.M) : p.M <= 4 ? 4 : p.M <= 8 ? 8 : 16;
     CUtensorMap tmW{}, tmX{};
-    if (make_tmap_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, p.K / 2, p.N, p.K / 2, (rows ? kb : kBlockK) / 2, rows ? kRowsN : kTileN,
+    if (make_tmap_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, p.K / 2, p.N, p.K / 2, (rows ? kb : kBlockK) / 2, rows ? (p.M <= 8 ? rows_n<1>() : rows_n<2>()) : kTileN,
                      rows && kb == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) != BI_OK ||
         make_tmap_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, p.K, p.M, ldx * 2, 64, rows ? p.x_rows : tm,
                      rows ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B) != BI_OK)
@@ -553,7 +571,7 @@ bi_status launch_gemm_int4(const void *X, int64_t ldx, const uint8_t *W, const v
     p.Z = reinterpret_cast<const uint32_t *>(zeros);
     p.Y = static_cast<uint16_t *>(Y);
     p.ldy = ldy;
-    p.M = M, p.N = N, p.K = K;
+    p.M = M, p.N = N, p.K = static_cast<int32_t>(K);
     p.groups = static_cast<int32_t>(K / group);
     p.s_last = N * p.groups / 2 - 1, p.z_last = N * p.groups / 4 - 1;   // (N % 8 == 0)
     p.group = static_cast<int32_t>(group);
