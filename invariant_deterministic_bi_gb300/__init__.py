@@ -469,7 +469,7 @@ def _launch_on(cache, tensors, stream):
     for t in tensors:
         if t is not None and t.get_device() != cur:
             raise ValueError(f"tensors must be on the current device cuda:{cur}, got {t.device}")
-    raw = torch._C._cuda_getCurrentRawStream(cur) if stream is None else stream.cuda_stream
+    raw = torch.cuda.current_stream(cur).cuda_stream if stream is None else stream.cuda_stream
     if cache is None:
         return raw, ()
     return raw, (cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr())
@@ -579,7 +579,7 @@ def attention_decode_int4(Q, cache: KVInt4Cache, block_table, seq_lens, max_seq_
     if O is None:
         O = _new((B, Hq, D), torch.bfloat16, Q, stream)
     _check(load().bi_attention_decode_int4(Q.data_ptr(), *c, block_table.data_ptr(), block_table.shape[1], nblk,
-                                           seq_lens.data_ptr(), B, Hq, Hkv, D, bs, max_seq_len, scale,
+                                           seq_lens.data_ptr(), B, Hq, Hkv, D, bs, max_seq_len, float(scale),
                                            workspace.data_ptr(), workspace.numel(), O.data_ptr(), raw),
            "bi_attention_decode_int4")
     return O
@@ -612,7 +612,7 @@ def attention_extend_int4(Q, cu_q, cache: KVInt4Cache, block_table, seq_lens, ma
         O = _new((T, Hq, D), torch.bfloat16, Q, stream)
     _check(load().bi_attention_extend_int4(Q.data_ptr(), cu_q.data_ptr(), T, *c, block_table.data_ptr(),
                                            block_table.shape[1], nblk, seq_lens.data_ptr(), B, Hq, Hkv, D, bs, max_seq_len,
-                                           max_q_len, scale, workspace.data_ptr() if workspace is not None else None,
+                                           max_q_len, float(scale), workspace.data_ptr() if workspace is not None else None,
                                            workspace.numel() if workspace is not None else 0, O.data_ptr(), raw),
            "bi_attention_extend_int4")
     return O
