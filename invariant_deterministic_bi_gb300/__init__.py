@@ -457,6 +457,13 @@ def kv_int4_cache(num_blocks: int, block_size: int, Hkv: int, device="cuda") -> 
                          for w, d in ((64, torch.uint8), (4, torch.bfloat16)) * 2))
 
 
+def _current_raw_stream(device: int) -> int:
+    """The current stream's handle (without making a Stream object, where torch offers that)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+
+
 def _launch_on(cache, tensors, stream):
     """(raw stream, cache arguments) for a call on the current device; the tensors and the cache have to be there."""
     import torch
@@ -469,7 +476,7 @@ def _launch_on(cache, tensors, stream):
     for t in tensors:
         if t is not None and t.get_device() != cur:
             raise ValueError(f"tensors must be on the current device cuda:{cur}, got {t.device}")
-    raw = torch.cuda.current_stream(cur).cuda_stream if stream is None else stream.cuda_stream
+    raw = _current_raw_stream(cur) if stream is None else stream.cuda_stream
     if cache is None:
         return raw, ()
     return raw, (cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr())
