@@ -484,10 +484,10 @@ BI_API bi_status bi_attention_decode_int4(const void *Q, const uint8_t *k_codes,
  * bi_attention_decode_int4 of each token's cut sequence.
  *   workspace  caller-owned device scratch, NULLABLE. With at least
  *              bi_attention_extend_int4_workspace_size(...) > 0 bytes, calls
- *              with few new tokens a sequence (drafts to verify) are split over
- *              the cache's chunks like decode; without, or where that size is
- *              0, one CTA walks the chunks of each tile of new tokens. The
- *              bits are the same.
+ *              with few new tokens (drafts to verify, a short prompt after a
+ *              long one) are split over the cache's chunks like decode;
+ *              without, or where that size is 0, one CTA walks the chunks of
+ *              each tile of new tokens. The bits are the same.
  * bi_attention_extend_int4_workspace_size returns -1 for arguments out of range.
  */
 BI_API int64_t bi_attention_extend_int4_workspace_size(int64_t total_q, int32_t Hq, int32_t Hkv, int32_t max_seq_len,

@@ -21,6 +21,17 @@
 //        transposed by movmatrix.
 // Step 2, attn_merge_int4_kernel, one CTA per (query token, query head): the
 //   chunk results are merged in chunk order and o / l is rounded to bf16.
+//
+// What bounds it: not HBM (3.6 times fewer bytes than bf16 leave 45 us at
+// 64 x 4096 tokens, 8 KV heads) but expanding the codes: 128 words of eight an
+// item and lane, 12 or 13 instructions each, on pipes that overlap only partly
+// with each other and with mma.sync (a word and a product: 21.6-24.7 cycles per
+// warp and scheduler, 17 and 8 apart). Measured (GB300): 64 x 4096, 32 heads over 8
+// 91 us, 3.3 TB/s (bf16 cache: 187 us); 1 x 4096 10.1 us; 2 x 131072, 64 over 8
+// heads 103 us; 16 sequences x 5 new tokens over 100..4000 59 us. Per warp two 9 KB
+// buffers and 12 warps; 16 warps with three 4.5 KB buffers each took 102 us (the
+// pipes, not the latencies, are what a warp waits for); reading the codes from
+// global memory into registers, 133 us.
 #include "attn_common.cuh"
 #include "bi_internal.h"
 #include "bi_ptx.cuh"
@@ -38,9 +49,12 @@ constexpr int kRecord = kD + 2;                // floats of a chunk result: m, l
 constexpr int kMergeThreads = 128;             // and a warp that loads
 constexpr int kMergeTile = 32, kMergeRing = 8; // chunk results of a tile, tiles on the way at most
 constexpr int kMergeStage = (kMergeTile * kRecord * 4 + 16 + 15) / 16 * 16;
-// Extend takes this split for at most so many query rows (tokens x shared heads) a sequence, and chunk results of
-// at most so many bytes.
-constexpr int kFewRows = 64;
+// Extend takes this split or the tiled kernel by their estimated times (the sizes decide, not the data): a CTA of
+// the tiled kernel spends about 13 K cycles on a chunk for up to 128 query rows, one CTA an SM and no split of the
+// chunks; an SM here about 1.7 K for each eight rows. Measured, 32 heads over 8, 4000 cached tokens, tiled / split:
+// 16 sequences x 5 tokens 262 / 77 us, x 16 229 / 196; 1 x 5 257 / 12, 1 x 16 217 / 21, 4 x 8 (64 heads) 222 / 53;
+// 64 x 16 over 2000 458 / 407. The chunk results take at most kFewBytes.
+constexpr int64_t kSms = 152, kTiledCost = 130, kSplitCost = 17;
 constexpr int64_t kFewBytes = 512ll << 20;
 
 struct SplitParams {
@@ -590,7 +604,9 @@ bi_status launch_few(SplitParams &p, cudaStream_t s) {
     const int64_t items = p.batch * p.tiles * p.c.Hkv * static_cast<int64_t>(p.chunks);
     const int64_t merges = p.batch * (EXT ? p.max_q : 1) * p.Hq;
     if (merges > 0x7FFFFFFF) return BI_ERR_UNSUPPORTED;
-    const bool blocks = p.c.bs % 8 == 0;                   // runs of whole blocks can be copied as they lie
+    // Block sizes that are multiples of eight can be copied as they lie (64 x 4096 tokens, blocks of 16: 91 us; by
+    // rows, the same with 64 more copies a lane, 131 against 100 when it was measured).
+    const bool blocks = p.c.bs % 8 == 0;
 #define BI_SPLIT(g) st = blocks ? launch_split<g, EXT, true>(items, info->sm_count, p, s) \
                                 : launch_split<g, EXT, false>(items, info->sm_count, p, s)
     switch (G) {
@@ -615,7 +631,12 @@ bi_status launch_few(SplitParams &p, cudaStream_t s) {
 int64_t attention_extend_int4_workspace_bytes(int64_t total_q, int32_t Hq, int32_t Hkv, int32_t max_len, int32_t max_q) {
     const int64_t bytes = attention_decode_workspace_bytes(total_q, Hq, max_len);
     if (bytes < 0) return -1;
-    return max_q <= kFewRows / (Hq / Hkv) && bytes <= kFewBytes ? bytes : 0;
+    if (bytes > kFewBytes) return 0;
+    // (total_q is small here) sequences at least, the tiled kernel's CTAs with work at least
+    const int64_t rows = total_q * (Hq / Hkv), seqs = (total_q + max_q - 1) / max_q;
+    const int64_t tiles = (rows + 127) / 128 > seqs ? (rows + 127) / 128 : seqs;
+    const int64_t tiled = (tiles * Hkv + kSms - 1) / kSms * kTiledCost, split = (rows + 7) / 8 * Hkv * kSplitCost / kSms;
+    return split < tiled ? bytes : 0;
 }
 
 bi_status launch_attention_decode_int4(const void *Q, const KvInt4 &c, const int32_t *table, int32_t max_blocks,

@@ -15,14 +15,28 @@
 //
 // The sum's order is fixed by (K, group): K is cut into units of 256 and the
 // units into S segments; a segment's groups (of longer ones, each 128 k) are added
-// in ascending order, and the segments' sums in order. The number of rows decides only who computes
-// what:
-//   - few rows (gemm_int4_rows_kernel, M <= 16): a warp a segment, the CTA's
-//     warps share 32 weight rows; every warp has its own ring of TMA
-//     copies and nobody waits for anybody before the final sum;
+// in ascending order, and the segments' sums in order. The number of rows of X
+// decides only who computes what:
+//   - few rows (gemm_int4_rows_kernel, M <= 16): a warp (two for M > 8) a
+//     segment, with its own ring of TMA copies, so that nobody waits for another
+//     segment before the final sum;
 //   - more (gemm_int4_tile_kernel): a CTA a tile of 128 weight rows x 32 or 64
 //     rows of X, both staged by TMA for all warps; it walks the segments, or, where the
 //     tiles would not fill the GPU, the CTAs of a cluster take one each.
+//
+// What bounds it: a word of eight codes costs 11 instructions to expand (three
+// shifts, four logic operations, four multiply-adds), and the integer pipe, the
+// packed bf16 pipe and mma.sync overlap only partly on this GPU: an expansion
+// alone takes 16.4-17.6 cycles per warp and scheduler, with one product 21.6-24.7
+// (17 and 8 apart; measured with independent chains). At the weights' HBM rate a
+// scheduler has 22 cycles for a word. Measured (GB300, weights from HBM): M = 1:
+// 6144 x 4096, g = 128 7.7 us (1.7 TB/s; 3 us of it launch and first latency),
+// 24576 x 4096 18.6 us (2.8 TB/s); M = 16, 24576 x 4096, g = 64 35 us; M = 200,
+// 4096 x 12288 118 us (g = 128) and 139 us (g = 32); M = 2048, 6144 x 4096 442 us
+// (233 TFLOP/s). A form with the expanded weights in tensor memory and tcgen05
+// products was 13.9, 39.9, 48, 88 and 146, 334 us in that order: faster for many
+// rows, but every M has to give the same bits, which the two products do not, and
+// few rows are what the call is for.
 #include "attn_common.cuh"
 #include "bi_internal.h"
 #include "bi_ptx.cuh"
@@ -42,7 +56,7 @@ struct GemmI4Params {
     int64_t ldy, M, N, s_last, z_last;       // last words of S and Z
     int32_t K;
     int32_t groups, group, blocks, units, segments;   // blocks: of kBlockK; units: of kUnitK
-    int32_t x_rows;          // rows kernel: staged rows of X (1, 2, 4 or 8)
+    int32_t x_rows;          // rows kernel: staged rows of X (1, 2, 4, 8 or 16)
     unsigned *status;
 };
 
@@ -340,8 +354,8 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         }
         if (kBuffers == 1) __syncthreads();
     }
-    if (!ok && wn == 0) {                                  // a wait ran out: report; the copies in flight get another limit
-        if (lane == 0) atomicOr(p.status, kDevTimeout);
+    if (!ok && lane == 0) atomicOr(p.status, kDevTimeout);
+    if (!ok && wn == 0) {                                  // a wait ran out: the copies in flight get another limit
         for (int k = 0; k < kRing; ++k) {
             mbar_wait(&full[seg][slot], parity, nullptr);
             if (++slot == kRing) slot = 0, parity ^= 1;
@@ -536,7 +550,8 @@ bi_status launch_tile_kernel(const CUtensorMap &tmW, const CUtensorMap &tmX, con
 
 template <int GS, int TM, bool ZEROS>
 bi_status launch_tiles(const CUtensorMap &tmW, const CUtensorMap &tmX, const GemmI4Params &p, int sms, cudaStream_t s) {
-    // a CTA a segment while the tiles alone would leave SMs without one
+    // A CTA a segment while the tiles alone would leave SMs without one: one segment a CTA / all, g = 128: 17 x 6144 x
+    // 4096 (48 tiles) 19.1 / 29.4 us, 64 rows 28.8 / 41.4, 200 x 4096 x 12288 (128) 116 / 117, 32 x 24576 x 4096 (192) 58 / 47
     const int64_t tiles = (p.N + kTileN - 1) / kTileN * ((p.M + TM - 1) / TM);
     if (p.segments > 1 && tiles < sms) return launch_tile_kernel<GS, TM, true, ZEROS>(tmW, tmX, p, tiles, s);
     return launch_tile_kernel<GS, TM, false, ZEROS>(tmW, tmX, p, tiles, s);
@@ -544,6 +559,8 @@ bi_status launch_tiles(const CUtensorMap &tmW, const CUtensorMap &tmX, const Gem
 
 template <int GS, bool ZEROS>
 bi_status launch_group(const void *X, int64_t ldx, const uint8_t *W, GemmI4Params &p, int sms, cudaStream_t s) {
+    // Rows kernel / tile kernel, g = 128: 9 x 6144 x 4096 11.8 / 17.0 us, 16 rows 11.9 / 17.9, 16 x 24576 x 4096 30 / 47.
+    // Tiles of 32 / 64 rows of X: 17 x 6144 x 4096 19.1 / 23.9 us, 33 rows 29.2 / 25.9, 64 rows 31.5 / 28.8.
     const bool rows = p.M <= 16;
     const int tm = p.M <= 32 ? 32 : 64, kb = p.M <= 8 ? rows_kb<1>() : rows_kb<2>();
     p.x_rows = p.M <= 2 ? static_cast<int>(p.M) : p.M <= 4 ? 4 : p.M <= 8 ? 8 : 16;

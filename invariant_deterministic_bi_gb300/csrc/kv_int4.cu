@@ -11,8 +11,9 @@
 // The two half warps take the K and the V row of the same token and head, and
 // a warp one or four heads of a token.
 //
-// Both kernels are bound by memory: 512 bytes in and 144 out per token and KV
-// head (append), the reverse (read).
+// 512 bytes in and 144 out per token and KV head (append), the reverse (read).
+// Measured (8 heads): 8155 tokens 26 us for both (3.3 TB/s each; append is bound by
+// its about 110 instructions a row pair as much as by memory), 64 tokens 3.7 us.
 #include "bi_internal.h"
 #include "bi_ptx.cuh"
 #include "kv_int4.cuh"
