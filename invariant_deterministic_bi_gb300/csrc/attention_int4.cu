@@ -139,7 +139,7 @@ __device__ __forceinline__ Item load_item(const SplitParams &p, const Cursor &u,
     if (BLOCKS) {
         const int first = j0 / p.c.bs, blk_i = first + lane;
         const int64_t start = static_cast<int64_t>(blk_i) * p.c.bs - j0;   // the block's first token in the chunk
-        const int t0 = static_cast<int>(max(start, static_cast<int64_t>(0)));
+        const int t0 = static_cast<int>(min(max(start, static_cast<int64_t>(0)), static_cast<int64_t>(x.n)));
         const int t1 = static_cast<int>(min(start + p.c.bs, static_cast<int64_t>(x.n)));
         x.row[0] = 0, x.row[1] = 0, x.row[2] = 0;
         if (t0 < t1) {

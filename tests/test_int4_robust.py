@@ -237,3 +237,28 @@ def test_prefill_then_decode_equals_decode_alone(bi):
     # largest value each
     assert (np.abs(got.float().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -12 * np.abs(v).max()).all()
     assert bi.device_status() == bi.BI_OK
+
+
+def test_block_past_2_31_tokens_ahead(bi):
+    """Blocks so large that the places of the next 31 blocks pass 31 bits: a chunk still lies in its one block."""
+    import torch
+    if torch.cuda.get_device_properties(0).total_memory < 64 << 30:
+        pytest.skip("needs a cache of 10 GB")
+    bs = 69273672                                      # 31 blocks on: past 2^31
+    c = bi.KVInt4Cache(*(torch.empty((1, 1, bs, w), dtype=d, device="cuda")
+                         for w, d in ((64, torch.uint8), (4, torch.bfloat16)) * 2))
+    g = torch.Generator(device="cuda").manual_seed(7)
+    K = torch.randn((300, 1, D), device="cuda", generator=g).to(torch.bfloat16)
+    V = torch.randn((300, 1, D), device="cuda", generator=g).to(torch.bfloat16)
+    small = bi.kv_int4_cache(20, 16, 1)
+    for cache in (c, small):
+        bi.kv_int4_append(K, V, torch.arange(300, device="cuda"), cache)
+    q = torch.randn((1, 8, D), device="cuda", generator=g).to(torch.bfloat16)
+    lens = torch.tensor([300], dtype=torch.int32, device="cuda")
+    one, many = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.arange(20, dtype=torch.int32, device="cuda").view(1, 20)
+    want = bi.attention_decode_int4(q, small, many, lens, 300, SCALE)
+    assert torch.equal(bi.attention_decode_int4(q, c, one, lens, 300, SCALE), want)
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    for ws in (None, torch.empty(16, dtype=torch.uint8, device="cuda")):
+        assert torch.equal(bi.attention_extend_int4(q, cu, c, one, lens, 300, 1, SCALE, workspace=ws), want)
+    assert bi.device_status() == bi.BI_OK
