@@ -460,7 +460,8 @@ bi_status bi_attention_extend_int4(const void *Q, const int32_t *cu_q, int32_t t
     st = require_device();
     if (st != BI_OK) return st;
     const int64_t few = attention_extend_int4_workspace_bytes(total_q, Hq, Hkv, max_seq_len, max_q_len);
-    if (workspace && few > 0 && workspace_bytes >= few)
+    if (max_q_len > total_q) max_q_len = total_q;      // (no sequence has more)
+    if (workspace && few > 0 && workspace_bytes >= few && B * max_q_len <= kI32Max / Hq)   // its merge's grid
         return launch_attention_extend_int4_few(Q, cu_q, total_q, c, block_table, max_blocks_per_seq, seq_lens, B, Hq,
                                                 max_seq_len, max_q_len, scale, workspace, O, as_stream(stream));
     return launch_attention_extend_int4(Q, cu_q, total_q, c, block_table, max_blocks_per_seq, seq_lens, B, Hq, max_seq_len,

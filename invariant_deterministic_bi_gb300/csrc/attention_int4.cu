@@ -633,7 +633,7 @@ int64_t attention_extend_int4_workspace_bytes(int64_t total_q, int32_t Hq, int32
     if (bytes < 0) return -1;
     if (bytes > kFewBytes) return 0;
     // (total_q is small here) sequences at least, the tiled kernel's CTAs with work at least
-    const int64_t rows = total_q * (Hq / Hkv), seqs = (total_q + max_q - 1) / max_q;
+    const int64_t rows = total_q * (Hq / Hkv), seqs = (total_q + max_q - 1) / max_q;   // (max_q > total_q: one)
     const int64_t tiles = (rows + 127) / 128 > seqs ? (rows + 127) / 128 : seqs;
     const int64_t tiled = (tiles * Hkv + kSms - 1) / kSms * kTiledCost, split = (rows + 7) / 8 * Hkv * kSplitCost / kSms;
     return split < tiled ? bytes : 0;

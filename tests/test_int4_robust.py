@@ -262,3 +262,22 @@ def test_block_past_2_31_tokens_ahead(bi):
     for ws in (None, torch.empty(16, dtype=torch.uint8, device="cuda")):
         assert torch.equal(bi.attention_extend_int4(q, cu, c, one, lens, 300, 1, SCALE, workspace=ws), want)
     assert bi.device_status() == bi.BI_OK
+
+
+@pytest.mark.parametrize("most", [5, 4096, 2 ** 31 - 1])
+def test_extend_with_a_generous_most_new_tokens(bi, most):
+    """max_q_len bounds a sequence's new tokens from above; however far above, the call is the same."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(11)
+    B, Hq = 6, 16
+    c = bi.kv_int4_cache(8 * B, 16, 4)
+    K = torch.randn((128 * B, 4, D), device="cuda", generator=g).to(torch.bfloat16)
+    bi.kv_int4_append(K, K, torch.arange(128 * B, device="cuda"), c)
+    table = torch.arange(8 * B, dtype=torch.int32, device="cuda").view(B, 8)
+    lens = torch.tensor([100, 5, 128, 77, 0, 33], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 5, 10, 11, 13, 13, 17], dtype=torch.int32, device="cuda")
+    q = torch.randn((17, Hq, D), device="cuda", generator=g).to(torch.bfloat16)
+    assert bi.attention_extend_int4_workspace_size(17, Hq, 4, 128, most) > 0
+    want = bi.attention_extend_int4(q, cu, c, table, lens, 128, 5, SCALE, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(bi.attention_extend_int4(q, cu, c, table, lens, 128, most, SCALE), want)
+    assert bi.device_status() == bi.BI_OK
