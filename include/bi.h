@@ -480,8 +480,9 @@ BI_API bi_status bi_attention_decode_int4(const void *Q, const uint8_t *k_codes,
 /*
  * bi_attention_extend_int4 -- bi_attention_extend over the 4-bit cache, which
  * already holds the new tokens' keys and values: the same bits as
- * bi_attention_extend over a bf16 cache holding the same values, and as
- * bi_attention_decode_int4 of each token's cut sequence.
+ * bi_attention_decode_int4 of each token's cut sequence, and as
+ * bi_attention_extend over a bf16 cache holding the same values (but a value
+ * that is not finite reaches only the tokens that see it).
  *   workspace  caller-owned device scratch, NULLABLE. With at least
  *              bi_attention_extend_int4_workspace_size(...) > 0 bytes, calls
  *              with few new tokens (drafts to verify, a short prompt after a

@@ -675,6 +675,7 @@ attn_extend_kernel(const ExtParams p) {
     uint8_t *KV = smem;                                                    // [2][K, V] tiles, swizzled rows
     uint16_t *qb = reinterpret_cast<uint16_t *>(smem + 4 * kTileBytes);   // [kExtRows][kD] bf16
     int64_t *rowoff = reinterpret_cast<int64_t *>(qb + kExtRows * kD);     // [kRowBufs][kChunk], -1: no row
+    __shared__ int nan_from[kI4Scales];                // I4: per 32 dimensions, the first such token (expand_chunk)
     uint8_t *stage = reinterpret_cast<uint8_t *>(rowoff + kRowBufs * kChunk); // I4: [2][K codes, V codes, K, V scales]
     // blockIdx.x = (tile from the last, sequence, KV head): the tiles with the
     // latest tokens (the most chunks) of every sequence start first, so the
@@ -772,7 +773,10 @@ attn_extend_kernel(const ExtParams p) {
     };
     // I4: chunk c's staged codes to the bf16 tile. A thread takes one row's 32
     // dimensions of a scale at a time: the word of dimensions 2a, 2a + 1 mod 8
-    // gives their pairs at the four 16-byte pieces of those dimensions.
+    // gives their pairs at the four 16-byte pieces of those dimensions. A value
+    // that is not finite, of a token that the tile's first row does not see,
+    // must not reach that row as 0 * NaN: the tile holds 0 in its place, and the
+    // rows that see the token become NaN at the end.
     auto expand_chunk = [&](int c) {
         const uint8_t *st = stage + (c & 1) * kI4Stage;
 #pragma unroll
@@ -782,8 +786,12 @@ attn_extend_kernel(const ExtParams p) {
             for (int r = 0; r < kChunk * 4 / kExtThreads; ++r) {
                 const int t = (tid + r * kExtThreads) >> 2, i = tid & 3;
                 const uint8_t *codes = st + which * kI4StageCodes + t * kI4Row;
-                const uint32_t sc = *reinterpret_cast<const uint16_t *>(st + 2 * kI4StageCodes + which * kI4StageScales +
-                                                                        t * kI4Scales * 2 + 2 * i);
+                uint32_t sc = *reinterpret_cast<const uint16_t *>(st + 2 * kI4StageCodes + which * kI4StageScales +
+                                                                  t * kI4Scales * 2 + 2 * i);
+                if (which == 1 && !i4_finite(sc) && c * kChunk + t > base + i0) {
+                    sc = 0;
+                    atomicMin(&nan_from[i], c * kChunk + t);
+                }
                 const uint32_t s2 = sc | (sc << 16), c2 = mul_bf16x2(s2, kBf16x2_m136);
                 const uint4 seg = *reinterpret_cast<const uint4 *>(codes + 16 * i);
                 uint32_t v[4][4];                      // [a][q]
@@ -797,6 +805,7 @@ attn_extend_kernel(const ExtParams p) {
             }
         }
     };
+    if (I4 && tid < kI4Scales) nan_from[tid] = 0x7FFFFFFF;
     // q rows and chunk 0's row offsets; bad_cur: chunk c has a token without a valid block
     int bad_cur = __syncthreads_or(chunk_rows(0)), bad_two = 0;
     issue_chunk(0);
@@ -1042,8 +1051,9 @@ attn_extend_kernel(const ExtParams p) {
         uint16_t *orow = p.O + ((q0 + i0 + r / G) * p.Hq + g * G + r % G) * kD + 2 * cq;
 #pragma unroll
         for (int nt = 0; nt < kD / 8; ++nt) {
-            const float x0 = __fdiv_rn(o_run[nt][2 * h], l_run[h]);
-            const float x1 = __fdiv_rn(o_run[nt][2 * h + 1], l_run[h]);
+            float x0 = __fdiv_rn(o_run[nt][2 * h], l_run[h]);
+            float x1 = __fdiv_rn(o_run[nt][2 * h + 1], l_run[h]);
+            if (I4 && nan_from[nt / 4] < (h ? len_b : len_a)) x0 = x1 = __int_as_float(0x7FFFFFFF);
             *reinterpret_cast<uint32_t *>(orow + nt * 8) = pack_bf16x2(__float_as_uint(x0), __float_as_uint(x1));
         }
     }

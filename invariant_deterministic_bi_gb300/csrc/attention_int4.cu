@@ -416,7 +416,19 @@ attn_split_int4_kernel(const SplitParams p) {
             if (nxt.n) staged<BLOCKS>(barK, parity ^ 1);
             return;
         }
-        if (!cur.whole && BLOCKS) {                        // a token without a row must not bring a NaN to 0 * v
+        // a token that some row does not see must not bring it a NaN (0 * v): the groups of tokens see0 .. see0 + 7 that
+        // are not finite (bit 4 (t - see0) + i) become zeros here, and NaN in the rows that see them below
+        uint32_t nans = 0;
+        if (kTQ > 1 && cur.ntok > 1 && !cur.whole) {
+            const int t = cur.see0 + (lane >> 2);
+            uint16_t *s1 = reinterpret_cast<uint16_t *>(Vs + kCodeBytes) + t * kI4Scales + (lane & 3);
+            const uint32_t valid = t < 64 ? (t < 32 ? cur.valid[0] : cur.valid[1]) : (t < 96 ? cur.valid[2] : cur.valid[3]);
+            const bool nan = t >= 0 && t < cur.n && ((valid >> (t & 31)) & 1) && !i4_finite(*s1);
+            nans = __ballot_sync(0xffffffffu, nan);
+            if (nan) *s1 = 0;
+            if (nans) __syncwarp();
+        }
+        if (!cur.whole && BLOCKS) {                        // nor one without a row
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (!((cur.valid[k] >> lane) & 1))
@@ -450,6 +462,13 @@ attn_split_int4_kernel(const SplitParams p) {
                 mma_16816(o[2 * i], a[0][0], a[0][1], a[1][0], a[1][1], pl[ks][0], pl[ks][1]);
                 mma_16816(o[2 * i + 1], a[0][2], a[0][3], a[1][2], a[1][3], pl[ks][0], pl[ks][1]);
             }
+        }
+        if (kTQ > 1 && nans) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int j = 0; j < kD / 16; ++j)
+                    if (nans & (0x11111111u << (j / 2)) & ((1u << (4 * ((2 * cq + e) / G))) - 1u)) o[j][e] = o[j][2 + e] = __int_as_float(0x7FFFFFFF);
         }
         __syncwarp();                                      // every lane has read V
         if (nxt.n)

@@ -66,6 +66,9 @@ __device__ __forceinline__ uint32_t dup16(uint32_t w) { return __byte_perm(w, 0,
 template <int HI>
 __device__ __forceinline__ uint32_t zip16(uint32_t a, uint32_t b) { return __byte_perm(a, b, HI ? 0x7632 : 0x5410); }
 
+// Whether a group with this scale holds numbers (else its values are NaN).
+__device__ __forceinline__ bool i4_finite(uint16_t scale) { return (scale & 0x7F80u) != 0x7F80u; }
+
 // Place of segment i in the code row of a token at this offset of its block.
 __device__ __forceinline__ int i4_place(int i, int offset) { return i ^ ((offset >> 1) & 3); }
 

@@ -339,3 +339,43 @@ def test_step_in_a_graph_and_on_a_side_stream(bi):
         side.synchronize()
         assert torch.equal(got, want[i]), i
     assert bi.device_status() == bi.BI_OK
+
+
+@pytest.mark.parametrize("Hq,Hkv,bs", [(4, 4, 16), (4, 2, 24), (8, 2, 1), (16, 2, 8)])
+def test_non_finite_rows_reach_only_the_tokens_that_see_them(bi, Hq, Hkv, bs):
+    """Among the new tokens some values and keys are infinite or NaN: every token still has the bits of decode of the
+    sequence cut after it, split over the chunks or tiled."""
+    import torch
+    lens, qlens = [50, 300, 260, 9, 129], [20, 130, 7, 9, 3]
+    Q, c, Kh, Vh, table, ld = make(bi, lens, bs, Hq, Hkv, seed=91, q_rows=sum(qlens))
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(qlens)]), dtype=torch.int32, device="cuda")
+    bad = float("nan"), float("inf"), -float("inf")
+    for b, (L, n) in enumerate(zip(lens, qlens)):      # new tokens 1, 4, 5 and, where there are more, 17, 100 and the last
+        for i, j in enumerate(t for t in (1, 4, 5, 17, 100, n - 1) if t < n):
+            j += L - n
+            k = torch.ones((1, Hkv, D), dtype=torch.bfloat16, device="cuda")
+            v = k.clone()
+            v[0, i % Hkv, 32 * (i % 4) + 5] = bad[i % 3]
+            if i == 2:
+                k[0, 0, 70] = bad[b % 3]
+            bi.kv_int4_append(k, v, (table[b, j // bs].long() * bs + j % bs).reshape(1), c)
+    want = torch.empty_like(Q)
+    for b, (L, n) in enumerate(zip(lens, qlens)):
+        for i in range(n):
+            cut = torch.tensor([L - n + i + 1], dtype=torch.int32, device="cuda")
+            r = int(cu[b]) + i
+            want[r:r + 1] = bi.attention_decode_int4(Q[r:r + 1], c, table[b:b + 1].contiguous(), cut, 300, SCALE)
+    assert bool(torch.isnan(want).any()) and bool(torch.isfinite(want).any())
+    need = bi.attention_decode_workspace_size(sum(qlens), Hq, 300)
+    for ws in (torch.empty(need, dtype=torch.uint8, device="cuda"), torch.empty(16, dtype=torch.uint8, device="cuda")):
+        got = bi.attention_extend_int4(Q, cu, c, table, ld, 300, max(qlens), SCALE, workspace=ws)
+        assert np.array_equal(bits_of(got), bits_of(want))
+    # the few new tokens of sequences 2 and 4 alone, which are split
+    few = [2, 4]
+    rows = torch.cat([torch.arange(int(cu[b]), int(cu[b + 1]), device="cuda") for b in few])
+    cu2 = torch.tensor([0, 7, 10], dtype=torch.int32, device="cuda")
+    q2, t2, l2 = Q[rows].contiguous(), table[few].contiguous(), ld[few].contiguous()
+    assert bi.attention_extend_int4_workspace_size(10, Hq, Hkv, 300, 7) > 0
+    got = bi.attention_extend_int4(q2, cu2, c, t2, l2, 300, 7, SCALE)
+    assert np.array_equal(bits_of(got), bits_of(want[rows]))
+    assert bi.device_status() == bi.BI_OK
