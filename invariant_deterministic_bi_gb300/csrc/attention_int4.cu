@@ -68,6 +68,7 @@ struct SplitParams {
     int64_t batch;
     int32_t total_q, max_q, tiles;   // extend: query rows, a sequence's most, its tiles of 8 / G tokens
     int32_t max_blocks, Hq, chunks, max_len;
+    bool scan;               // look for the longest sequence first
     float scale;
     unsigned *status;
 };
@@ -266,7 +267,17 @@ attn_split_int4_kernel(const SplitParams p) {
     grid_dep_launch();
     uint8_t *Ks = smem + warp * kWarpBytes, *Vs = Ks + kHalfBytes;
     const int64_t ws_head = static_cast<int64_t>(p.chunks) * kRecord;   // next query head's records
-    // the walk: `step` items on, digit by digit
+    // the walk over (sequence, chunk, tile, head), as far as the longest sequence's last chunk where that is looked
+    // for; `step` items on, digit by digit
+    int chunks = p.chunks;
+    if (p.scan) {
+        int longest = 1;
+        for (int64_t b = lane; b < p.batch; b += 32) {
+            const int L = p.lens[b];
+            if (L <= p.max_len) longest = max(longest, L);
+        }
+        chunks = (__reduce_max_sync(0xffffffffu, longest) + kChunk - 1) / kChunk;
+    }
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
     auto split = [&](int64_t i) {
         Cursor u;
@@ -274,8 +285,8 @@ attn_split_int4_kernel(const SplitParams p) {
         i /= p.c.Hkv;
         u.tile = EXT ? static_cast<int>(i % p.tiles) : 0;
         if (EXT) i /= p.tiles;
-        u.c = static_cast<int>(i % p.chunks);
-        u.b = i / p.chunks;
+        u.c = static_cast<int>(i % chunks);
+        u.b = i / chunks;
         return u;
     };
     Cursor u = split(blockIdx.x + static_cast<int64_t>(gridDim.x) * warp);
@@ -291,8 +302,8 @@ attn_split_int4_kernel(const SplitParams p) {
                 carry = (u.tile += step.tile + carry) >= p.tiles;
                 if (carry) u.tile -= p.tiles;
             }
-            carry = (u.c += step.c + carry) >= p.chunks;
-            if (carry) u.c -= p.chunks;
+            carry = (u.c += step.c + carry) >= chunks;
+            if (carry) u.c -= chunks;
             u.b += step.b + carry;
         }
         return x;
@@ -621,6 +632,10 @@ bi_status launch_few(SplitParams &p, cudaStream_t s) {
     p.chunks = static_cast<int32_t>((static_cast<int64_t>(p.max_len) + kChunk - 1) / kChunk);
     p.status = device_status_word();
     const int64_t items = p.batch * p.tiles * p.c.Hkv * static_cast<int64_t>(p.chunks);
+    // Where the maximum length would make a walk of many steps (each some 450 cycles if there is nothing to do), a warp
+    // first reads all lengths: 64 sequences of 1000 tokens, 32 heads over 8, maximum 131072: 96 us without this
+    // and the merge's room below, 49 with this, 31 with both (29 at a maximum of 1000).
+    p.scan = items >= 16 * static_cast<int64_t>(kMaxWarps) * info->sm_count && p.chunks * static_cast<int64_t>(p.tiles) * p.c.Hkv >= 64;
     const int64_t merges = p.batch * (EXT ? p.max_q : 1) * p.Hq;
     if (merges > 0x7FFFFFFF) return BI_ERR_UNSUPPORTED;
     // Block sizes that are multiples of eight can be copied as they lie (64 x 4096 tokens, blocks of 16: 91 us; by
@@ -640,7 +655,13 @@ bi_status launch_few(SplitParams &p, cudaStream_t s) {
     static unsigned long long configured = 0;
     if (ensure_smem_attr(reinterpret_cast<const void *>(attn_merge_int4_kernel<EXT>), kMergeRing * kMergeStage, &configured) != BI_OK)
         return BI_ERR_CUDA;
-    const int tiles = (p.chunks + kMergeTile - 1) / kMergeTile, ring = tiles < kMergeRing ? tiles : kMergeRing;
+    // Tiles on the way: as many as leave room for the other CTAs of the SM, up to six of them (256 sequences of 300
+    // tokens, maximum 131072: 57 us for both kernels; with eight tiles, one CTA an SM, 135).
+    const int64_t per_sm = (merges + info->sm_count - 1) / info->sm_count;
+    const int tiles = (p.chunks + kMergeTile - 1) / kMergeTile;
+    const int room = info->max_smem_optin / (kMergeStage + 1024) / static_cast<int>(per_sm < 6 ? per_sm : 6);
+    int ring = tiles < kMergeRing ? tiles : kMergeRing;
+    if (ring > room) ring = room;
     return launch_pdl(attn_merge_int4_kernel<EXT>, dim3(static_cast<unsigned>(merges)), dim3(kMergeThreads + 32), ring * kMergeStage, s,
                       p, ring);
 }

@@ -281,3 +281,57 @@ def test_extend_with_a_generous_most_new_tokens(bi, most):
     want = bi.attention_extend_int4(q, cu, c, table, lens, 128, 5, SCALE, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert torch.equal(bi.attention_extend_int4(q, cu, c, table, lens, 128, most, SCALE), want)
     assert bi.device_status() == bi.BI_OK
+
+
+def test_generous_maximum_length_of_many(bi):
+    """Enough room under the maximum length that the lengths are read first; among them one of 0 and one past it."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(5)
+    B, top = 40, 200_000
+    c = bi.kv_int4_cache(64, 16, 2)
+    K = torch.randn((1024, 2, D), device="cuda", generator=g).to(torch.bfloat16)
+    bi.kv_int4_append(K, K, torch.arange(1024, device="cuda"), c)
+    lens = torch.randint(1, 520, (B,), device="cuda", generator=g).int()
+    lens[0], lens[39] = 1, 520
+    wide = torch.zeros((B, top // 16), dtype=torch.int32, device="cuda")
+    wide[:, :33] = torch.randint(0, 64, (B, 33), device="cuda", generator=g).int()
+    table = wide[:, :33].contiguous()
+    q = torch.randn((B, 8, D), device="cuda", generator=g).to(torch.bfloat16)
+    a = bi.attention_decode_int4(q, c, table, lens, 520, SCALE)
+    assert torch.equal(a, bi.attention_decode_int4(q, c, wide, lens, top, SCALE))
+    assert bi.device_status() == bi.BI_OK
+    lens[7], lens[8] = 0, top + 1
+    o = torch.full_like(a, 7.0)
+    bi.attention_decode_int4(q, c, wide, lens, top, SCALE, O=o)
+    assert bi.device_status() == bi.BI_ERR_INVALID_ARG
+    assert bool((o[7:9] == 7).all())
+    keep = [b for b in range(B) if b not in (7, 8)]
+    assert torch.equal(o[keep], a[keep])
+
+
+def test_results_made_on_another_stream(bi):
+    """Outputs and workspaces that a call on another stream allocates: not the memory of work still queued on the
+    current stream, and not reused before the current stream has read them."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(6)
+    X = torch.randn((64, 4096), device="cuda", generator=g).bfloat16()
+    W = torch.randint(0, 256, (2048, 2048), dtype=torch.uint8, device="cuda", generator=g)
+    S = torch.rand((2048, 32), device="cuda", generator=g).bfloat16()
+    S_neg = S.neg()
+    want = bi.gemm_int4(X, W, S)
+    side = torch.cuda.Stream()
+    big = torch.randn((8192, 8192), device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(4):
+        before = torch.full((64, 2048), 3.0, device="cuda", dtype=torch.bfloat16)
+        (big @ big)                                        # keeps the current stream busy
+        copy = before + 1
+        del before                                         # free for the current stream, still to be read there
+        y = bi.gemm_int4(X, W, S, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        (big @ big)
+        got = y + 0
+        del y                                              # free, still to be read by the current stream
+        z = bi.gemm_int4(X, W, S_neg, stream=side)
+        torch.cuda.synchronize()
+        assert bool((copy == 4).all()) and torch.equal(got, want) and torch.equal(z, -want)
