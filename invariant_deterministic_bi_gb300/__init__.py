@@ -483,11 +483,14 @@ def _launch_on(cache, tensors, stream):
 
 
 def _new(shape, dtype, like, stream):
-    """An uninitialised tensor that stays allocated until the work of `stream` that uses it is done."""
+    """An uninitialised tensor of `stream` (None: the current one), which the current stream may use as well."""
     import torch
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        t.record_stream(stream)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    current = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(current)
     return t
 
 
