@@ -117,8 +117,11 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
 
 // Where lane (g, c) finds its operands among KB staged k, GS k a scale: word j of
 // group `sub` holds k = GS sub + (GS / 4) c + 8 j and the seven after it. Weight
-// rows are KB / 2 bytes with the TMA's swizzle of that width, rows of X boxes of 64 k,
-// swizzled (X_SWIZZLED) or as they are.
+// rows are KB / 2 bytes with the TMA's swizzle of that width, rows of X boxes of 64 k
+// with the 128-byte swizzle, which goes by the address: a 16-byte piece is exchanged
+// by the address's 128-byte line modulo 8. Boxes lie x_stride apart, which is 2 or 6
+// lines modulo 8 (1 where X has one row): the pieces that eight lanes load at once, of
+// two rows and (GS = 128) two boxes, are then in all the banks.
 template <int GS, int KB>
 __device__ __forceinline__ void load_words(uint32_t w_row, int row, int sub, int cq, uint32_t (&w)[GS / 32]) {
     const int byte = GS / 2 * sub + GS / 8 * cq;
@@ -130,12 +133,19 @@ __device__ __forceinline__ void load_words(uint32_t w_row, int row, int sub, int
     else
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at));
 }
-// The B operands of word j: (b0, b1) of its two steps. `rows` rows of X a box.
-template <int GS, bool X_SWIZZLED>
-__device__ __forceinline__ void load_x(uint32_t x_tile, int rows, int row, int sub, int cq, int j, uint32_t (&b)[4]) {
-    const int k = GS * sub + GS / 4 * cq + 8 * j;
+// Bytes between the boxes of X: of `rows` rows, and two more lines where four rows or more make their number 4 or 0
+// modulo 8.
+__host__ __device__ constexpr int x_box(int rows) { return rows * 128 + (rows >= 4 ? 256 : 0); }
+// Address of word 0's piece of X (x_tile begins at a multiple of 1024).
+template <int GS>
+__device__ __forceinline__ uint32_t x_piece(uint32_t x_tile, int x_stride, int row, int sub, int cq) {
+    const int k = GS * sub + GS / 4 * cq, line = (k >> 6) * (x_stride >> 7) + row;
+    return x_tile + line * 128 + ((((k >> 3) ^ line) & 7) << 4);
+}
+// The B operands of word j: (b0, b1) of its two steps.
+__device__ __forceinline__ void load_x(uint32_t piece, int j, uint32_t (&b)[4]) {
     uint32_t x0, x1, x2, x3;
-    ld_shared_v4(x_tile + ((k >> 6) * rows + row) * 128 + ((((k >> 3) ^ (X_SWIZZLED ? row : 0)) & 7) << 4), x0, x1, x2, x3);
+    ld_shared_v4(piece ^ (j << 4), x0, x1, x2, x3);
     b[0] = zip16<0>(x0, x2), b[1] = zip16<1>(x0, x2), b[2] = zip16<0>(x1, x3), b[3] = zip16<1>(x1, x3);
 }
 __device__ __forceinline__ void expand_weights(uint32_t w, uint32_t z2, uint32_t (&a)[4]) {
@@ -163,17 +173,19 @@ struct GroupCursor {
 };
 
 // acc += KB staged k, each group scaled, for weight rows row0 .. row0 + 16 MR - 1 of
-// the staged ROWS and 8 NT rows of X from x_row0 of the staged x_rows (x_mask: rows
-// that are not there repeat others; their columns are not stored). `g`: the first
-// group; k_left: k from the first one to K's end.
-template <int GS, int KB, int MR, int NT, int ROWS, bool X_SWIZZLED, bool ZEROS>
-__device__ __forceinline__ void product(uint32_t w_tile, uint32_t x_tile, const uint8_t *sc, int row0, int x_rows, int x_row0, int x_mask,
+// the staged ROWS and 8 NT rows of X from x_row0 (x_mask: rows that are not there
+// repeat others; their columns are not stored). `g`: the first group; k_left: k from
+// the first one to K's end.
+template <int GS, int KB, int MR, int NT, int ROWS, bool ZEROS>
+__device__ __forceinline__ void product(uint32_t w_tile, uint32_t x_tile, const uint8_t *sc, int row0, int x_stride, int x_row0, int x_mask,
                                         int groups, const GroupCursor<GS> &g, int k_left, int gq, int cq,
                                         float (&acc)[MR][NT][4]) {
     constexpr int kSub = KB / GS;
 #pragma unroll
     for (int sub = 0; sub < kSub; ++sub) {
-        uint32_t w[MR][2][GS / 32];
+        uint32_t w[MR][2][GS / 32], xp[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) xp[t] = x_piece<GS>(x_tile, x_stride, x_row0 + 8 * t + (gq & x_mask), sub, cq);
         float s[MR][2];
         uint32_t z2[MR][2];
         float part[MR][NT][4];
@@ -198,7 +210,7 @@ __device__ __forceinline__ void product(uint32_t w_tile, uint32_t x_tile, const 
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 uint32_t b[4];
-                load_x<GS, X_SWIZZLED>(x_tile, x_rows, x_row0 + 8 * t + (gq & x_mask), sub, cq, j, b);
+                load_x(xp[t], j, b);
 #pragma unroll
                 for (int m = 0; m < MR; ++m) {
                     if (j == 0)
@@ -242,7 +254,7 @@ template <int NT>
 constexpr int rows_sums() { return rows_n<NT>() * (8 * NT + 1); }   // floats of a segment's sums
 template <int GS, int NT>
 constexpr int rows_stage(int x_rows) {
-    return rows_w<NT>() + (x_rows * rows_kb<NT>() * 2 + ScaleTile<GS, rows_kb<NT>()>::bytes(rows_n<NT>()) + 1023) / 1024 * 1024;
+    return rows_w<NT>() + (rows_kb<NT>() / 64 * x_box(x_rows) + ScaleTile<GS, rows_kb<NT>()>::bytes(rows_n<NT>()) + 1023) / 1024 * 1024;
 }
 template <int NT>
 constexpr int rows_buffers() { return NT == 1 ? 2 : 1; }       // of the sums
@@ -254,7 +266,7 @@ __global__ void __launch_bounds__(32 * kMaxSegments * NT, NT == 1 ? 2 : 1)
 gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmI4Params p) {
     constexpr int KB = rows_kb<NT>(), kBlocks = KB / kBlockK, kW = rows_w<NT>(), kCols = 8 * NT + 1, kSums = rows_sums<NT>();
     constexpr int kN = rows_n<NT>(), kBuffers = rows_buffers<NT>();
-    const int x_bytes = p.x_rows * KB * 2, stage_bytes = rows_stage<GS, NT>(p.x_rows);
+    const int x_stride = x_box(p.x_rows), x_bytes = KB / 64 * x_stride, stage_bytes = rows_stage<GS, NT>(p.x_rows);
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ uint64_t full[kMaxSegments][kRing], empty[kMaxSegments][kRing];
@@ -293,11 +305,11 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         uint8_t *dst = ring + fs * stage_bytes;
         uint64_t *bar = &full[seg][fs];
         if (lane == 0) {
-            mbar_arrive_expect_tx(bar, kW + x_bytes);
+            mbar_arrive_expect_tx(bar, kW + p.x_rows * KB * 2);
             tma_load_2d(dst, &tmW, bar, fb * (KB / 2), ft * kN);
 #pragma unroll
             for (int k = 0; k < KB / 64; ++k)
-                tma_load_2d(dst + kW + k * (x_bytes / (KB / 64)), &tmX, bar, fb * KB + 64 * k, 0);
+                tma_load_2d(dst + kW + k * x_stride, &tmX, bar, fb * KB + 64 * k, 0);
         }
         stage_scales<GS, KB, kN, 32, ZEROS>(p, smem_u32(dst + kW + x_bytes), bar, row_e + fg.group, lane);
         if (++fs == kRing) fs = 0;
@@ -324,7 +336,7 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
             __syncwarp();
             if (!ok) break;
             const uint8_t *st = ring + slot * stage_bytes;
-            product<GS, KB, 2, NT, kN, false, ZEROS>(smem_u32(st), smem_u32(st) + kW, st + kW + x_bytes, 32 * wn, p.x_rows, 0,
+            product<GS, KB, 2, NT, kN, ZEROS>(smem_u32(st), smem_u32(st) + kW, st + kW + x_bytes, 32 * wn, x_stride, 0,
                                                      NT == 1 ? p.x_rows - 1 : 7, p.groups, g, p.K - blk * KB, gq, cq, acc);
             for (int k = 0; k < kBlocks; ++k) g.next(p);
             __syncwarp();                                  // every lane has read the slot
@@ -369,7 +381,7 @@ constexpr int kTileN = 128;                    // weight rows of a CTA
 constexpr int kTileThreads = 256;              // warps: four of 32 weight rows x two of TM / 2 rows of X
 constexpr int kTileW = kTileN * (kBlockK / 2); // 8 KB a stage
 template <int TM>
-constexpr int tile_stage() { return kTileW + TM * kBlockK * 2; }
+constexpr int tile_stage() { return kTileW + (2 * x_box(TM) + 1023) / 1024 * 1024; }
 template <int TM>
 constexpr int tile_stages() { return TM == 64 ? 3 : 5; }
 template <int GS, int TM>
@@ -408,10 +420,10 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         const int slot = (blk - first) % kTileStages;
         uint8_t *dst = smem + slot * kTileStage;
         if (tid == 0) {
-            mbar_arrive_expect_tx(&full[slot], kTileStage);
+            mbar_arrive_expect_tx(&full[slot], kTileW + kTileM * kBlockK * 2);
             tma_load_2d(dst, &tmW, &full[slot], blk * (kBlockK / 2), static_cast<int32_t>(n0));
             tma_load_2d(dst + kTileW, &tmX, &full[slot], blk * kBlockK, static_cast<int32_t>(m0));
-            tma_load_2d(dst + kTileW + kTileM * 128, &tmX, &full[slot], blk * kBlockK + 64, static_cast<int32_t>(m0));
+            tma_load_2d(dst + kTileW + x_box(kTileM), &tmX, &full[slot], blk * kBlockK + 64, static_cast<int32_t>(m0));
         }
         stage_scales<GS, kBlockK, kTileN, kTileThreads, ZEROS>(p, smem_u32(scales + slot * kScaleBytes), &full[slot], n0 * p.groups + fg.group, tid);
         fg.next(p);
@@ -443,7 +455,7 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         }
         if (blk + kTileStages - 1 < last) fill(blk + kTileStages - 1);
         const uint32_t st = smem_u32(smem + slot * kTileStage);
-        product<GS, kBlockK, MR, NT, kTileN, true, ZEROS>(st, st + kTileW, scales + slot * kScaleBytes, 16 * MR * wn, kTileM, 8 * NT * wm, 7,
+        product<GS, kBlockK, MR, NT, kTileN, ZEROS>(st, st + kTileW, scales + slot * kScaleBytes, 16 * MR * wn, x_box(kTileM), 8 * NT * wm, 7,
                                                           p.groups, g, p.K - blk * kBlockK, gq, cq, acc);
         g.next(p);
         if (!SPLIT && blk + 1 == seg_end) {
@@ -568,7 +580,7 @@ bi_status launch_group(const void *X, int64_t ldx, const uint8_t *W, GemmI4Param
     if (make_tmap_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, p.K / 2, p.N, p.K / 2, (rows ? kb : kBlockK) / 2, rows ? (p.M <= 8 ? rows_n<1>() : rows_n<2>()) : kTileN,
                      rows && kb == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) != BI_OK ||
         make_tmap_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, p.K, p.M, ldx * 2, 64, rows ? p.x_rows : tm,
-                     rows ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B) != BI_OK)
+                     CU_TENSOR_MAP_SWIZZLE_128B) != BI_OK)
         return BI_ERR_CUDA;
     if (rows) return p.M <= 8 ? launch_rows<GS, 1, ZEROS>(tmW, tmX, p, sms, s) : launch_rows<GS, 2, ZEROS>(tmW, tmX, p, sms, s);
     if (tm == 32) return launch_tiles<GS, 32, ZEROS>(tmW, tmX, p, sms, s);
