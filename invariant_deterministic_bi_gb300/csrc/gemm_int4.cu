@@ -74,24 +74,23 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Starts the copies of a block's scales and zeros for ROWS weight rows by THREADS
-// threads, each of which arrives on the barrier once its copies have landed.
-// e0: element (row n0, the first group) of the arrays. Words past the
-// arrays (rows past N, groups past K) repeat the last one.
-template <int GS, int KB, int ROWS, int THREADS, bool ZEROS>
-__device__ __forceinline__ void stage_scales(const GemmI4Params &p, uint32_t dst, uint64_t *bar, int64_t e0, int thread) {
+// Starts the copies of a block's scales and zeros for ROWS weight rows (of a tile of TILE) by THREADS threads, each of
+// which arrives on the barrier once its copies have landed. row: the first of the rows in the tile; e0: its element of
+// the first group in the arrays. Words past the arrays (rows past N, groups past K) repeat the last one.
+template <int GS, int KB, int ROWS, int TILE, int THREADS, bool ZEROS>
+__device__ __forceinline__ void stage_scales(const GemmI4Params &p, uint32_t dst, uint64_t *bar, int row, int64_t e0, int thread) {
     using T = ScaleTile<GS, KB>;
 #pragma unroll
     for (int i = 0; i < (ROWS * T::kSWords + THREADS - 1) / THREADS; ++i) {
         const int v = thread + i * THREADS, r = v / T::kSWords, w = v % T::kSWords;
-        if (v < ROWS * T::kSWords) cp_async_4(dst + v * 4, p.S + min(((e0 + r * p.groups) >> 1) + w, p.s_last));
+        if (v < ROWS * T::kSWords) cp_async_4(dst + (row * T::kSWords + v) * 4, p.S + min(((e0 + r * p.groups) >> 1) + w, p.s_last));
     }
     if (ZEROS) {
 #pragma unroll
         for (int i = 0; i < (ROWS * T::kZWords + THREADS - 1) / THREADS; ++i) {
             const int v = thread + i * THREADS, r = v / T::kZWords, w = v % T::kZWords;
             if (v < ROWS * T::kZWords)
-                cp_async_4(dst + (ROWS * T::kSWords + v) * 4, p.Z + min(((e0 + r * p.groups) >> 2) + w, p.z_last));
+                cp_async_4(dst + (TILE * T::kSWords + row * T::kZWords + v) * 4, p.Z + min(((e0 + r * p.groups) >> 2) + w, p.z_last));
         }
     }
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -276,7 +275,7 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     float *sums = reinterpret_cast<float *>(smem + p.segments * kRing * stage_bytes);   // [kBuffers][segments][kSums]
     if (wn == 0 && lane == 0) {
         for (int k = 0; k < kRing; ++k) {
-            mbar_init(&full[seg][k], 33);                  // 32 lanes' scale copies, and the TMA's bytes
+            mbar_init(&full[seg][k], 32 * NT + 1);         // the lanes' scale copies, and the TMA's bytes
             mbar_init(&empty[seg][k], NT);
         }
         fence_mbar_init();
@@ -295,29 +294,29 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     const int u1 = static_cast<int>(static_cast<int64_t>(seg + 1) * p.units / p.segments);
     const int b1 = KB == kUnitK ? u1 : min(p.blocks, 2 * u1);
     const GroupCursor<GS> g0(p, b0 * kBlocks);
-    // the next stage to be copied (by the segment's first warp), its group, and its slot
+    // the next stage to be copied (W and X by the segment's first warp, scales by each warp its rows'), its group, and
+    // its slot
     int ft = blockIdx.x, fb = b0, fs = 0;
     GroupCursor<GS> fg = g0;
-    int64_t row_e = static_cast<int64_t>(ft) * kN * p.groups;   // element (the tile's first row, group 0)
+    int64_t row_e = (static_cast<int64_t>(ft) * kN + 32 * wn) * p.groups;   // element (the warp's first row, group 0)
     const int64_t step_e = static_cast<int64_t>(gridDim.x) * kN * p.groups;
     auto fill = [&]() {
         if (ft >= tiles) return;
         uint8_t *dst = ring + fs * stage_bytes;
         uint64_t *bar = &full[seg][fs];
-        if (lane == 0) {
+        if (wn == 0 && lane == 0) {
             mbar_arrive_expect_tx(bar, kW + p.x_rows * KB * 2);
             tma_load_2d(dst, &tmW, bar, fb * (KB / 2), ft * kN);
 #pragma unroll
             for (int k = 0; k < KB / 64; ++k)
                 tma_load_2d(dst + kW + k * x_stride, &tmX, bar, fb * KB + 64 * k, 0);
         }
-        stage_scales<GS, KB, kN, 32, ZEROS>(p, smem_u32(dst + kW + x_bytes), bar, row_e + fg.group, lane);
+        stage_scales<GS, KB, 32, kN, 32, ZEROS>(p, smem_u32(dst + kW + x_bytes), bar, 32 * wn, row_e + fg.group, lane);
         if (++fs == kRing) fs = 0;
         for (int k = 0; k < kBlocks; ++k) fg.next(p);
         if (++fb == b1) fb = b0, fg = g0, ft += gridDim.x, row_e += step_e;
     };
-    if (wn == 0)
-        for (int k = 0; k < kRing; ++k) fill();
+    for (int k = 0; k < kRing; ++k) fill();
     int slot = 0, buf = 0;
     uint32_t parity = 0;
     bool ok = true;
@@ -344,7 +343,7 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                 if (lane == 0) mbar_arrive(&empty[seg][slot]);
                 if (wn == 0) ok = __all_sync(0xffffffffu, mbar_wait(&empty[seg][slot], parity, nullptr));
             }
-            if (wn == 0 && ok) fill();
+            if (ok) fill();
             if (++slot == kRing) slot = 0, parity ^= 1;
         }
         // the segments' sums, added in order
@@ -367,6 +366,7 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         if (kBuffers == 1) __syncthreads();
     }
     if (!ok && lane == 0) atomicOr(p.status, kDevTimeout);
+    if (!ok) asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok && wn == 0) {                                  // a wait ran out: the copies in flight get another limit
         for (int k = 0; k < kRing; ++k) {
             mbar_wait(&full[seg][slot], parity, nullptr);
@@ -425,7 +425,7 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
             tma_load_2d(dst + kTileW, &tmX, &full[slot], blk * kBlockK, static_cast<int32_t>(m0));
             tma_load_2d(dst + kTileW + x_box(kTileM), &tmX, &full[slot], blk * kBlockK + 64, static_cast<int32_t>(m0));
         }
-        stage_scales<GS, kBlockK, kTileN, kTileThreads, ZEROS>(p, smem_u32(scales + slot * kScaleBytes), &full[slot], n0 * p.groups + fg.group, tid);
+        stage_scales<GS, kBlockK, kTileN, kTileN, kTileThreads, ZEROS>(p, smem_u32(scales + slot * kScaleBytes), &full[slot], 0, n0 * p.groups + fg.group, tid);
         fg.next(p);
     };
     for (int blk = first; blk < last && blk < first + kTileStages - 1; ++blk) fill(blk);
