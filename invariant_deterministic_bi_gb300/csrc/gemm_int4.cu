@@ -97,14 +97,14 @@ __device__ __forceinline__ void stage_scales(const GemmI4Params &p, uint32_t dst
 }
 
 // (scale as fp32, -(128 + z) as a bf16 pair) of a staged row and its `at`-th staged group. `e` is the element of
-// (row, the first staged group) modulo 4: tiles begin at multiples of 16 rows, so row * groups + group will do.
+// (row, the first staged group) modulo 4: tiles begin at multiples of 16 rows, so (row % 8) * groups + group will do.
 template <int GS, int KB, int ROWS, bool ZEROS>
 __device__ __forceinline__ void read_scale(const uint8_t *tile, int row, int e, int at, bool in, float &s, uint32_t &z2) {
     using T = ScaleTile<GS, KB>;
     const uint32_t bits = *reinterpret_cast<const uint16_t *>(tile + row * T::kSWords * 4 + (e & 1) * 2 + at * 2);
     s = in ? __uint_as_float(bits << 16) : 0.0f;
     z2 = kBf16x2_m136;
-    if (ZEROS) z2 = 0xC300C300u | ((tile[(ROWS * T::kSWords + row * T::kZWords) * 4 + (e & 3) + at] & 15u) * 0x00010001u);
+    if (ZEROS) z2 = __byte_perm(tile[(ROWS * T::kSWords + row * T::kZWords) * 4 + (e & 3) + at] & 15u, 0xC3u, 0x4040);
 }
 
 // The first product of a chain: D = A B.
@@ -180,6 +180,7 @@ __device__ __forceinline__ void product(uint32_t w_tile, uint32_t x_tile, const 
                                         int groups, const GroupCursor<GS> &g, int k_left, int gq, int cq,
                                         float (&acc)[MR][NT][4]) {
     constexpr int kSub = KB / GS;
+    const int e = gq * groups + g.group;
 #pragma unroll
     for (int sub = 0; sub < kSub; ++sub) {
         uint32_t w[MR][2][GS / 32], xp[NT];
@@ -196,7 +197,7 @@ __device__ __forceinline__ void product(uint32_t w_tile, uint32_t x_tile, const 
                 load_words<GS, KB>(w_tile + row * (KB / 2), row, sub, cq, w[m][h]);
                 // a group of more than 128 k: the second 128 are the next group's only where the first one's is done
                 const int at = GS < kBlockK || sub == 0 ? sub : g.left == 1;
-                read_scale<GS, KB, ROWS, ZEROS>(sc, row, row * groups + g.group, at, kSub == 1 || sub * GS < k_left, s[m][h], z2[m][h]);
+                read_scale<GS, KB, ROWS, ZEROS>(sc, row, e, at, kSub == 1 || sub * GS < k_left, s[m][h], z2[m][h]);
             }
         }
 #pragma unroll
