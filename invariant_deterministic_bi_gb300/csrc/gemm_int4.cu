@@ -120,7 +120,8 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
 // with the 128-byte swizzle, which goes by the address: a 16-byte piece is exchanged
 // by the address's 128-byte line modulo 8. Boxes lie x_stride apart, which is 2 or 6
 // lines modulo 8 (1 where X has one row): the pieces that eight lanes load at once, of
-// two rows and (GS = 128) two boxes, are then in all the banks.
+// two rows and (GS = 128) two boxes, are then in all the banks. With GS = 32 they are
+// four neighbours of two rows, which have to be four lines apart: x_row.
 template <int GS, int KB>
 __device__ __forceinline__ void load_words(uint32_t w_row, int row, int sub, int cq, uint32_t (&w)[GS / 32]) {
     const int byte = GS / 2 * sub + GS / 8 * cq;
@@ -132,6 +133,9 @@ __device__ __forceinline__ void load_words(uint32_t w_row, int row, int sub, int
     else
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at));
 }
+// The row of X (of eight) that column n of a product takes.
+template <int GS>
+__device__ __forceinline__ int x_row(int n) { return GS == 32 ? ((n & 1) << 2) | (n >> 1) : n; }
 // Bytes between the boxes of X: of `rows` rows, and two more lines where four rows or more make their number 4 or 0
 // modulo 8.
 __host__ __device__ constexpr int x_box(int rows) { return rows * 128 + (rows >= 4 ? 256 : 0); }
@@ -185,7 +189,7 @@ __device__ __forceinline__ void product(uint32_t w_tile, uint32_t x_tile, const 
     for (int sub = 0; sub < kSub; ++sub) {
         uint32_t w[MR][2][GS / 32], xp[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) xp[t] = x_piece<GS>(x_tile, x_stride, x_row0 + 8 * t + (gq & x_mask), sub, cq);
+        for (int t = 0; t < NT; ++t) xp[t] = x_piece<GS>(x_tile, x_stride, x_row0 + 8 * t + (x_row<GS>(gq) & x_mask), sub, cq);
         float s[MR][2];
         uint32_t z2[MR][2];
         float part[MR][NT][4];
@@ -354,7 +358,7 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mine[(16 * m + gq + 8 * (e >> 1)) * kCols + 8 * t + 2 * cq + (e & 1)] = acc[m][t][e];
+                for (int e = 0; e < 4; ++e) mine[(16 * m + gq + 8 * (e >> 1)) * kCols + 8 * t + x_row<GS>(2 * cq + (e & 1))] = acc[m][t][e];
         if (__syncthreads_or(!ok)) break;                  // (two buffers: the one before last has been read)
         for (int i = threadIdx.x; i < kN * 8 * NT; i += blockDim.x) {
             const int r = i % kN, t = i / kN;
@@ -482,7 +486,7 @@ gemm_int4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                red[(8 * NT * wm + 8 * t + 2 * cq + (e & 1)) * kLd + 16 * MR * wn + 16 * m + gq + 8 * (e >> 1)] =
+                red[(8 * NT * wm + 8 * t + x_row<GS>(2 * cq + (e & 1))) * kLd + 16 * MR * wn + 16 * m + gq + 8 * (e >> 1)] =
                     SPLIT ? acc[m][t][e] : tot[m][t][e];
     if (SPLIT)
         cluster_sync();
