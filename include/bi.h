@@ -445,7 +445,7 @@ BI_API bi_status bi_attention_decode_noalloc(const void *Q, const void *K_cache,
  * BI_ERR_INVALID_ARG. The slots of one call must differ (two tokens of one
  * call with the same slot leave an unspecified mixture there). Everything
  * else in the cache stays as it was.
- * Requirements: head_dim == 128; ldk, ldv >= Hkv * 128 and multiples of 8.
+ * Requirements: head_dim == 128; Hkv <= 2^20; ldk, ldv >= Hkv * 128 and multiples of 8.
  */
 BI_API bi_status bi_kv_int4_append(const void *K, int64_t ldk, const void *V, int64_t ldv, int64_t T,
                                    const int64_t *slots, uint8_t *k_codes, void *k_scales, uint8_t *v_codes,

@@ -367,6 +367,7 @@ bi_status check_kv_int4(const uint8_t *kc, const void *ks, const uint8_t *vc, co
 // The rows of K and V and the slots of bi_kv_int4_append / _read.
 bi_status check_kv_rows(const void *K, int64_t ldk, const void *V, int64_t ldv, const int64_t *slots, int32_t Hkv) {
     if (!K || !V || !slots) return BI_ERR_INVALID_ARG;
+    if (Hkv > (1 << 20)) return BI_ERR_UNSUPPORTED;    // (offsets within a token are 32 bits)
     if (ldk < static_cast<int64_t>(Hkv) * 128 || ldv < static_cast<int64_t>(Hkv) * 128) return BI_ERR_INVALID_ARG;
     if (ldk % 8 != 0 || ldv % 8 != 0 || !aligned16(K) || !aligned16(V) || !aligned8(slots)) return BI_ERR_MISALIGNED;
     return BI_OK;

@@ -26,7 +26,7 @@ def kv(**kw):
 @pytest.mark.parametrize("change,want", [
     (dict(T=-1), 1), (dict(T=1 << 31), 1), (dict(K=None), 1), (dict(slots=None), 1), (dict(vs=None), 1), (dict(nb=0), 1),
     (dict(Hkv=0), 1), (dict(bs=0), 1), (dict(ldk=1016), 1), (dict(D=64), 2), (dict(nb=1 << 40), 2),
-    (dict(nb=1 << 25, bs=16, Hkv=8), 2), (dict(ldv=1028), 3), (dict(V=FAKE + 8), 3), (dict(kc=FAKE + 8), 3),
+    (dict(nb=1 << 25, bs=16, Hkv=8), 2), (dict(nb=1, bs=1, Hkv=(1 << 20) + 1, ldk=1 << 28, ldv=1 << 28), 2), (dict(ldv=1028), 3), (dict(V=FAKE + 8), 3), (dict(kc=FAKE + 8), 3),
     (dict(ks=FAKE + 8), 3), (dict(slots=FAKE + 4), 3), (dict(T=0), 0)])
 def test_append_and_read(so, change, want):
     append, read = kv(**change)
