@@ -565,21 +565,43 @@ bi_status launch_tile_kernel(const CUtensorMap &tmW, const CUtensorMap &tmX, con
     return BI_ERR_CUDA;
 }
 
+// Rows of X a tile (32 or 64), and whether the CTAs of a cluster take a segment each, by the time it should take (tenths
+// of a microsecond). The SMs work in rounds: one CTA an SM with tiles of 64 rows and all segments, else two. Per block of
+// 128 k a round takes 1.2 us with tiles of 64 rows, 1.3 with two CTAs of 32 (0.9 with one); of one segment 1.4 with tiles
+// of 32 and 2.1 with 64, and 4 or 5.5 us for filling the stages and joining the sums. Measured, tiles of 32 / 64 rows /
+// segments with 32 / 64 (g = 128): 17 x 6144 x 4096 28.5 / 39.3 / 18.5 / 23.1 us; 64 rows 28.6 / 39.4 / 31.4 / 28.4; 96
+// rows 28.7 / 39.5 / 44.0 / 43.4; 200 rows 68.5 / 77.5 / 91.4 / 77.8; 200 x 24576 x 4096 193 / 231 / 347 / 286;
+// 130 x 4096 x 12288 126 / 110 / 94 / 89, 200 rows 126 / 110 / 125 / 112.
+struct TilePlan {
+    int rows;
+    bool split;
+};
+TilePlan tile_plan(const GemmI4Params &p, int sms) {
+    const int64_t tiles_n = (p.N + kTileN - 1) / kTileN, t32 = tiles_n * ((p.M + 31) / 32), t64 = tiles_n * ((p.M + 63) / 64);
+    const int64_t two = 2 * static_cast<int64_t>(sms), left = t32 % two, seg = (p.blocks + p.segments - 1) / p.segments;
+    const int64_t all32 = (t32 / two * 13 + (left > sms ? 14 : left > 0 ? 9 : 0)) * p.blocks;
+    const int64_t all64 = (t64 + sms - 1) / sms * 12 * p.blocks;
+    TilePlan best{all32 <= all64 ? 32 : 64, false};
+    if (p.segments > 1) {
+        const int64_t seg32 = (t32 * p.segments + two - 1) / two * (40 + 14 * seg), seg64 = (t64 * p.segments + two - 1) / two * (55 + 21 * seg);
+        const int64_t least = seg32 < seg64 ? seg32 : seg64;
+        if (least < (all32 <= all64 ? all32 : all64)) best = TilePlan{seg32 < seg64 ? 32 : 64, true};
+    }
+    return best;
+}
+
 template <int GS, int TM, bool ZEROS>
-bi_status launch_tiles(const CUtensorMap &tmW, const CUtensorMap &tmX, const GemmI4Params &p, int sms, cudaStream_t s) {
-    // A CTA a segment while the tiles alone would leave SMs without one: one segment a CTA / all, g = 128: 17 x 6144 x
-    // 4096 (48 tiles) 19.1 / 29.4 us, 64 rows 28.8 / 41.4, 200 x 4096 x 12288 (128) 116 / 117, 32 x 24576 x 4096 (192) 58 / 47
+bi_status launch_tiles(const CUtensorMap &tmW, const CUtensorMap &tmX, const GemmI4Params &p, bool split, cudaStream_t s) {
     const int64_t tiles = (p.N + kTileN - 1) / kTileN * ((p.M + TM - 1) / TM);
-    if (p.segments > 1 && tiles < sms) return launch_tile_kernel<GS, TM, true, ZEROS>(tmW, tmX, p, tiles, s);
-    return launch_tile_kernel<GS, TM, false, ZEROS>(tmW, tmX, p, tiles, s);
+    return split ? launch_tile_kernel<GS, TM, true, ZEROS>(tmW, tmX, p, tiles, s) : launch_tile_kernel<GS, TM, false, ZEROS>(tmW, tmX, p, tiles, s);
 }
 
 template <int GS, bool ZEROS>
 bi_status launch_group(const void *X, int64_t ldx, const uint8_t *W, GemmI4Params &p, int sms, cudaStream_t s) {
-    // Rows kernel / tile kernel, g = 128: 9 x 6144 x 4096 11.8 / 17.0 us, 16 rows 11.9 / 17.9, 16 x 24576 x 4096 30 / 47.
-    // Tiles of 32 / 64 rows of X: 17 x 6144 x 4096 19.1 / 23.9 us, 33 rows 29.2 / 25.9, 64 rows 31.5 / 28.8.
+    // Rows kernel / tile kernel, g = 128: 9 x 6144 x 4096 9.9 / 16.9 us, 16 rows 10.0 / 17.5, 16 x 24576 x 4096 24.5 / 45.8.
     const bool rows = p.M <= 16;
-    const int tm = p.M <= 32 ? 32 : 64, kb = p.M <= 8 ? rows_kb<1>() : rows_kb<2>();
+    const TilePlan plan = tile_plan(p, sms);
+    const int tm = plan.rows, kb = p.M <= 8 ? rows_kb<1>() : rows_kb<2>();
     p.x_rows = p.M <= 2 ? static_cast<int>(p.M) : p.M <= 4 ? 4 : p.M <= 8 ? 8 : 16;
     CUtensorMap tmW{}, tmX{};
     if (make_tmap_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, p.K / 2, p.N, p.K / 2, (rows ? kb : kBlockK) / 2, rows ? (p.M <= 8 ? rows_n<1>() : rows_n<2>()) : kTileN,
@@ -588,8 +610,8 @@ bi_status launch_group(const void *X, int64_t ldx, const uint8_t *W, GemmI4Param
                      CU_TENSOR_MAP_SWIZZLE_128B) != BI_OK)
         return BI_ERR_CUDA;
     if (rows) return p.M <= 8 ? launch_rows<GS, 1, ZEROS>(tmW, tmX, p, sms, s) : launch_rows<GS, 2, ZEROS>(tmW, tmX, p, sms, s);
-    if (tm == 32) return launch_tiles<GS, 32, ZEROS>(tmW, tmX, p, sms, s);
-    return launch_tiles<GS, 64, ZEROS>(tmW, tmX, p, sms, s);
+    if (tm == 32) return launch_tiles<GS, 32, ZEROS>(tmW, tmX, p, plan.split, s);
+    return launch_tiles<GS, 64, ZEROS>(tmW, tmX, p, plan.split, s);
 }
 
 }  // namespace

@@ -120,3 +120,16 @@ def test_refusals(bi):
     assert e.value.status == bi.BI_ERR_MISALIGNED
     assert bi.gemm_int4(X[:0], W, S).shape == (0, 16)
     assert bi.device_status() == bi.BI_OK
+
+
+@pytest.mark.parametrize("g,zeros", [(128, False), (64, True), (32, False)])
+@pytest.mark.parametrize("M,N,K", [(17, 6144, 4096), (64, 6144, 4096), (96, 6144, 4096), (130, 6144, 4096), (200, 4096, 12288)])
+def test_every_form_of_the_tiles_has_the_bits_of_single_rows(bi, M, N, K, g, zeros):
+    """Tiles of 32 and 64 rows, with a segment a CTA or all of them (the sizes choose): the rows kernel's bits."""
+    import torch
+    X, W, S, Z = inputs(M, N, K, g, zeros, seed=M + g)
+    Y = run(bi, X, W, S, Z)
+    for m in sorted({0, 15, 16, 31, 32, 63, M // 2, M - 1} & set(range(M))):
+        assert torch.equal(Y[m:m + 1], run(bi, X[m:m + 1], W, S, Z))
+    check(Y[:, -24:], X, W[-24:], S[-24:], Z[-24:] if zeros else None)
+    assert bi.device_status() == bi.BI_OK
