@@ -21,22 +21,25 @@
 //     segment, with its own ring of TMA copies, so that nobody waits for another
 //     segment before the final sum;
 //   - more (gemm_int4_tile_kernel): a CTA a tile of 128 weight rows x 32 or 64
-//     rows of X, both staged by TMA for all warps; it walks the segments, or, where the
-//     tiles would not fill the GPU, the CTAs of a cluster take one each.
+//     rows of X, both staged by TMA for all warps; it walks the segments, or the CTAs
+//     of a cluster take one each.
 //
 // What bounds it: a word of eight codes costs 11 instructions to expand (three
 // shifts, four logic operations, four multiply-adds), and the integer pipe, the
 // packed bf16 pipe and mma.sync overlap only partly on this GPU: an expansion
 // alone takes 16.4-17.6 cycles per warp and scheduler, with one product 21.6-24.7
 // (17 and 8 apart; measured with independent chains). At the weights' HBM rate a
-// scheduler has 22 cycles for a word. Measured (GB300, weights from HBM): M = 1:
-// 6144 x 4096, g = 128 7.7 us (1.7 TB/s; 3 us of it launch and first latency),
-// 24576 x 4096 18.6 us (2.8 TB/s); M = 16, 24576 x 4096, g = 64 35 us; M = 200,
-// 4096 x 12288 118 us (g = 128) and 139 us (g = 32); M = 2048, 6144 x 4096 442 us
-// (233 TFLOP/s). A form with the expanded weights in tensor memory and tcgen05
-// products was 13.9, 39.9, 48, 88 and 146, 334 us in that order: faster for many
+// scheduler has 22 cycles for a word; tiles spend 44 % of their cycles in mma.sync,
+// 38 % and 19 % in the other two. Measured (GB300, weights from HBM), M = 1:
+// 6144 x 4096, g = 128 7.7 us (1.7 TB/s; without the products 4.5), 24576 x 4096
+// 18.3 us (2.9 TB/s; 10.5); M = 16, 24576 x 4096, g = 64 with zeros 29.8 us; M = 200,
+// 4096 x 12288 111 us (g = 128) and 118 us (g = 32); M = 2048, 6144 x 4096 421 us
+// (245 TFLOP/s). A form with the expanded weights in tensor memory and tcgen05
+// products took 13.9, 39.9, 48, 88, 146 and 334 us in that order: faster for many
 // rows, but every M has to give the same bits, which the two products do not, and
-// few rows are what the call is for.
+// few rows are what the call is for. Tiles of 128 rows of X (half the expansions a
+// product, eight warps an SM) took 387 us at M = 2048, but 154 and 180 at M = 200;
+// X's operand pairs made once, in place, a stage ahead, 5-7 % more than here.
 #include "attn_common.cuh"
 #include "bi_internal.h"
 #include "bi_ptx.cuh"
