@@ -379,3 +379,26 @@ def test_non_finite_rows_reach_only_the_tokens_that_see_them(bi, Hq, Hkv, bs):
     got = bi.attention_extend_int4(q2, cu2, c, t2, l2, 300, 7, SCALE)
     assert np.array_equal(bits_of(got), bits_of(want[rows]))
     assert bi.device_status() == bi.BI_OK
+
+
+@pytest.mark.parametrize("exponent", [127, 127 - 98, 127 + 122])
+def test_every_quotient_is_rounded_exactly(bi, exponent):
+    """For each of the 128 significands of the largest magnitude, all numbers of the six binades up to it, of both signs:
+    the codes and scales of the definition (ordinary magnitudes, and where the scale reaches its least and largest)."""
+    groups = []
+    for m in range(128):
+        top = exponent << 7 | m
+        below = np.arange(top - 6 * 128 + 1, top + 1).astype(np.uint16)
+        below = np.concatenate([below, below | 0x8000, np.zeros(-2 * below.size % 31, np.uint16)]).reshape(-1, 31)
+        groups.append(np.concatenate([np.full((below.shape[0], 1), top | (0x8000 if m & 1 else 0), np.uint16), below], 1))
+    x = np.concatenate(groups)
+    x = np.concatenate([x, np.zeros((-x.shape[0] % 4, 32), np.uint16)]).reshape(-1, 1, D)
+    T = x.shape[0]
+    c = bi.kv_int4_cache(T, 1, 1)
+    slots = to_dev(np.arange(T, dtype=np.int64))
+    bi.kv_int4_append(to_dev_bf16(x), to_dev_bf16(x ^ 0x8000), slots, c)
+    n, s = ref.held(x)
+    assert np.array_equal(bits_of(c.k_scales).reshape(T, 1, 4), syn.to_bf16_bits(s.astype(np.float32)))
+    assert np.array_equal(c.k_codes.cpu().numpy().reshape(T, 1, 64), ref.pack(n, 0))
+    assert np.array_equal(c.v_codes.cpu().numpy().reshape(T, 1, 64), ref.pack(-n, 0))
+    assert bi.device_status() == bi.BI_OK
