@@ -335,3 +335,34 @@ def test_results_made_on_another_stream(bi):
         z = bi.gemm_int4(X, W, S_neg, stream=side)
         torch.cuda.synchronize()
         assert bool((copy == 4).all()) and torch.equal(got, want) and torch.equal(z, -want)
+
+
+def test_another_stream_inside_a_capture(bi):
+    """A call on a stream forked from the captured one, its output and workspace allocated for that stream: replays give
+    the eager bits."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(9)
+    X = torch.randn((24, 1024), device="cuda", generator=g).bfloat16()
+    W = torch.randint(0, 256, (512, 512), dtype=torch.uint8, device="cuda", generator=g)
+    S = torch.rand((512, 8), device="cuda", generator=g).bfloat16()
+    c = bi.kv_int4_cache(24, 16, 2)
+    K = torch.randn((384, 2, D), device="cuda", generator=g).bfloat16()
+    bi.kv_int4_append(K, K, torch.arange(384, device="cuda"), c)
+    q = torch.randn((1, 8, D), device="cuda", generator=g).bfloat16()
+    table, lens = torch.arange(24, dtype=torch.int32, device="cuda").view(1, 24), torch.tensor([380], dtype=torch.int32, device="cuda")
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        y = bi.gemm_int4(X, W, S, stream=side)
+        o = bi.attention_decode_int4(q, c, table, lens, 384, SCALE, stream=side)
+        z = bi.gemm_int4(X, W, S)
+        torch.cuda.current_stream().wait_stream(side)
+        both = y + z
+    for _ in range(2):
+        X.normal_(generator=g), q.normal_(generator=g)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, bi.gemm_int4(X, W, S)) and torch.equal(z, y) and torch.equal(both, y + z)
+        assert torch.equal(o, bi.attention_decode_int4(q, c, table, lens, 384, SCALE))
+    assert bi.device_status() == bi.BI_OK
