@@ -467,8 +467,9 @@ BI_API bi_status bi_kv_int4_read(const uint8_t *k_codes, const void *k_scales, c
  * bi_attention_decode_int4 -- bi_attention_decode over the 4-bit cache: the
  * same bits as bi_attention_decode over a bf16 cache holding the same values
  * (same chunks, product order and merge; same workspace size; same checks and
- * skips of sequence lengths and blocks). A chunk whose blocks all lie outside
- * the cache counts nothing.
+ * skips of sequence lengths and blocks), but for one case: a chunk whose blocks
+ * all lie outside the cache counts nothing. (A sequence none of whose blocks lies
+ * in the cache has nothing to weigh: its row is NaN.)
  */
 BI_API bi_status bi_attention_decode_int4(const void *Q, const uint8_t *k_codes, const void *k_scales,
                                           const uint8_t *v_codes, const void *v_scales, const int32_t *block_table,

@@ -926,9 +926,14 @@ attn_extend_kernel(const ExtParams p) {
                     m[e >> 1] = fmaxf(m[e >> 1], s[nt][e]);
                 }
         }
-        if (I4 && bad) {                               // a chunk without a valid token counts nothing
-            m[0] = fmaxf(m[0], kNoScore);
-            m[1] = fmaxf(m[1], kNoScore);
+        if (I4 && bad) {                               // a chunk counts nothing for a row that sees no valid token of it
+            uint32_t in[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) in[k] = __ballot_sync(0xffffffffu, ro[lane + 32 * k] >= 0);
+            const int first = in[0] ? __ffs(in[0]) - 1 : in[1] ? __ffs(in[1]) + 31 : in[2] ? __ffs(in[2]) + 63
+                            : in[3] ? __ffs(in[3]) + 95 : kChunk;
+            m[0] = fmaxf(m[0], first < na ? -INFINITY : kNoScore);
+            m[1] = fmaxf(m[1], first < nb ? -INFINITY : kNoScore);
         }
         // per row: max (any order gives the same value), then e^(s - m) for the
         // tokens it sees (0 past them)

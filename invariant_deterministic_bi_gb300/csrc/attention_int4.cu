@@ -362,6 +362,7 @@ attn_split_int4_kernel(const SplitParams p) {
         for (int mt = 0; mt < kChunk / 16; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[mt][e] = __fmul_rn(s[mt][e], p.scale);
+        float m[2] = {-INFINITY, -INFINITY};
         if (!cur.whole) {
 #pragma unroll
             for (int mt = 0; mt < kChunk / 16; ++mt)
@@ -371,14 +372,20 @@ attn_split_int4_kernel(const SplitParams p) {
                     const bool in = ((cur.valid[mt >> 1] >> (t & 31)) & 1) && (!EXT || t < cur.see0 + (2 * cq + (e & 1)) / G);
                     if (!in) s[mt][e] = -INFINITY;
                 }
+            int first = 0x7FFFFFFF;                        // the chunk's first token with a row in the cache
+#pragma unroll
+            for (int k = 3; k >= 0; --k)
+                if (cur.valid[k]) first = 32 * k + __ffs(cur.valid[k]) - 1;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (first >= cur.see0 + (EXT ? (2 * cq + e) / G : 0)) m[e] = kNoScore;
         }
         // per row: the maximum, the exponentials, and their sum in the bf16 kernels' order: tokens
         // L, L + 32, L + 64, L + 96 in turn (mt = L / 16 % 2 + 0, 2, 4, 6), then a butterfly over
         // L xor 16 (mt), 8 (the fragment's half), 4, 2, 1 (lanes)
-        float m[2], l[2];
+        float l[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            m[e] = kNoScore;
 #pragma unroll
             for (int mt = 0; mt < kChunk / 16; ++mt) m[e] = fmaxf(m[e], fmaxf(s[mt][e], s[mt][2 + e]));
 #pragma unroll

@@ -10,9 +10,12 @@ namespace bi {
 
 constexpr int kD = 128;
 constexpr int kChunk = 128;                    // tokens per chunk: fixed, by position
-// Over the 4-bit cache: the least maximum of a chunk, so that a chunk whose
-// blocks all lie outside the cache weighs e^(kNoScore - m) = 0 in the merge.
-constexpr float kNoScore = -3.0e38f;
+// Over the 4-bit cache: the maximum of a chunk of which a row sees no token in
+// the cache (its blocks lie outside). The least number, so that the chunk's sums,
+// which are 0, leave every other chunk's weight as it is, whatever its scores;
+// with -inf its exponentials would be NaN, as they have to be where the scores of
+// tokens in the cache are all -inf (bi_attention_decode gives NaN there).
+constexpr float kNoScore = -0x1.fffffep127f;
 
 // 16-byte global -> shared copy; src_bytes = 0 writes 16 zero bytes and reads nothing.
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint32_t src_bytes) {
