@@ -328,7 +328,8 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     int slot = 0, buf = 0;
     uint32_t parity = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf = (buf + 1) % kBuffers) {
+    int tile = blockIdx.x, blk = b0;                       // the stage at work
+    for (; tile < tiles; tile += gridDim.x, buf = (buf + 1) % kBuffers) {
         const int64_t n0 = static_cast<int64_t>(tile) * kN;
         float acc[2][NT][4];
 #pragma unroll
@@ -338,7 +339,7 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[m][t][e] = 0.0f;
         GroupCursor<GS> g = g0;
-        for (int blk = b0; blk < b1 && ok; ++blk) {
+        for (blk = b0; blk < b1 && ok; ++blk) {
             ok = __all_sync(0xffffffffu, mbar_wait(&full[seg][slot], parity, nullptr));
             __syncwarp();
             if (!ok) break;
@@ -362,7 +363,18 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mine[(16 * m + gq + 8 * (e >> 1)) * kCols + 8 * t + x_row<GS>(2 * cq + (e & 1))] = acc[m][t][e];
-        if (__syncthreads_or(!ok)) break;                  // (two buffers: the one before last has been read)
+        if (__syncthreads_or(!ok)) {                       // (two buffers: the one before last has been read)
+            // a wait of the CTA ran out: report; every segment's copies in flight, the stages from the one at work up to
+            // the next to be copied, get another limit
+            if (!ok && lane == 0) atomicOr(p.status, kDevTimeout);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            const int flying = (ft - tile) / static_cast<int>(gridDim.x) * (b1 - b0) + fb - blk;
+            for (int k = 0; wn == 0 && k < flying; ++k) {
+                mbar_wait(&full[seg][slot], parity, nullptr);
+                if (++slot == kRing) slot = 0, parity ^= 1;
+            }
+            return;
+        }
         for (int i = threadIdx.x; i < kN * 8 * NT; i += blockDim.x) {
             const int r = i % kN, t = i / kN;
             if (t >= p.M) break;
@@ -372,14 +384,6 @@ gemm_int4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
             store_y(p, t, n0 + r, y);
         }
         if (kBuffers == 1) __syncthreads();
-    }
-    if (!ok && lane == 0) atomicOr(p.status, kDevTimeout);
-    if (!ok) asm volatile("cp.async.wait_all;" ::: "memory");
-    if (!ok && wn == 0) {                                  // a wait ran out: the copies in flight get another limit
-        for (int k = 0; k < kRing; ++k) {
-            mbar_wait(&full[seg][slot], parity, nullptr);
-            if (++slot == kRing) slot = 0, parity ^= 1;
-        }
     }
 }
 

@@ -1,0 +1,86 @@
+"""CPU models of what the kernels of the 4-bit operators do when a bounded wait runs out: every copy in flight gets
+another limit before its CTA leaves, a wait is made only for copies that were started, and all warps leave at the same
+place. No GPU: such a wait cannot be made to run out on one without a fault. Each model is also run in the form that
+breaks the rule, which pins it to a fault that it must catch."""
+import random
+
+import pytest
+
+LIMIT = 1000                          # a bounded wait, in steps
+
+
+# ------------------------------------------------- rows kernel of the linear
+
+def _rows_cta(segments, stages, tiles, delay, waits):
+    """One CTA of gemm_int4_rows_kernel: each segment walks `stages` blocks of each tile through its ring of two; the
+    segments meet after a tile. delay(seg, k): steps that the segment's k-th copy takes. waits: "cta" (after a wait ran
+    out, every segment waits for the stages between its place and its fill cursor) or "warp" (only the segment whose
+    wait ran out does, for two stages). Returns the copies in flight when the CTA gave up, as (landing, end), and the
+    step at which its last warp leaves; None where nothing ran out."""
+    ring = 2
+    seg = [dict(now=0, ft=0, fb=0, n=0, ring=[], ok=True, blk=0) for _ in range(segments)]
+
+    def fill(i, s):
+        if s["ft"] >= tiles:
+            return
+        s["ring"].append(s["now"] + delay(i, s["n"]))
+        s["n"] += 1
+        s["fb"] += 1
+        if s["fb"] == stages:
+            s["fb"], s["ft"] = 0, s["ft"] + 1
+
+    for i, s in enumerate(seg):
+        for _ in range(ring):
+            fill(i, s)
+    for tile in range(tiles):
+        for i, s in enumerate(seg):
+            s["blk"] = 0
+            while s["blk"] < stages:
+                if s["ring"][0] > s["now"] + LIMIT:
+                    s["now"] += LIMIT
+                    s["ok"] = False
+                    break
+                s["now"] = max(s["now"], s["ring"].pop(0)) + 1
+                fill(i, s)
+                s["blk"] += 1
+        meet = max(s["now"] for s in seg)
+        for s in seg:
+            s["now"] = meet
+        if all(s["ok"] for s in seg):
+            continue
+        flying = [x for s in seg for x in s["ring"] if x > meet]
+        for s in seg:
+            started = len(s["ring"])
+            n = (s["ft"] - tile) * stages + s["fb"] - s["blk"]       # as the kernel counts them
+            assert n == started
+            if waits == "cta" or not s["ok"]:
+                for x in s["ring"][:n]:
+                    s["now"] = min(max(s["now"], x), s["now"] + LIMIT)
+        return flying, meet, max(s["now"] for s in seg)
+    return None
+
+
+def _rows_faults(waits):
+    """Runs in which a copy that lands within another limit of the give-up lands after the CTA has left."""
+    faults = gave_up = 0
+    for seed in range(600):
+        r = random.Random(seed)
+        segments, stages, tiles = r.randint(1, 8), r.randint(1, 6), r.randint(1, 5)
+        slow = {(r.randrange(segments), r.randrange(stages * tiles)) for _ in range(r.randint(1, 4))}
+        d = lambda i, k: r.randint(LIMIT + 1, 2 * LIMIT) if (i, k) in slow else r.randint(1, 50)
+        out = _rows_cta(segments, stages, tiles, d, waits)
+        if out is None:
+            continue
+        flying, meet, left = out
+        gave_up += 1
+        faults += any(left < x <= meet + LIMIT for x in flying)
+    assert gave_up > 100
+    return faults
+
+
+def test_rows_kernel_leaves_no_copy_in_flight():
+    assert _rows_faults("cta") == 0
+
+
+def test_rows_model_catches_waits_of_the_failing_segment_only():
+    assert _rows_faults("warp") > 0
