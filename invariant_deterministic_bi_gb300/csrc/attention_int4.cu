@@ -322,7 +322,8 @@ attn_split_int4_kernel(const SplitParams p) {
         const Item nxt = next();
         if (!staged<BLOCKS>(barK, parity)) {
             if (lane == 0) atomicOr(p.status, kDevTimeout);
-            staged<BLOCKS>(barV, parity);                  // no copy in flight at the exit
+            staged<BLOCKS>(barK, parity);                  // the copies in flight get another limit
+            staged<BLOCKS>(barV, parity);
             return;
         }
         // scores: s[mt][e], token 16 mt + gq + 8 (e / 2), query row 2 cq + e % 2
@@ -431,6 +432,7 @@ attn_split_int4_kernel(const SplitParams p) {
             }
         if (!staged<BLOCKS>(barV, parity)) {
             if (lane == 0) atomicOr(p.status, kDevTimeout);
+            staged<BLOCKS>(barV, parity);
             if (nxt.n) staged<BLOCKS>(barK, parity ^ 1);
             return;
         }

@@ -84,3 +84,59 @@ def test_rows_kernel_leaves_no_copy_in_flight():
 
 def test_rows_model_catches_waits_of_the_failing_segment_only():
     assert _rows_faults("warp") > 0
+
+
+# ------------------------------------------- a warp of the split attention
+
+def _split_warp(items, delay, again):
+    """One warp of attn_split_int4_kernel: its K and V buffers are filled one item ahead. delay(which, k): steps that the
+    copy of item k takes. again: after a wait ran out, its own copy gets another limit too. Returns the copies in flight
+    when the wait ran out, that step, and the step at which the warp leaves; None where nothing ran out."""
+    now = 0
+    copy = {"K": delay("K", 0), "V": delay("V", 0)}       # landing steps
+
+    def wait(which):
+        nonlocal now
+        ok = copy[which] <= now + LIMIT
+        now = max(now, min(copy[which], now + LIMIT))
+        return ok
+
+    for k in range(items):
+        for which, other in (("K", "V"), ("V", "K")):
+            if not wait(which):
+                gave_up, flying = now, [copy[which]]
+                if which == "K" or k + 1 < items:          # V of this item, or K of the next one
+                    flying.append(copy[other])
+                if again:
+                    wait(which)
+                if which == "K" or k + 1 < items:
+                    wait(other)
+                return flying, gave_up, now
+            now += 5                                       # scores; softmax and values
+            if k + 1 < items:
+                copy[which] = now + delay(which, k + 1)
+    return None
+
+
+def _split_faults(again):
+    faults = gave_up = 0
+    for seed in range(600):
+        r = random.Random(seed)
+        items = r.randint(1, 12)
+        slow = {(r.choice("KV"), r.randrange(items)) for _ in range(r.randint(1, 3))}
+        out = _split_warp(items, lambda w, k: r.randint(LIMIT + 1, 2 * LIMIT) if (w, k) in slow else r.randint(1, 50), again)
+        if out is None:
+            continue
+        flying, at, left = out
+        gave_up += 1
+        faults += any(left < x <= at + LIMIT for x in flying)
+    assert gave_up > 100
+    return faults
+
+
+def test_split_warp_leaves_no_copy_in_flight():
+    assert _split_faults(True) == 0
+
+
+def test_split_model_catches_a_wait_for_the_other_copy_only():
+    assert _split_faults(False) > 0
