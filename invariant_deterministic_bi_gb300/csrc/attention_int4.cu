@@ -588,7 +588,7 @@ attn_merge_int4_kernel(const SplitParams p, int ring) {
         if (failed) {                                      // a wait ran out: report; the copies in flight get another limit
             if (d == kMergeThreads) {
                 atomicOr(p.status, kDevTimeout);
-                for (int k = t; k < nt && k < t + ring; ++k) mbar_wait(&full[k % ring], (k / ring) & 1, nullptr);
+                for (int k = t; k < nt && k < t + ring - (t > 0); ++k) mbar_wait(&full[k % ring], (k / ring) & 1, nullptr);
             }
             return;
         }

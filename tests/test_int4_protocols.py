@@ -140,3 +140,41 @@ def test_split_warp_leaves_no_copy_in_flight():
 
 def test_split_model_catches_a_wait_for_the_other_copy_only():
     assert _split_faults(False) > 0
+
+
+# --------------------------------------------------- the merge of the chunks
+
+def _merge_loader(tiles, ring, lost, early=1):
+    """The loading warp of attn_merge_int4_kernel over `tiles` tiles, of which `lost` never lands (None: all do).
+    early: after the first tile, a wait's end is seen before that many copies of its turn are started. Returns (tiles
+    waited for that were not started, tiles in flight that were not waited for at the exit)."""
+    started, unstarted = set(), []
+
+    def factors(t):                                        # waits for tile t
+        if t not in started:
+            unstarted.append(t)
+        return t != lost and t in started
+
+    started.update(range(min(tiles, ring)))
+    ok = factors(0)
+    for t in range(tiles):
+        if not ok:                                         # seen behind the barrier, before the next copy is started
+            waited = range(t, min(tiles, t + ring - (early if t > 0 else 0)))
+            unstarted += [k for k in waited if k not in started]
+            return unstarted, [k for k in started if k >= t and k not in waited]
+        if t > 0 and t - 1 + ring < tiles:
+            started.add(t - 1 + ring)
+        if t + 1 < tiles:
+            ok = factors(t + 1)
+    return unstarted, []
+
+
+def test_merge_waits_for_the_tiles_that_were_started():
+    for ring in range(2, 9):
+        for tiles in range(1, 30):
+            for lost in [None, *range(tiles)]:
+                assert _merge_loader(tiles, ring, lost) == ([], []), (ring, tiles, lost)
+
+
+def test_merge_model_catches_a_wait_for_a_tile_that_was_not_started():
+    assert _merge_loader(9, 4, 3, early=0) == ([6], [])
