@@ -671,6 +671,9 @@ bi_status launch_few(SplitParams &p, cudaStream_t s) {
     const int room = info->max_smem_optin / (kMergeStage + 1024) / static_cast<int>(per_sm < 6 ? per_sm : 6);
     int ring = tiles < kMergeRing ? tiles : kMergeRing;
     if (ring > room) ring = room;
+    // and two at least where there are two: a tile's factors are made while the one before it is merged
+    static_assert(kMergeRing >= 2, "two tiles of the merge");
+    if (ring < 2 && tiles > 1) ring = 2;
     return launch_pdl(attn_merge_int4_kernel<EXT>, dim3(static_cast<unsigned>(merges)), dim3(kMergeThreads + 32), ring * kMergeStage, s,
                       p, ring);
 }

@@ -178,3 +178,9 @@ def test_merge_waits_for_the_tiles_that_were_started():
 
 def test_merge_model_catches_a_wait_for_a_tile_that_was_not_started():
     assert _merge_loader(9, 4, 3, early=0) == ([6], [])
+
+
+def test_merge_needs_two_tiles_of_room():
+    """With one, the next tile's factors are wanted before its copy is started: the launch never takes it."""
+    assert _merge_loader(1, 1, None) == ([], [])
+    assert _merge_loader(2, 1, None)[0]
