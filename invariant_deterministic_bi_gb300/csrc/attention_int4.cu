@@ -521,13 +521,13 @@ attn_merge_int4_kernel(const SplitParams p, int ring) {
     extern __shared__ __align__(16) uint8_t tiles[];       // [ring][kMergeStage]
     __shared__ float fa[2][kTile], fb[2][kTile], fl[2][kTile];   // alpha, beta, l of a tile's chunks
     __shared__ uint64_t full[kMergeRing];
-    __shared__ int failed;
+    __shared__ int failed[2];                              // tile t's wait ran out: [t % 2], read while t + 1's may be set
     const int d = threadIdx.x, lane = d & 31;
     const bool loader = d >= kMergeThreads;
     if (d == kMergeThreads) {
         for (int k = 0; k < ring; ++k) mbar_init(&full[k], 1);
         fence_mbar_init();
-        failed = 0;
+        failed[0] = failed[1] = 0;
     }
     __syncthreads();
     grid_dep_wait();      // earlier work of the stream is complete and visible
@@ -554,7 +554,7 @@ attn_merge_int4_kernel(const SplitParams p, int ring) {
     auto tile_at = [&](int t) { return reinterpret_cast<const float *>(tiles + t % ring * kMergeStage) + skew; };
     float m_run = -INFINITY;                               // the loader's running maximum
     auto factors = [&](int t) {                            // warp 4: tile t's factors, once it has landed
-        if (!mbar_wait(&full[t % ring], (t / ring) & 1, nullptr)) failed = 1;
+        if (!mbar_wait(&full[t % ring], (t / ring) & 1, nullptr)) failed[t & 1] = 1;
         __syncwarp();
         const int n = floats(t);
         if ((n & 2) && lane < 2)
@@ -585,7 +585,7 @@ attn_merge_int4_kernel(const SplitParams p, int ring) {
     float o = 0.0f, l = 0.0f;
     for (int t = 0; t < nt; ++t) {
         __syncthreads();                                   // tile t's factors are there, tile t - 1 is merged
-        if (failed) {                                      // a wait ran out: report; the copies in flight get another limit
+        if (failed[t & 1]) {                               // a wait ran out: report; the copies in flight get another limit
             if (d == kMergeThreads) {
                 atomicOr(p.status, kDevTimeout);
                 for (int k = t; k < nt && k < t + ring - (t > 0); ++k) mbar_wait(&full[k % ring], (k / ring) & 1, nullptr);

@@ -184,3 +184,32 @@ def test_merge_needs_two_tiles_of_room():
     """With one, the next tile's factors are wanted before its copy is started: the launch never takes it."""
     assert _merge_loader(1, 1, None) == ([], [])
     assert _merge_loader(2, 1, None)[0]
+
+
+def _merge_exits(tiles, lost, flags, seed):
+    """The iterations at which the merging warps leave, tile `lost` never landing: between the barriers t and t + 1 the
+    loading warp sets flag (t + 1) % flags, at any moment, and each merging warp reads flag t % flags, at any moment."""
+    r = random.Random(seed)
+    failed = [False] * flags
+    if lost == 0:
+        failed[0] = True
+    left = {}
+    for t in range(tiles):
+        events = [("set", None)] * (t + 1 == lost) + [("read", w) for w in range(4) if w not in left]
+        r.shuffle(events)
+        for kind, w in events:
+            if kind == "set":
+                failed[(t + 1) % flags] = True
+            elif failed[t % flags]:
+                left[w] = t
+    return set(left.values())
+
+
+@pytest.mark.parametrize("lost", [0, 1, 2, 5])
+def test_merging_warps_leave_together(lost):
+    for seed in range(200):
+        assert _merge_exits(6, lost, 2, seed) == {lost}
+
+
+def test_merge_model_catches_one_flag_for_two_tiles():
+    assert any(len(_merge_exits(6, 2, 1, seed)) > 1 for seed in range(200))
