@@ -31,7 +31,6 @@ namespace bi {
 
 constexpr int kI4Row = 64;                     // code bytes of a cache row
 constexpr int kI4Scales = 4;                   // scales of a cache row
-constexpr int kI4Group = 32;                   // dimensions that share a scale
 constexpr uint32_t kBf16x2_m136 = 0xC308C308u; // (-136, -136)
 
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
