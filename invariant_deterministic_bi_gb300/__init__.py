@@ -464,15 +464,20 @@ def _current_raw_stream(device: int) -> int:
     return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
+def _cache_dims(cache):
+    """(blocks, Hkv, block_size, device) of a cache."""
+    if not isinstance(cache, KVInt4Cache):
+        raise TypeError("cache must be a KVInt4Cache")
+    return cache._dims
+
+
 def _launch_on(cache, tensors, stream):
-    """(raw stream, cache arguments) for a call on the current device; the tensors and the cache have to be there."""
+    """(raw stream, cache arguments) for a call on the current device; the tensors and the cache (None for a call
+    without one), which have passed their checks of type, have to be there."""
     import torch
     cur = torch.cuda.current_device()
-    if cache is not None:
-        if not isinstance(cache, KVInt4Cache):
-            raise TypeError("cache must be a KVInt4Cache")
-        if cache._dims[3] != cur:
-            raise ValueError(f"the cache must be on the current device cuda:{cur}, it is on cuda:{cache._dims[3]}")
+    if cache is not None and cache._dims[3] != cur:
+        raise ValueError(f"the cache must be on the current device cuda:{cur}, it is on cuda:{cache._dims[3]}")
     for t in tensors:
         if t is not None and t.get_device() != cur:
             raise ValueError(f"tensors must be on the current device cuda:{cur}, got {t.device}")
@@ -533,9 +538,9 @@ def kv_int4_append(K, V, slots, cache: KVInt4Cache, stream=None) -> KVInt4Cache:
     projection); slots int64 [T]: block * block_size + offset, -1 to skip a
     token. The slots of one call must differ."""
     T = _slots(slots)
-    raw, c = _launch_on(cache, (K, V, slots), stream)
-    nblk, Hkv, bs, _ = cache._dims
+    nblk, Hkv, bs, _ = _cache_dims(cache)
     ldk, ldv = _kv_rows(K, T, Hkv, "K"), _kv_rows(V, T, Hkv, "V")
+    raw, c = _launch_on(cache, (K, V, slots), stream)
     _check(load().bi_kv_int4_append(K.data_ptr(), ldk, V.data_ptr(), ldv, T, slots.data_ptr(), *c, nblk, Hkv, 128, bs, raw),
            "bi_kv_int4_append")
     return cache
@@ -545,13 +550,14 @@ def kv_int4_read(cache: KVInt4Cache, slots, K=None, V=None, stream=None):
     """(K, V) bf16 [T, Hkv, 128]: the values held at `slots` (int64 [T]; -1 gives zeros)."""
     import torch
     T = _slots(slots)
+    nblk, Hkv, bs, _ = _cache_dims(cache)
+    ldk = _kv_rows(K, T, Hkv, "K") if K is not None else Hkv * 128
+    ldv = _kv_rows(V, T, Hkv, "V") if V is not None else Hkv * 128
     raw, c = _launch_on(cache, (slots, K, V), stream)
-    nblk, Hkv, bs, _ = cache._dims
     if K is None:
         K = _new((T, Hkv, 128), torch.bfloat16, slots, stream)
     if V is None:
         V = _new((T, Hkv, 128), torch.bfloat16, slots, stream)
-    ldk, ldv = _kv_rows(K, T, Hkv, "K"), _kv_rows(V, T, Hkv, "V")
     _check(load().bi_kv_int4_read(*c, nblk, Hkv, 128, bs, slots.data_ptr(), T, K.data_ptr(), ldk, V.data_ptr(), ldv, raw),
            "bi_kv_int4_read")
     return K, V
@@ -580,8 +586,8 @@ def attention_decode_int4(Q, cache: KVInt4Cache, block_table, seq_lens, max_seq_
     allocated with torch if not given."""
     import torch
     B, Hq, D = _attention_int4_args(Q, block_table, seq_lens, workspace, O)
+    nblk, Hkv, bs, _ = _cache_dims(cache)
     raw, c = _launch_on(cache, (Q, block_table, seq_lens, workspace, O), stream)
-    nblk, Hkv, bs, _ = cache._dims
     if seq_lens.shape != (B,):
         raise ValueError("one query token a sequence: seq_lens must be [B], B the rows of Q")
     if workspace is None:
@@ -611,8 +617,8 @@ def attention_extend_int4(Q, cu_q, cache: KVInt4Cache, block_table, seq_lens, ma
     import torch
     T, Hq, D = _attention_int4_args(Q, block_table, seq_lens, workspace, O)
     B = _typed(cu_q, torch.int32, "cu_q").numel() - 1
+    nblk, Hkv, bs, _ = _cache_dims(cache)
     raw, c = _launch_on(cache, (Q, cu_q, block_table, seq_lens, workspace, O), stream)
-    nblk, Hkv, bs, _ = cache._dims
     if seq_lens.shape != (B,):
         raise ValueError("cu_q must have one entry more than seq_lens")
     if workspace is None:
@@ -646,11 +652,11 @@ def gemm_int4(X, W, scales, zeros=None, Y=None, stream=None):
         raise ValueError("scales must divide K into groups")
     if zeros is not None and _typed(zeros, torch.uint8, "zeros").shape != ss:
         raise ValueError("zeros must have scales' shape")
+    if Y is not None and (_typed(Y, torch.bfloat16, "Y", contiguous=False).shape != (M, N) or Y.stride(1) != 1):
+        raise ValueError("Y must be [M, N] with unit column stride")
     raw, _ = _launch_on(None, (X, W, scales, zeros, Y), stream)
     if Y is None:
         Y = _new((M, N), torch.bfloat16, X, stream)
-    elif _typed(Y, torch.bfloat16, "Y", contiguous=False).shape != (M, N) or Y.stride(1) != 1:
-        raise ValueError("Y must be [M, N] with unit column stride")
     _check(load().bi_gemm_int4(X.data_ptr(), X.stride(0) if M > 1 else K, W.data_ptr(), scales.data_ptr(),
                                zeros.data_ptr() if zeros is not None else None, Y.data_ptr(), Y.stride(0) if M > 1 else N,
                                M, N, K, K // groups, raw), "bi_gemm_int4")
