@@ -470,8 +470,15 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 wsh[h * ws_head + 1] = l;
             }
         }
+        const bool ok_v = !kSplitKV || mbar_wait(&fullV[slot * NG + grp], (k / (kSlots * NG)) & 1, abort_flag);
+        // rows behind the sequence's end that came with its last box (of 8, 16, 32,
+        // 64 or 128 rows): whatever stands there, p = 0 has to meet finite values
+        if (n < kChunk && p.box_rows > 0) {
+            for (int i = gw * 32 + lane; i < (-n & (p.box_rows - 1)) * (kRowBytes / 16); i += 32 * GW)
+                st_shared_v4(smem_u32(Vs + kv_piece(n + i / (kRowBytes / 16), i % (kRowBytes / 16))), 0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();                     // before later bulk copies into these rows
+        }
         if (kSplitKV) {
-            const bool ok_v = mbar_wait(&fullV[slot * NG + grp], (k / (kSlots * NG)) & 1, abort_flag);
             if (group_sync_or<GW>(grp, !ok_v)) {              // the V rows did not land
                 if (gw == 0 && lane == 0) {
                     atomicOr(p.status, kDevTimeout);
