@@ -611,9 +611,10 @@ def attention_extend_int4(Q, cu_q, cache: KVInt4Cache, block_table, seq_lens, ma
     of the same values.
 
     Q bf16 [total_q, Hq, 128]; cu_q int32 [B+1]; block_table int32 [B, max_blocks];
-    seq_lens int32 [B], the new tokens (already in the cache) included. The
-    workspace (uint8, ``attention_extend_int4_workspace_size`` bytes) is
-    allocated with torch if not given."""
+    seq_lens int32 [B], the new tokens (already in the cache) included;
+    max_q_len the most new tokens of a sequence (the work is laid out for that
+    many of each). The workspace (uint8, ``attention_extend_int4_workspace_size``
+    bytes) is allocated with torch if not given."""
     import torch
     T, Hq, D = _attention_int4_args(Q, block_table, seq_lens, workspace, O)
     B = _typed(cu_q, torch.int32, "cu_q").numel() - 1
@@ -639,7 +640,8 @@ def gemm_int4(X, W, scales, zeros=None, Y=None, stream=None):
 
     X bf16 [M, K] (may be a row-strided view); W uint8 [N, K/2], two codes a
     byte, low nibble for even k; scales bf16 [N, K/g]; zeros uint8 [N, K/g] or
-    None (8 throughout). A weight is (code - zero) * scale."""
+    None (8 throughout). A weight is (code - zero) * scale. Made for few rows:
+    beyond 32, ``gemm_bf16`` over bf16 weights is faster (see bi.h)."""
     import torch
     _typed(X, torch.bfloat16, "X", contiguous=False), _typed(W, torch.uint8, "W"), _typed(scales, torch.bfloat16, "scales")
     xs, ws, ss = X.shape, W.shape, scales.shape

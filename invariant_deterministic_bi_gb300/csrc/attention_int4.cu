@@ -23,12 +23,12 @@
 //   chunk results are merged in chunk order and o / l is rounded to bf16.
 //
 // What bounds it: not HBM (3.6 times fewer bytes than bf16 leave 45 us at
-// 64 x 4096 tokens, 8 KV heads) but expanding the codes: 128 words of eight an
-// item and lane, 12 or 13 instructions each, on pipes that overlap only partly
-// with each other and with mma.sync (a word and a product: 21.6-24.7 cycles per
-// warp and scheduler, 17 and 8 apart). Measured (GB300): 64 x 4096, 32 heads over 8
-// 91 us, 3.3 TB/s (bf16 cache: 187 us); 1 x 4096 10.1 us; 2 x 131072, 64 over 8
-// heads 103 us; 16 sequences x 5 new tokens over 100..4000 59 us. Per warp two 9 KB
+// 64 x 4096 tokens, 8 KV heads) but its instructions, 3184 an item: expanding 128
+// words of eight codes takes 1408 of them, their scales 256, mma.sync 192, softmax,
+// transposes, stores and the walk the rest, on pipes that overlap only partly (a
+// word and a product: 21.6-24.7 cycles per warp and scheduler, 17 and 8 apart). Measured (GB300): 64 x 4096, 32 heads over 8
+// 91 us, 3.3 TB/s (bf16 cache: 187 us); 1 x 4096 10.1 us (9.9); 2 x 131072, 64 over
+// 8 heads 102 us; 16 sequences x 5 new tokens over 100..4000 58 us. Per warp two 9 KB
 // buffers and 12 warps; 16 warps with three 4.5 KB buffers each took 102 us (the
 // pipes, not the latencies, are what a warp waits for); reading the codes from
 // global memory into registers, 133 us.
@@ -49,11 +49,16 @@ constexpr int kRecord = kD + 2;                // floats of a chunk result: m, l
 constexpr int kMergeThreads = 128;             // and a warp that loads
 constexpr int kMergeTile = 32, kMergeRing = 8; // chunk results of a tile, tiles on the way at most
 constexpr int kMergeStage = (kMergeTile * kRecord * 4 + 16 + 15) / 16 * 16;
-// Extend takes this split or the tiled kernel by their estimated times (the sizes decide, not the data): a CTA of
-// the tiled kernel spends about 13 K cycles on a chunk for up to 128 query rows, one CTA an SM and no split of the
-// chunks; an SM here about 1.7 K for each eight rows. Measured, 32 heads over 8, 4000 cached tokens, tiled / split:
-// 16 sequences x 5 tokens 262 / 77 us, x 16 229 / 196; 1 x 5 257 / 12, 1 x 16 217 / 21, 4 x 8 (64 heads) 222 / 53;
-// 64 x 16 over 2000 458 / 407. The chunk results take at most kFewBytes.
+// Extend takes this split or the tiled kernel by their estimated times (the sizes decide, not the data; the SMs are
+// these because the workspace's size is asked for without a device): a CTA of the tiled kernel spends about 13 K cycles
+// on a chunk for up to 128 query rows, one CTA an SM and no split of the chunks; an SM here about 1.7 K for each eight
+// rows. Measured, 32 heads over 8, 4000 cached tokens each, tiled / split: 16 sequences x 5 tokens 263 / 75 us, x 16
+// 227 / 194; 1 x 5 257 / 13, 1 x 16 215 / 22, 1 x 64 203 / 52, 4 x 8 (64 heads) 218 / 53; 64 x 16 over 2000 455 / 405;
+// 64 x 1 over 4096 1057 / 103. The estimate knows neither the number of sequences nor their tokens, only the sum and
+// max_q, and both kernels work for max_q tokens of each sequence, so uneven batches are not what it is made for:
+// 63 x 1 and one x 64 over 4096 1059 / 553, one x 200 1073 / 1065, one x 512 1288 (tiled); 255 x 1 and one x 64 over
+// 1000 951 (tiled); 256 x 1 over 1000 with max_q 256 1005 / 2649, where it takes the split, with max_q 1 940 / 106.
+// The chunk results take at most kFewBytes.
 constexpr int64_t kSms = 152, kTiledCost = 130, kSplitCost = 17;
 constexpr int64_t kFewBytes = 512ll << 20;
 

@@ -32,9 +32,11 @@
 // scheduler has 22 cycles for a word; tiles spend 44 % of their cycles in mma.sync,
 // 38 % and 19 % in the other two. Measured (GB300, weights from HBM), M = 1:
 // 6144 x 4096, g = 128 7.7 us (1.7 TB/s; without the products 4.5), 24576 x 4096
-// 18.3 us (2.9 TB/s; 10.5); M = 16, 24576 x 4096, g = 64 with zeros 29.8 us; M = 200,
+// 18.3 us (2.9 TB/s; 10.4); M = 16, 24576 x 4096, g = 64 with zeros 29.8 us; M = 200,
 // 4096 x 12288 111 us (g = 128) and 118 us (g = 32); M = 2048, 6144 x 4096 421 us
-// (245 TFLOP/s). A form with the expanded weights in tensor memory and tcgen05
+// (245 TFLOP/s). bi_gemm_bf16 over bf16 weights, which gives other bits, takes 16.6,
+// 48.9, 49.9 (M = 16), 32 (M = 200) and 66 us: from 33 rows on it is the faster one
+// (6144 x 4096: from 17). A form with the expanded weights in tensor memory and tcgen05
 // products took 13.9, 39.9, 48, 88, 146 and 334 us in that order: faster for many
 // rows, but every M has to give the same bits, which the two products do not, and
 // few rows are what the call is for. Tiles of 128 rows of X (half the expansions a
