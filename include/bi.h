@@ -529,6 +529,136 @@ BI_API bi_status bi_attention_extend_int4(const void *Q, const int32_t *cu_q, in
 BI_API bi_status bi_gemm_int4(const void *X, int64_t ldx, const uint8_t *W, const void *scales, const uint8_t *zeros,
                               void *Y, int64_t ldy, int64_t M, int64_t N, int64_t K, int64_t group, bi_stream stream);
 
+/*
+ * ---- From the qkv projection to the attention: rotary positions, norms of the
+ * query and key heads, and the way into the paged bf16 cache. The pages test
+ * models that need all three (Qwen3-8B, Qwen3-30B-A3B; vllm-ascend guide,
+ * Tested Models). Every row (one head of one token) is computed alone, in fp32,
+ * and rounded once: its bits depend on its own values, position and weights.
+ *
+ * Rotation: at position p the pair (a, b) of frequency f_i, i < rotary_dim / 2,
+ *   -> (factor * (a cos p f_i - b sin p f_i), factor * (b cos p f_i + a sin p f_i)),
+ * the pair being dimensions (i, i + rotary_dim / 2), or (2i, 2i + 1) interleaved;
+ * dimensions from rotary_dim on stay as they are. The frequencies are held in
+ * turns per position as 64-bit fractions (f / 2 pi = turns * 2^-64), so that the
+ * angle of any position is exact to 2^-65 turns a position.
+ * Norm: x / sqrt(mean x^2 + eps) * w over the head's dimensions, before the rotation.
+ *
+ *   positions i64 [T] (device)  any that fits in 32 bits, negative ones too (they turn
+ *             back); a token with another is skipped, status BI_ERR_INVALID_ARG
+ *   turns     u64 [rotary_dim / 2] (device), made by bi_rope_freqs
+ * Heads of a token are contiguous; tokens may be ld elements apart (slices of a
+ * fused projection need no copy). Outputs may be the inputs themselves (same
+ * pointer and ld); any other overlap is not allowed.
+ * Requirements: head_dim and rotary_dim multiples of 16, rotary_dim <= head_dim
+ * <= 256; ld >= heads * head_dim, multiples of 8; T, heads < 2^31, heads <= 2^20.
+ */
+typedef struct {
+    const uint64_t *turns;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    float factor;
+} bi_rope_t;
+
+/*
+ * bi_rope_freqs -- the frequencies on the host (no GPU needed): turns[i] for
+ * i < rotary_dim / 2, and the factor of cos and sin.
+ *   f_i = base^(-2i / rotary_dim), for longer contexts scaled by s = `scale`:
+ *   BI_ROPE_LINEAR  f / s
+ *   BI_ROPE_NTK     base * s^(R / (R - 2)) for base, R = rotary_dim
+ *   BI_ROPE_BANDS   by n = original_length f / 2 pi, the turns over the original length: n > high: f; n < low: f / s;
+ *                   between, with t = (n - low) / (high - low): f (t + (1 - t) / s)
+ *   BI_ROPE_YARN    dim(n) = R ln(original_length / (2 pi n)) / (2 ln base), a = max(floor dim(high), 0),
+ *                   b = min(ceil dim(low), R - 1), t = (i - a) / max(b - a, 0.001) kept in [0, 1]:
+ *                   f (1 - t + t / s); factor = 0.1 ln s + 1 for s > 1
+ *   BI_ROPE_GIVEN   f_i = given[i]
+ * factor is 1 but for BI_ROPE_YARN. Computed in double precision.
+ * Requirements: rotary_dim a multiple of 16, at most 256; base > 1, scale > 0, and for the last two original_length > 0,
+ * 0 < low < high (all finite); given frequencies finite, below 2^40 in magnitude.
+ */
+enum { BI_ROPE_NONE = 0, BI_ROPE_LINEAR = 1, BI_ROPE_NTK = 2, BI_ROPE_BANDS = 3, BI_ROPE_YARN = 4, BI_ROPE_GIVEN = 5 };
+BI_API bi_status bi_rope_freqs(int32_t rotary_dim, int32_t scaling, double base, double scale, double original_length,
+                               double low, double high, const double *given, uint64_t *turns, float *factor);
+
+/* bi_rope -- rotate heads: Y[t][h] = rotation of X[t][h] at positions[t]. X, Y bf16 [T][H][head_dim]. */
+BI_API bi_status bi_rope(const void *X, int64_t ldx, const int64_t *positions, int64_t T, int32_t H, int32_t head_dim,
+                         const bi_rope_t *rope, void *Y, int64_t ldy, bi_stream stream);
+
+/*
+ * bi_qk_norm_rope -- RMSNorm of every query and key head with the rotation in
+ * the same pass: Q, Q_out bf16 [T][Hq][head_dim], K, K_out [T][Hkv][head_dim],
+ * q_weight, k_weight bf16 [head_dim]. rope NULL: the norms alone (positions not read).
+ */
+BI_API bi_status bi_qk_norm_rope(const void *Q, int64_t ldq, const void *K, int64_t ldk, const void *q_weight,
+                                 const void *k_weight, float eps, const int64_t *positions, int64_t T, int32_t Hq,
+                                 int32_t Hkv, int32_t head_dim, const bi_rope_t *rope, void *Q_out, int64_t ldqo,
+                                 void *K_out, int64_t ldko, bi_stream stream);
+
+/*
+ * bi_kv_append -- keys and values of T tokens into the paged bf16 cache that
+ * bi_attention_decode and bi_attention_extend read, the keys normed (k_weight
+ * given) and rotated (rope given) on the way, the values as they are; and, in the
+ * same launch, the tokens' queries normed (q_weight) and rotated to Q_out.
+ *   K, V     bf16, token t's [Hkv][head_dim] at K + t * ldk, V + t * ldv
+ *   slots    i64 [T] (device)  token t goes to block slots[t] / block_size, offset
+ *            slots[t] % block_size; -1: its key and value are not stored (padding, or
+ *            a token that the cache holds already). The slots of one call must differ.
+ *   K_cache, V_cache  bf16 [num_blocks][block_size][Hkv][head_dim]
+ *   Q, Q_out bf16 [T][Hq][head_dim], whatever the token's slot; Hq = 0: no queries (both NULL)
+ *   k_weight, q_weight, rope  NULL: no norm, no rotation (positions not read)
+ * A slot outside the cache is like -1 and the device status becomes
+ * BI_ERR_INVALID_ARG. Everything else in the cache stays as it was.
+ * K and V rows are the bits of bi_qk_norm_rope and of V. Requirements as above, and
+ * num_blocks * block_size < 2^40.
+ */
+BI_API bi_status bi_kv_append(const void *K, int64_t ldk, const void *V, int64_t ldv, int64_t T, const int64_t *slots,
+                              const void *k_weight, float eps, const int64_t *positions, const bi_rope_t *rope,
+                              void *K_cache, void *V_cache, int64_t num_blocks, int32_t Hkv, int32_t head_dim,
+                              int32_t block_size, const void *Q, int64_t ldq, const void *q_weight, int32_t Hq,
+                              void *Q_out, int64_t ldqo, bi_stream stream);
+
+/*
+ * ---- Sliding window. bi_attention_decode and bi_attention_extend where the
+ * token at position p sees the cached tokens j <= p with j > p - window or
+ * j < sinks (the first tokens, which stay visible). A sequence's chunks are the
+ * same 128 tokens by position; those in which the token sees nothing are left
+ * out, and the rest are computed and merged in chunk order as in the calls
+ * without a window: a token's bits depend on its position, window and sinks, not on the
+ * batch, and decode and extend give the same ones. Where the window holds every
+ * token, they are the bits of the calls without one (but for the cases below).
+ *   window >= 1, sinks >= 0 (values beyond BI_ATTENTION_MAX_SEQ_LEN count as that)
+ * A block that holds no token in sight is not read and its table entry may be
+ * anything (-1 for a block that was given back); in a block that holds some, what
+ * stands in the places out of sight has no effect, not even infinities and NaN
+ * (nor, in extend, on tokens of the same call for which they are out of sight).
+ * A block in sight that lies outside the cache is ignored, status
+ * BI_ERR_INVALID_ARG; a chunk of whose tokens in sight none is in the cache counts
+ * nothing. (A token that sees none in the cache has nothing to weigh: NaN.)
+ * Arguments, requirements and workspaces as in the calls without a window;
+ * bi_attention_decode_window_workspace_size is at most their size.
+ */
+BI_API int64_t bi_attention_decode_window_workspace_size(int64_t B, int32_t Hq, int32_t max_seq_len, int32_t window,
+                                                         int32_t sinks);
+BI_API bi_status bi_attention_decode_window(const void *Q, const void *K_cache, const void *V_cache,
+                                            const int32_t *block_table, int32_t max_blocks_per_seq, int64_t num_blocks,
+                                            const int32_t *seq_lens, int64_t B, int32_t Hq, int32_t Hkv,
+                                            int32_t head_dim, int32_t block_size, int32_t max_seq_len, float scale,
+                                            int32_t window, int32_t sinks, void *workspace, int64_t workspace_bytes,
+                                            void *O, bi_stream stream);
+/*
+ * workspace  caller-owned device scratch, NULLABLE: with at least
+ *            bi_attention_extend_window_workspace_size(...) > 0 bytes, calls with
+ *            few new tokens are split over the chunks like decode. The bits are the same.
+ */
+BI_API int64_t bi_attention_extend_window_workspace_size(int64_t total_q, int32_t Hq, int32_t Hkv, int32_t max_seq_len,
+                                                         int32_t max_q_len, int32_t window, int32_t sinks);
+BI_API bi_status bi_attention_extend_window(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K_cache,
+                                            const void *V_cache, const int32_t *block_table, int32_t max_blocks_per_seq,
+                                            int64_t num_blocks, const int32_t *seq_lens, int64_t B, int32_t Hq,
+                                            int32_t Hkv, int32_t head_dim, int32_t block_size, int32_t max_seq_len,
+                                            int32_t max_q_len, float scale, int32_t window, int32_t sinks,
+                                            void *workspace, int64_t workspace_bytes, void *O, bi_stream stream);
+
 /* Operation ids for bi_plan. */
 enum { BI_OP_GEMM_BF16 = 0, BI_OP_GROUPED_GEMM_BF16 = 1, BI_OP_GEMM_NVFP4 = 2, BI_OP_RMSNORM = 3,
        BI_OP_QUANTIZE_NVFP4 = 4, BI_OP_GROUPED_GEMM_SILU_BF16 = 5 /* N carries I */ };

@@ -9,11 +9,15 @@ is no CPU or PyTorch fallback. If the library is missing this module raises.
 Names follow the C ABI: ``gemm_bf16``, ``grouped_gemm_bf16``, ``gemm_nvfp4``,
 ``quantize_nvfp4``, ``rmsnorm``, ``plan``, ``device_status``, ``check_wait_timeout``;
 the 4-bit forms ``kv_int4_cache``, ``kv_int4_append``, ``kv_int4_read``,
-``attention_decode_int4``, ``attention_extend_int4``, ``gemm_int4``.
+``attention_decode_int4``, ``attention_extend_int4``, ``gemm_int4``; from the
+projection to the attention ``rope_freqs``, ``rope``, ``qk_norm_rope``,
+``kv_append``; with a sliding window ``attention_decode_window``,
+``attention_extend_window``.
 """
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 
@@ -61,7 +65,7 @@ def load() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"libbi.so is not built ({LIB_PATH}); run __graft_entry__.build() first")
         lib = ctypes.CDLL(LIB_PATH)
-        P, I64, I32, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+        P, I64, I32, F, D = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_double
         sig = {
             "bi_gemm_bf16": [P, I64, P, I64, P, I64, I64, I64, I64, P],
             "bi_grouped_gemm_bf16": [P, P, P, P, I32, I64, I64, I64, P],
@@ -89,6 +93,15 @@ def load() -> ctypes.CDLL:
                                          I64, P, P],
             "bi_attention_extend_int4_workspace_size": [I64, I32, I32, I32, I32],
             "bi_gemm_int4": [P, I64, P, P, P, P, I64, I64, I64, I64, I64, P],
+            "bi_rope_freqs": [I32, I32, D, D, D, D, D, P, P, ctypes.POINTER(F)],
+            "bi_rope": [P, I64, P, I64, I32, I32, P, P, I64, P],
+            "bi_qk_norm_rope": [P, I64, P, I64, P, P, F, P, I64, I32, I32, I32, P, P, I64, P, I64, P],
+            "bi_kv_append": [P, I64, P, I64, I64, P, P, F, P, P, P, P, I64, I32, I32, I32, P, I64, P, I32, P, I64, P],
+            "bi_attention_decode_window_workspace_size": [I64, I32, I32, I32, I32],
+            "bi_attention_decode_window": [P, P, P, P, I32, I64, P, I64, I32, I32, I32, I32, I32, F, I32, I32, P, I64, P, P],
+            "bi_attention_extend_window_workspace_size": [I64, I32, I32, I32, I32, I32, I32],
+            "bi_attention_extend_window": [P, P, I32, P, P, P, I32, I64, P, I64, I32, I32, I32, I32, I32, I32, F, I32, I32,
+                                           P, I64, P, P],
             "bi_plan": [I32, I64, I64, I64, I32, ctypes.POINTER(Plan)],
             "bi_device_status": [P],
             "bi_check_wait_timeout": [ctypes.c_uint32, P],
@@ -101,7 +114,9 @@ def load() -> ctypes.CDLL:
             fn.restype = ctypes.c_int
         lib.bi_status_string.restype = ctypes.c_char_p
         lib.bi_attention_decode_workspace_size.restype = ctypes.c_int64
-        lib.bi_attention_extend_int4_workspace_size.restype = ctypes.c_int64
+        for name in ("bi_attention_extend_int4_workspace_size", "bi_attention_decode_window_workspace_size",
+                     "bi_attention_extend_window_workspace_size"):
+            getattr(lib, name).restype = ctypes.c_int64
         _lib = lib
         return lib
 
@@ -663,6 +678,250 @@ def gemm_int4(X, W, scales, zeros=None, Y=None, stream=None):
                                zeros.data_ptr() if zeros is not None else None, Y.data_ptr(), Y.stride(0) if M > 1 else N,
                                M, N, K, K // groups, raw), "bi_gemm_int4")
     return Y
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("factor", ctypes.c_float)]
+
+
+class RopeFreqs:
+    """The frequencies of a rotation (made by ``rope_freqs``): turns int64 [rotary_dim / 2] on the GPU, turns per
+    position in units of 2^-64, and how they are used."""
+    __slots__ = ("turns", "rotary_dim", "interleaved", "factor", "_c")
+
+    def __init__(self, turns, rotary_dim: int, interleaved: bool = False, factor: float = 1.0):
+        import torch
+        _typed(turns, torch.int64, "turns")
+        if tuple(turns.shape) != (rotary_dim // 2,) or rotary_dim % 2:
+            raise ValueError(f"turns must be [rotary_dim / 2] = [{rotary_dim / 2:g}], got {tuple(turns.shape)}")
+        for n, v in (("turns", turns), ("rotary_dim", int(rotary_dim)), ("interleaved", bool(interleaved)), ("factor", float(factor))):
+            object.__setattr__(self, n, v)
+        object.__setattr__(self, "_c", _Rope(turns.data_ptr(), self.rotary_dim, self.interleaved, self.factor))
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a RopeFreqs is fixed; make a new one")
+
+
+_ROPE_SCALING = {None: 0, "none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+
+
+def rope_freqs(rotary_dim: int, base: float = 10000.0, interleaved: bool = False, scaling=None, scale: float = 1.0,
+               original_length: float = 0.0, low=None, high=None, factor=None, freqs=None, device="cuda") -> RopeFreqs:
+    """Frequencies base^(-2i / rotary_dim) for ``rope``, ``qk_norm_rope`` and ``kv_append`` (formulas in bi.h).
+
+    scaling for longer contexts, by `scale`: None, "linear", "ntk", "bands" (by turns over original_length: low 1,
+    high 4 by default) or "yarn" (low 1, high 32). freqs: rotary_dim / 2 frequencies (radians a position) to use
+    instead. factor: what cos and sin are multiplied by (None: 1, or what yarn gives)."""
+    import torch
+    if freqs is not None:
+        kind, given = 5, [float(x) for x in freqs]
+        if scaling is not None or 2 * len(given) != rotary_dim:
+            raise ValueError("freqs must be rotary_dim / 2 numbers, without a scaling")
+        given = (ctypes.c_double * len(given))(*given)
+    else:
+        if scaling not in _ROPE_SCALING:
+            raise ValueError(f"scaling must be one of {sorted(k for k in _ROPE_SCALING if k)}, got {scaling!r}")
+        kind, given = _ROPE_SCALING[scaling], None
+    turns = torch.zeros(max(rotary_dim // 2, 1), dtype=torch.int64)
+    m = ctypes.c_float()
+    _check(load().bi_rope_freqs(rotary_dim, kind, base, scale, original_length, 1.0 if low is None else low,
+                                (32.0 if scaling == "yarn" else 4.0) if high is None else high, given, turns.data_ptr(),
+                                ctypes.byref(m)), "bi_rope_freqs")
+    return RopeFreqs(turns.to(device), rotary_dim, interleaved, m.value if factor is None else factor)
+
+
+def _heads(t, name, T=None, D=None):
+    """(T, heads, D, token stride) of bf16 heads [T, H, D] that are contiguous within a token."""
+    import torch
+    _typed(t, torch.bfloat16, name, contiguous=False)
+    shape = t.shape
+    if len(shape) != 3 or (T is not None and (shape[0] != T or shape[2] != D)):
+        raise ValueError(f"{name} must be [T, heads, head_dim]" + ("" if T is None else f" with T = {T}, head_dim = {D}") +
+                         f", got {tuple(shape)}")
+    T, H, D = shape
+    st = t.stride()
+    if T * H and ((D > 1 and st[2] != 1) or (H > 1 and st[1] != D)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous (a token stride is allowed)")
+    return T, H, D, st[0] if T > 1 else H * D
+
+
+def _rope_args(positions, freqs, T):
+    """(pointers of positions and rotation, tensors to check) -- both or neither given."""
+    import torch
+    if freqs is None:
+        if positions is not None:
+            raise ValueError("positions without freqs")
+        return None, None, ()
+    if not isinstance(freqs, RopeFreqs):
+        raise TypeError("freqs must be a RopeFreqs")
+    if _typed(positions, torch.int64, "positions").shape != (T,):
+        raise ValueError(f"positions must be [T] = [{T}], got {tuple(positions.shape)}")
+    return positions.data_ptr(), ctypes.byref(freqs._c), (positions, freqs.turns)
+
+
+def _weight(w, D, name):
+    import torch
+    if _typed(w, torch.bfloat16, name).shape != (D,):
+        raise ValueError(f"{name} must be [head_dim] = [{D}], got {tuple(w.shape)}")
+    return w
+
+
+def rope(X, positions, freqs: RopeFreqs, Y=None, stream=None):
+    """Rotary positions: Y[t, h] = X[t, h] turned by positions[t].
+
+    X bf16 [T, H, head_dim] (a token stride is allowed); positions int64 [T]. Y may be X (in place)."""
+    import torch
+    T, H, D, ldx = _heads(X, "X")
+    if freqs is None:
+        raise TypeError("freqs must be a RopeFreqs")
+    pos, c, used = _rope_args(positions, freqs, T)
+    if Y is not None and _heads(Y, "Y", T, D)[1] != H:
+        raise ValueError("Y must have X's shape")
+    raw, _ = _launch_on(None, (X, Y, *used), stream)
+    if Y is None:
+        Y = _new((T, H, D), torch.bfloat16, X, stream)
+    _check(load().bi_rope(X.data_ptr(), ldx, pos, T, H, D, c, Y.data_ptr(), _heads(Y, "Y")[3], raw), "bi_rope")
+    return Y
+
+
+def qk_norm_rope(Q, K, q_weight, k_weight, eps: float, positions=None, freqs=None, Q_out=None, K_out=None, stream=None):
+    """(Q_out, K_out): every query and key head normed (x / sqrt(mean x^2 + eps) * weight) and turned by its position.
+
+    Q bf16 [T, Hq, head_dim], K [T, Hkv, head_dim] (token strides allowed); weights bf16 [head_dim];
+    positions int64 [T]; freqs None: the norms alone. Q_out may be Q and K_out K (in place)."""
+    import torch
+    T, Hq, D, ldq = _heads(Q, "Q")
+    _, Hkv, _, ldk = _heads(K, "K", T, D)
+    _weight(q_weight, D, "q_weight"), _weight(k_weight, D, "k_weight")
+    pos, c, used = _rope_args(positions, freqs, T)
+    for t, H, n in ((Q_out, Hq, "Q_out"), (K_out, Hkv, "K_out")):
+        if t is not None and _heads(t, n, T, D)[1] != H:
+            raise ValueError(f"{n} must be {(T, H, D)}, got {tuple(t.shape)}")
+    raw, _ = _launch_on(None, (Q, K, q_weight, k_weight, Q_out, K_out, *used), stream)
+    if Q_out is None:
+        Q_out = _new((T, Hq, D), torch.bfloat16, Q, stream)
+    if K_out is None:
+        K_out = _new((T, Hkv, D), torch.bfloat16, K, stream)
+    _check(load().bi_qk_norm_rope(Q.data_ptr(), ldq, K.data_ptr(), ldk, q_weight.data_ptr(), k_weight.data_ptr(), float(eps),
+                                  pos, T, Hq, Hkv, D, c, Q_out.data_ptr(), _heads(Q_out, "Q_out")[3], K_out.data_ptr(),
+                                  _heads(K_out, "K_out")[3], raw), "bi_qk_norm_rope")
+    return Q_out, K_out
+
+
+def kv_append(K, V, slots, K_cache, V_cache, positions=None, freqs=None, k_weight=None, eps: float = 1e-6, Q=None,
+              q_weight=None, Q_out=None, stream=None):
+    """Store tokens' keys and values in the paged bf16 cache, the keys normed (k_weight) and turned (positions, freqs)
+    on the way; with Q, norm and turn the same tokens' queries in the same launch. Returns Q_out (None without Q).
+
+    K, V bf16 [T, Hkv, head_dim] and Q [T, Hq, head_dim] (token strides allowed: slices of a fused projection);
+    slots int64 [T]: block * block_size + offset, -1 to store nothing for a token (its query is computed all the
+    same). The slots of one call must differ. K_cache, V_cache bf16 [blocks, block_size, Hkv, head_dim]. Q_out may be Q."""
+    import torch
+    T, Hkv, D, ldk = _heads(K, "K")
+    _, Hv, _, ldv = _heads(V, "V", T, D)
+    if Hv != Hkv or _slots(slots) != T:
+        raise ValueError(f"shape mismatch K{tuple(K.shape)} V{tuple(V.shape)} slots{tuple(slots.shape)}")
+    shape = _typed(K_cache, torch.bfloat16, "K_cache").shape
+    if len(shape) != 4 or tuple(shape[2:]) != (Hkv, D) or _typed(V_cache, torch.bfloat16, "V_cache").shape != shape:
+        raise ValueError(f"K_cache and V_cache must be [blocks, block_size, {Hkv}, {D}], got {tuple(shape)} and {tuple(V_cache.shape)}")
+    if k_weight is not None:
+        _weight(k_weight, D, "k_weight")
+    pos, c, used = _rope_args(positions, freqs, T)
+    Hq = ldq = 0
+    if Q is not None:
+        _, Hq, _, ldq = _heads(Q, "Q", T, D)
+        if q_weight is not None:
+            _weight(q_weight, D, "q_weight")
+        if Q_out is not None and _heads(Q_out, "Q_out", T, D)[1] != Hq:
+            raise ValueError(f"Q_out must be {(T, Hq, D)}, got {tuple(Q_out.shape)}")
+    elif q_weight is not None or Q_out is not None:
+        raise ValueError("q_weight and Q_out belong to Q")
+    raw, _ = _launch_on(None, (K, V, slots, K_cache, V_cache, k_weight, Q, q_weight, Q_out, *used), stream)
+    if Q is not None and Q_out is None:
+        Q_out = _new((T, Hq, D), torch.bfloat16, Q, stream)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    _check(load().bi_kv_append(K.data_ptr(), ldk, V.data_ptr(), ldv, T, slots.data_ptr(), ptr(k_weight), float(eps), pos, c,
+                               K_cache.data_ptr(), V_cache.data_ptr(), shape[0], Hkv, D, shape[1], ptr(Q), ldq, ptr(q_weight), Hq,
+                               ptr(Q_out), 0 if Q_out is None else _heads(Q_out, "Q_out")[3], raw), "bi_kv_append")
+    return Q_out
+
+
+def _attention_window_args(Q, K_cache, V_cache, block_table, seq_lens, workspace, O):
+    """Checks shared by the windowed calls: Q's and the cache's shapes."""
+    import torch
+    shape = _attention_int4_args(Q, block_table, seq_lens, workspace, O)
+    cache = _typed(K_cache, torch.bfloat16, "K_cache").shape
+    if len(cache) != 4 or cache[3] != 128 or _typed(V_cache, torch.bfloat16, "V_cache").shape != cache:
+        raise ValueError(f"K_cache and V_cache must be [blocks, block_size, Hkv, 128], got {tuple(cache)} and {tuple(V_cache.shape)}")
+    return shape, cache
+
+
+def _window(window, sinks):
+    """Both as 32-bit numbers: anything past the longest sequence counts as that, anything below 0 is refused by the call."""
+    return tuple(max(-1, min(operator.index(x), 1 << 30)) for x in (window, sinks))
+
+
+def attention_decode_window_workspace_size(B: int, Hq: int, max_seq_len: int, window: int, sinks: int = 0) -> int:
+    window, sinks = _window(window, sinks)
+    return int(load().bi_attention_decode_window_workspace_size(B, Hq, max_seq_len, window, sinks))
+
+
+def attention_decode_window(Q, K_cache, V_cache, block_table, seq_lens, max_seq_len: int, scale: float, window: int,
+                            sinks: int = 0, workspace=None, O=None, stream=None):
+    """``attention_decode`` where a token sees the last `window` tokens (itself among them) and the first `sinks`.
+
+    Table entries of blocks out of sight may be anything (-1 once given back). The workspace (uint8,
+    ``attention_decode_window_workspace_size`` bytes) is allocated with torch if not given."""
+    import torch
+    (B, Hq, D), (nblk, bs, Hkv, _) = _attention_window_args(Q, K_cache, V_cache, block_table, seq_lens, workspace, O)
+    if seq_lens.shape != (B,):
+        raise ValueError("one query token a sequence: seq_lens must be [B], B the rows of Q")
+    window, sinks = _window(window, sinks)
+    raw, _ = _launch_on(None, (Q, K_cache, V_cache, block_table, seq_lens, workspace, O), stream)
+    if workspace is None:
+        workspace = _new(max(attention_decode_window_workspace_size(B, Hq, max_seq_len, window, sinks), 16), torch.uint8, Q, stream)
+    if O is None:
+        O = _new((B, Hq, D), torch.bfloat16, Q, stream)
+    _check(load().bi_attention_decode_window(Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), block_table.data_ptr(),
+                                             block_table.shape[1], nblk, seq_lens.data_ptr(), B, Hq, Hkv, D, bs, max_seq_len,
+                                             float(scale), window, sinks, workspace.data_ptr(), workspace.numel(), O.data_ptr(),
+                                             raw), "bi_attention_decode_window")
+    return O
+
+
+def attention_extend_window_workspace_size(total_q: int, Hq: int, Hkv: int, max_seq_len: int, max_q_len: int, window: int,
+                                           sinks: int = 0) -> int:
+    window, sinks = _window(window, sinks)
+    return int(load().bi_attention_extend_window_workspace_size(total_q, Hq, Hkv, max_seq_len, max_q_len, window, sinks))
+
+
+def attention_extend_window(Q, cu_q, K_cache, V_cache, block_table, seq_lens, max_seq_len: int, max_q_len: int, scale: float,
+                            window: int, sinks: int = 0, workspace=None, O=None, stream=None):
+    """``attention_extend`` where a token sees the last `window` tokens (itself among them) and the first `sinks`: the
+    bits of ``attention_decode_window`` of each token's cut sequence.
+
+    Table entries of blocks out of every new token's sight may be anything. The workspace (uint8,
+    ``attention_extend_window_workspace_size`` bytes) is allocated with torch if not given."""
+    import torch
+    (T, Hq, D), (nblk, bs, Hkv, _) = _attention_window_args(Q, K_cache, V_cache, block_table, seq_lens, workspace, O)
+    B = _typed(cu_q, torch.int32, "cu_q").numel() - 1
+    if seq_lens.shape != (B,):
+        raise ValueError("cu_q must have one entry more than seq_lens")
+    window, sinks = _window(window, sinks)
+    raw, _ = _launch_on(None, (Q, cu_q, K_cache, V_cache, block_table, seq_lens, workspace, O), stream)
+    if workspace is None:
+        need = attention_extend_window_workspace_size(T, Hq, Hkv, max_seq_len, max_q_len, window, sinks)
+        workspace = _new(need, torch.uint8, Q, stream) if need > 0 else None
+    if O is None:
+        O = _new((T, Hq, D), torch.bfloat16, Q, stream)
+    _check(load().bi_attention_extend_window(Q.data_ptr(), cu_q.data_ptr(), T, K_cache.data_ptr(), V_cache.data_ptr(),
+                                             block_table.data_ptr(), block_table.shape[1], nblk, seq_lens.data_ptr(), B, Hq, Hkv,
+                                             D, bs, max_seq_len, max_q_len, float(scale), window, sinks,
+                                             workspace.data_ptr() if workspace is not None else None,
+                                             workspace.numel() if workspace is not None else 0, O.data_ptr(), raw),
+           "bi_attention_extend_window")
+    return O
 
 
 def plan(op: int, M: int, N: int, K: int, num_sms: int = 0) -> dict:

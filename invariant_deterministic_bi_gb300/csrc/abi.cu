@@ -3,6 +3,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <functional>
 #include <mutex>
@@ -301,10 +302,14 @@ int64_t bi_attention_decode_workspace_size(int64_t B, int32_t Hq, int32_t max_se
     return attention_decode_workspace_bytes(B, Hq, max_seq_len);
 }
 
-bi_status bi_attention_decode(const void *Q, const void *K_cache, const void *V_cache, const int32_t *block_table,
-                              int32_t max_blocks_per_seq, int64_t num_blocks, const int32_t *seq_lens, int64_t B,
-                              int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t block_size, int32_t max_seq_len,
-                              float scale, void *workspace, int64_t workspace_bytes, void *O, bi_stream stream) {
+namespace {
+inline int32_t at_most_max_len(int32_t x) { return x < BI_ATTENTION_MAX_SEQ_LEN ? x : BI_ATTENTION_MAX_SEQ_LEN; }
+// Decode and extend attention over the bf16 cache, with a window (>= 1) or without (0).
+bi_status attention_decode(const void *Q, const void *K_cache, const void *V_cache, const int32_t *block_table,
+                           int32_t max_blocks_per_seq, int64_t num_blocks, const int32_t *seq_lens, int64_t B, int32_t Hq,
+                           int32_t Hkv, int32_t head_dim, int32_t block_size, int32_t max_seq_len, float scale,
+                           int32_t window, int32_t sinks, void *workspace, int64_t workspace_bytes, void *O,
+                           bi_stream stream) {
     if (B < 0 || B > 65535 || Hq < 1 || Hkv < 1 || block_size < 1 || max_seq_len < 1 ||
         max_seq_len > BI_ATTENTION_MAX_SEQ_LEN || max_blocks_per_seq < 1 || num_blocks < 1 || !(scale == scale))
         return BI_ERR_INVALID_ARG;
@@ -313,7 +318,7 @@ bi_status bi_attention_decode(const void *Q, const void *K_cache, const void *V_
     if (head_dim != 128 || Hq % Hkv != 0) return BI_ERR_UNSUPPORTED;
     const int32_t G = Hq / Hkv;
     if (G != 1 && G != 2 && G != 4 && G != 8) return BI_ERR_UNSUPPORTED;
-    const int64_t need = attention_decode_workspace_bytes(B, Hq, max_seq_len);
+    const int64_t need = attention_decode_workspace_bytes(B, Hq, max_seq_len, window, sinks);
     if (need < 0 || workspace_bytes < need) return BI_ERR_INVALID_ARG;
     if (!aligned16(Q) || !aligned16(K_cache) || !aligned16(V_cache) || !aligned16(O) || !aligned16(workspace) ||
         !aligned4(block_table) || !aligned4(seq_lens))
@@ -321,14 +326,14 @@ bi_status bi_attention_decode(const void *Q, const void *K_cache, const void *V_
     bi_status st = require_device();
     if (st != BI_OK) return st;
     return launch_attention_decode(Q, K_cache, V_cache, block_table, max_blocks_per_seq, num_blocks, seq_lens, B, Hq,
-                                   Hkv, head_dim, block_size, max_seq_len, scale, workspace, O, as_stream(stream));
+                                   Hkv, head_dim, block_size, max_seq_len, scale, window, sinks, workspace, O,
+                                   as_stream(stream));
 }
-
-bi_status bi_attention_extend(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K_cache,
-                              const void *V_cache, const int32_t *block_table, int32_t max_blocks_per_seq,
-                              int64_t num_blocks, const int32_t *seq_lens, int64_t B, int32_t Hq, int32_t Hkv,
-                              int32_t head_dim, int32_t block_size, int32_t max_seq_len, int32_t max_q_len, float scale,
-                              void *O, bi_stream stream) {
+bi_status attention_extend(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K_cache, const void *V_cache,
+                           const int32_t *block_table, int32_t max_blocks_per_seq, int64_t num_blocks,
+                           const int32_t *seq_lens, int64_t B, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                           int32_t block_size, int32_t max_seq_len, int32_t max_q_len, float scale, int32_t window,
+                           int32_t sinks, void *O, bi_stream stream) {
     if (B < 0 || B > 65535 || total_q < 0 || Hq < 1 || Hkv < 1 || block_size < 1 || max_seq_len < 1 ||
         max_seq_len > BI_ATTENTION_MAX_SEQ_LEN || max_q_len < 1 || max_blocks_per_seq < 1 || num_blocks < 1 ||
         !(scale == scale))
@@ -344,8 +349,63 @@ bi_status bi_attention_extend(const void *Q, const int32_t *cu_q, int32_t total_
     bi_status st = require_device();
     if (st != BI_OK) return st;
     return launch_attention_extend(Q, cu_q, total_q, K_cache, V_cache, block_table, max_blocks_per_seq, num_blocks,
-                                   seq_lens, B, Hq, Hkv, block_size, max_seq_len, max_q_len, scale, O,
+                                   seq_lens, B, Hq, Hkv, block_size, max_seq_len, max_q_len, scale, window, sinks, O,
                                    as_stream(stream));
+}
+}  // namespace
+
+bi_status bi_attention_decode(const void *Q, const void *K_cache, const void *V_cache, const int32_t *block_table,
+                              int32_t max_blocks_per_seq, int64_t num_blocks, const int32_t *seq_lens, int64_t B,
+                              int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t block_size, int32_t max_seq_len,
+                              float scale, void *workspace, int64_t workspace_bytes, void *O, bi_stream stream) {
+    return attention_decode(Q, K_cache, V_cache, block_table, max_blocks_per_seq, num_blocks, seq_lens, B, Hq, Hkv, head_dim,
+                            block_size, max_seq_len, scale, 0, 0, workspace, workspace_bytes, O, stream);
+}
+
+bi_status bi_attention_extend(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K_cache,
+                              const void *V_cache, const int32_t *block_table, int32_t max_blocks_per_seq,
+                              int64_t num_blocks, const int32_t *seq_lens, int64_t B, int32_t Hq, int32_t Hkv,
+                              int32_t head_dim, int32_t block_size, int32_t max_seq_len, int32_t max_q_len, float scale,
+                              void *O, bi_stream stream) {
+    return attention_extend(Q, cu_q, total_q, K_cache, V_cache, block_table, max_blocks_per_seq, num_blocks, seq_lens, B, Hq,
+                            Hkv, head_dim, block_size, max_seq_len, max_q_len, scale, 0, 0, O, stream);
+}
+
+int64_t bi_attention_decode_window_workspace_size(int64_t B, int32_t Hq, int32_t max_seq_len, int32_t window, int32_t sinks) {
+    if (B < 0 || Hq < 1 || max_seq_len < 1 || max_seq_len > BI_ATTENTION_MAX_SEQ_LEN || window < 1 || sinks < 0) return -1;
+    return attention_decode_workspace_bytes(B, Hq, max_seq_len, at_most_max_len(window), at_most_max_len(sinks));
+}
+
+bi_status bi_attention_decode_window(const void *Q, const void *K_cache, const void *V_cache, const int32_t *block_table,
+                                     int32_t max_blocks_per_seq, int64_t num_blocks, const int32_t *seq_lens, int64_t B,
+                                     int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t block_size, int32_t max_seq_len,
+                                     float scale, int32_t window, int32_t sinks, void *workspace, int64_t workspace_bytes,
+                                     void *O, bi_stream stream) {
+    if (window < 1 || sinks < 0) return BI_ERR_INVALID_ARG;
+    return attention_decode(Q, K_cache, V_cache, block_table, max_blocks_per_seq, num_blocks, seq_lens, B, Hq, Hkv, head_dim,
+                            block_size, max_seq_len, scale, at_most_max_len(window), at_most_max_len(sinks), workspace,
+                            workspace_bytes, O, stream);
+}
+
+int64_t bi_attention_extend_window_workspace_size(int64_t total_q, int32_t Hq, int32_t Hkv, int32_t max_seq_len,
+                                                  int32_t max_q_len, int32_t window, int32_t sinks) {
+    if (total_q < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || max_q_len < 1 || max_seq_len < 1 ||
+        max_seq_len > BI_ATTENTION_MAX_SEQ_LEN || window < 1 || sinks < 0)
+        return -1;
+    return 0;
+}
+
+bi_status bi_attention_extend_window(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K_cache,
+                                     const void *V_cache, const int32_t *block_table, int32_t max_blocks_per_seq,
+                                     int64_t num_blocks, const int32_t *seq_lens, int64_t B, int32_t Hq, int32_t Hkv,
+                                     int32_t head_dim, int32_t block_size, int32_t max_seq_len, int32_t max_q_len,
+                                     float scale, int32_t window, int32_t sinks, void *workspace, int64_t workspace_bytes,
+                                     void *O, bi_stream stream) {
+    if (window < 1 || sinks < 0 || workspace_bytes < 0) return BI_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return BI_ERR_MISALIGNED;
+    return attention_extend(Q, cu_q, total_q, K_cache, V_cache, block_table, max_blocks_per_seq, num_blocks, seq_lens, B, Hq,
+                            Hkv, head_dim, block_size, max_seq_len, max_q_len, scale, at_most_max_len(window),
+                            at_most_max_len(sinks), O, stream);
 }
 
 namespace {
@@ -482,6 +542,146 @@ bi_status bi_gemm_int4(const void *X, int64_t ldx, const uint8_t *W, const void 
     const bi_status st = require_device();
     if (st != BI_OK) return st;
     return launch_gemm_int4(X, ldx, W, scales, zeros, Y, ldy, M, N, K, group, as_stream(stream));
+}
+
+namespace {
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+// What the calls over heads share: sizes, the rotation and the positions.
+bi_status check_heads(int64_t T, int32_t head_dim, const bi_rope_t *rope, const int64_t *positions, HeadsParams *p) {
+    if (T < 0 || T >= kI32Max || head_dim < 1) return BI_ERR_INVALID_ARG;
+    if (head_dim % 16 != 0 || head_dim > 256) return BI_ERR_UNSUPPORTED;
+    p->T = T;
+    p->D = head_dim;
+    p->inv_d = 1.0f / static_cast<float>(head_dim);
+    p->cache_rows = 1;
+    if (!rope || T == 0) return BI_OK;
+    if (!rope->turns || !positions || rope->rotary_dim < 1 || rope->rotary_dim > head_dim || !(rope->factor == rope->factor))
+        return BI_ERR_INVALID_ARG;
+    if (rope->rotary_dim % 16 != 0) return BI_ERR_UNSUPPORTED;
+    if (!aligned8(rope->turns) || !aligned8(positions)) return BI_ERR_MISALIGNED;
+    p->turns = rope->turns;
+    p->R = rope->rotary_dim;
+    p->factor = rope->factor;
+    p->pos = positions;
+    return BI_OK;
+}
+// One part's heads (dst: a [T] tensor with ldd, or a cache).
+bi_status check_part(const void *src, int64_t lds, const void *w, void *dst, int64_t ldd, int32_t heads, int32_t D, bool cache,
+                     Heads *h) {
+    if (!src || !dst || heads < 1) return BI_ERR_INVALID_ARG;
+    if (heads > (1 << 20)) return BI_ERR_UNSUPPORTED;      // (offsets within a token are 32 bits)
+    if (lds < static_cast<int64_t>(heads) * D || ldd < static_cast<int64_t>(heads) * D) return BI_ERR_INVALID_ARG;
+    if (lds % 8 != 0 || ldd % 8 != 0 || !aligned16(src) || !aligned16(dst) || !aligned16(w)) return BI_ERR_MISALIGNED;
+    *h = Heads{static_cast<const uint16_t *>(src), static_cast<uint16_t *>(dst), static_cast<const uint16_t *>(w), lds, ldd,
+               heads, cache ? 1 : 0};
+    return BI_OK;
+}
+}  // namespace
+
+bi_status bi_rope_freqs(int32_t rotary_dim, int32_t scaling, double base, double scale, double original_length, double low,
+                        double high, const double *given, uint64_t *turns, float *factor) {
+    if (rotary_dim < 1 || scaling < BI_ROPE_NONE || scaling > BI_ROPE_GIVEN || !turns || !factor) return BI_ERR_INVALID_ARG;
+    if (rotary_dim % 16 != 0 || rotary_dim > 256) return BI_ERR_UNSUPPORTED;
+    const int half = rotary_dim / 2;
+    const double R = rotary_dim;
+    if (scaling == BI_ROPE_GIVEN) {
+        if (!given) return BI_ERR_INVALID_ARG;
+        for (int i = 0; i < half; ++i)
+            if (!(std::fabs(given[i]) < 0x1p40)) return BI_ERR_INVALID_ARG;
+    } else {
+        if (!(base > 1.0) || !std::isfinite(base)) return BI_ERR_INVALID_ARG;
+        if (scaling != BI_ROPE_NONE && (!(scale > 0.0) || !std::isfinite(scale))) return BI_ERR_INVALID_ARG;
+        if ((scaling == BI_ROPE_BANDS || scaling == BI_ROPE_YARN) &&
+            (!(original_length > 0.0) || !(low > 0.0) || !(high > low) || !std::isfinite(original_length) || !std::isfinite(high)))
+            return BI_ERR_INVALID_ARG;
+    }
+    if (scaling == BI_ROPE_NTK) base *= std::pow(scale, R / (R - 2.0));
+    double ramp_from = 0.0, ramp_width = 1.0;
+    if (scaling == BI_ROPE_YARN) {
+        const auto dim = [&](double n) { return R * std::log(original_length / (kTwoPi * n)) / (2.0 * std::log(base)); };
+        ramp_from = std::fmax(std::floor(dim(high)), 0.0);
+        ramp_width = std::fmax(std::fmin(std::ceil(dim(low)), R - 1.0) - ramp_from, 0.001);
+    }
+    *factor = scaling == BI_ROPE_YARN && scale > 1.0 ? static_cast<float>(0.1 * std::log(scale) + 1.0) : 1.0f;
+    for (int i = 0; i < half; ++i) {
+        double f = scaling == BI_ROPE_GIVEN ? given[i] : std::pow(base, -2.0 * i / R);
+        if (scaling == BI_ROPE_LINEAR) {
+            f /= scale;
+        } else if (scaling == BI_ROPE_BANDS) {
+            const double t = std::fmin(std::fmax((original_length * f / kTwoPi - low) / (high - low), 0.0), 1.0);
+            f *= t + (1.0 - t) / scale;
+        } else if (scaling == BI_ROPE_YARN) {
+            const double t = std::fmin(std::fmax((i - ramp_from) / ramp_width, 0.0), 1.0);
+            f *= 1.0 - t + t / scale;
+        }
+        double part = f / kTwoPi;
+        part -= std::floor(part);                          // whole turns change nothing
+        turns[i] = part < 1.0 ? static_cast<uint64_t>(std::ldexp(part, 64)) : 0u;
+    }
+    return BI_OK;
+}
+
+bi_status bi_rope(const void *X, int64_t ldx, const int64_t *positions, int64_t T, int32_t H, int32_t head_dim,
+                  const bi_rope_t *rope, void *Y, int64_t ldy, bi_stream stream) {
+    HeadsParams p{};
+    if (!rope) return BI_ERR_INVALID_ARG;
+    bi_status st = check_heads(T, head_dim, rope, positions, &p);
+    if (st != BI_OK) return st;
+    if (T == 0 || H == 0) return BI_OK;
+    st = check_part(X, ldx, nullptr, Y, ldy, H, head_dim, false, &p.part[0]);
+    if (st != BI_OK) return st;
+    st = require_device();
+    if (st != BI_OK) return st;
+    return launch_heads(p, rope->interleaved != 0, as_stream(stream));
+}
+
+bi_status bi_qk_norm_rope(const void *Q, int64_t ldq, const void *K, int64_t ldk, const void *q_weight,
+                          const void *k_weight, float eps, const int64_t *positions, int64_t T, int32_t Hq, int32_t Hkv,
+                          int32_t head_dim, const bi_rope_t *rope, void *Q_out, int64_t ldqo, void *K_out, int64_t ldko,
+                          bi_stream stream) {
+    HeadsParams p{};
+    if (!(eps >= 0.0f)) return BI_ERR_INVALID_ARG;
+    bi_status st = check_heads(T, head_dim, rope, positions, &p);
+    if (st != BI_OK) return st;
+    if (T == 0) return BI_OK;
+    if (!q_weight || !k_weight) return BI_ERR_INVALID_ARG;
+    p.eps = eps;
+    st = check_part(Q, ldq, q_weight, Q_out, ldqo, Hq, head_dim, false, &p.part[0]);
+    if (st != BI_OK) return st;
+    st = check_part(K, ldk, k_weight, K_out, ldko, Hkv, head_dim, false, &p.part[1]);
+    if (st != BI_OK) return st;
+    st = require_device();
+    if (st != BI_OK) return st;
+    return launch_heads(p, rope && rope->interleaved != 0, as_stream(stream));
+}
+
+bi_status bi_kv_append(const void *K, int64_t ldk, const void *V, int64_t ldv, int64_t T, const int64_t *slots,
+                       const void *k_weight, float eps, const int64_t *positions, const bi_rope_t *rope, void *K_cache,
+                       void *V_cache, int64_t num_blocks, int32_t Hkv, int32_t head_dim, int32_t block_size, const void *Q,
+                       int64_t ldq, const void *q_weight, int32_t Hq, void *Q_out, int64_t ldqo, bi_stream stream) {
+    HeadsParams p{};
+    if (!(eps >= 0.0f) || num_blocks < 1 || block_size < 1 || Hkv < 1 || Hq < 0) return BI_ERR_INVALID_ARG;
+    bi_status st = check_heads(T, head_dim, rope, positions, &p);
+    if (st != BI_OK) return st;
+    if (T == 0) return BI_OK;
+    if (!slots || (Hq == 0 && (Q || Q_out || q_weight))) return BI_ERR_INVALID_ARG;
+    if (num_blocks > (static_cast<int64_t>(1) << 40) / block_size) return BI_ERR_UNSUPPORTED;
+    if (!aligned8(slots)) return BI_ERR_MISALIGNED;
+    p.eps = eps;
+    p.slots = slots;
+    p.cache_rows = num_blocks * block_size;
+    const int64_t row = static_cast<int64_t>(Hkv) * head_dim;
+    if (Hq > 0) {
+        st = check_part(Q, ldq, q_weight, Q_out, ldqo, Hq, head_dim, false, &p.part[0]);
+        if (st != BI_OK) return st;
+    }
+    st = check_part(K, ldk, k_weight, K_cache, row, Hkv, head_dim, true, &p.part[1]);
+    if (st != BI_OK) return st;
+    st = check_part(V, ldv, nullptr, V_cache, row, Hkv, head_dim, true, &p.part[2]);
+    if (st != BI_OK) return st;
+    st = require_device();
+    if (st != BI_OK) return st;
+    return launch_heads(p, rope && rope->interleaved != 0, as_stream(stream));
 }
 
 bi_status bi_plan(int32_t op, int64_t M, int64_t N, int64_t K, int32_t num_sms, bi_plan_t *out) {

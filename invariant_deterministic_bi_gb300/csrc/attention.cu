@@ -74,8 +74,26 @@ struct AttnParams {
     int64_t num_blocks, batch;
     int32_t max_blocks, Hq, Hkv, bs, chunks, max_len;
     int32_t box_rows;        // tokens per TMA box of the decode loader; 0: per-row copies
+    int32_t window, sinks;   // windowed form (chunks then counts the records a head)
     float scale;
     unsigned *status;
+};
+
+// Sliding window: a token at position p sees the tokens j <= p with j > p - window
+// or j < sinks. For the earliest of some tokens (its length n, n - window = from)
+// and all after it: first tokens [0, first), then from `lo` on; of the chunks,
+// the `ns` that hold first tokens before lo's chunk c0, then c0 and the rest.
+struct Seen {
+    int first, lo, ns, c0;
+    __device__ __forceinline__ Seen(int from, int sinks) {
+        lo = max(0, from);
+        first = min(sinks, lo);
+        c0 = lo / kChunk;
+        ns = min((first + kChunk - 1) / kChunk, c0);
+    }
+    __device__ __forceinline__ int chunks(int n) const { return ns + (n + kChunk - 1) / kChunk - c0; }
+    __device__ __forceinline__ int start(int i) const { return (i < ns ? i : c0 + i - ns) * kChunk; }   // of the i-th chunk
+    __device__ __forceinline__ bool has(int j) const { return j < first || j >= lo; }
 };
 
 // A read-only load issued where it stands (the table is not written while a
@@ -151,7 +169,12 @@ __device__ __forceinline__ bool group_sync_or(int grp, bool pred) {
     return r != 0;
 }
 
-template <int G, int kSlots, int NG>
+// WIN: the windowed form. A sequence's items are the chunks in which its token
+// sees something (record c is the c-th of them); table entries, boxes and rows of
+// tokens out of sight are not read, scores there are -inf, and V rows that came
+// along are zeroed. A chunk of whose visible tokens none is in the cache counts
+// nothing (kNoScore).
+template <int G, int kSlots, int NG, bool WIN>
 __global__ void __launch_bounds__(dec_threads<kSlots>(), kSlots == 1 ? 2 : 1)
 attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const AttnParams p) {
@@ -185,20 +208,42 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         fence_mbar_init();
     }
     __syncthreads();
-    const int64_t items = p.batch * p.Hkv * static_cast<int64_t>(p.chunks);
-    // item -> (sequence b, KV head g, chunk c) and the tokens n of the chunk;
-    // false when the chunk is past the sequence (or the sequence is invalid)
-    auto item = [&](int64_t it, int64_t &b, int &g, int &c, int &n) {
+    int walk = p.chunks;                                 // chunks walked a sequence
+    if (WIN && kSlots > 1) {                             // as many as the batch's longest walk has, at least one
+        __shared__ int most;
+        if (tid == 0) most = 1;
+        __syncthreads();
+        for (int64_t b = tid; b < p.batch; b += dec_threads<kSlots>()) {
+            int L;
+            if (seq_ok(p, b, L)) atomicMax(&most, Seen(L - p.window, p.sinks).chunks(L));
+        }
+        __syncthreads();
+        walk = most;
+    }
+    const int64_t items = p.batch * p.Hkv * static_cast<int64_t>(walk);
+    // item -> (sequence b, KV head g, record c), the chunk's first token j0 and
+    // its tokens n (of which [h0, h1) are out of sight); false when the chunk is
+    // past the sequence (or the sequence is invalid)
+    auto item = [&](int64_t it, int64_t &b, int &g, int &c, int &j0, int &n, int &h0, int &h1) {
         g = static_cast<int>(it % p.Hkv);               // KV head fastest: the heads of one
         const int64_t r = it / p.Hkv;                    // cache block are read together
-        c = static_cast<int>(r % p.chunks);
-        b = r / p.chunks;
+        c = static_cast<int>(r % walk);
+        b = r / walk;
         int L;
         if (!seq_ok(p, b, L)) {
             if (warp == kDecConsumers && lane == 0 && c == 0 && g == 0) atomicOr(p.status, kDevBadOffsets);   // loader 0
             return false;
         }
-        n = min(kChunk, L - c * kChunk);
+        j0 = c * kChunk;
+        h0 = h1 = 0;
+        if (WIN) {
+            const Seen w(L - p.window, p.sinks);
+            if (c >= w.chunks(L)) return false;
+            j0 = w.start(c);
+            h0 = max(w.first - j0, 0);
+            h1 = w.lo - j0;
+        }
+        n = min(kChunk, L - j0);
         return n > 0;
     };
 
@@ -220,7 +265,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             // reads box i's) are requested before its sequence length is
             // known, so the two reads overlap instead of following each other
             int32_t spec_blk = -1;
-            if (p.box_rows > 0) {
+            if (!WIN && p.box_rows > 0) {
                 const int64_t r = it / p.Hkv;
                 const int64_t bb = r / p.chunks;
                 const int64_t bi = ((r % p.chunks) * kChunk + lane * p.box_rows) / p.bs;
@@ -228,28 +273,30 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     spec_blk = ld_nc_s32(p.table + bb * p.max_blocks + bi);
             }
             int64_t b;
-            int g, c, n;
-            if (!item(it, b, g, c, n)) continue;
+            int g, c, j0, n, h0, h1;
+            if (!item(it, b, g, c, j0, n, h0, h1)) continue;
             if (k % kSlots != lw) {
                 ++k;
                 continue;
             }
             // the block-table reads first: they do not touch the slot
-            const int j0 = c * kChunk;
             int64_t off[kChunk / 32];                 // per-row copies: element offset of each row, -1: none
             bool ok_row[kChunk / 32];                 // the row's block is inside the cache
             int32_t box_blk = -1;                     // boxes: lane i < nbox holds box i's block
             const int nbox = p.box_rows > 0 ? (n + p.box_rows - 1) / p.box_rows : 0;
+            // this lane's box is loaded: it has a token in sight
+            const bool box = lane < nbox && (!WIN || lane * p.box_rows < h0 || (lane + 1) * p.box_rows > h1);
             if (p.box_rows > 0) {
-                if (lane < nbox) {
-                    box_blk = spec_blk;            // p.table[b][(j0 + lane * box_rows) / bs]
+                if (box) {
+                    box_blk = WIN ? ld_nc_s32(p.table + b * p.max_blocks + (j0 + lane * p.box_rows) / p.bs)
+                                  : spec_blk;      // p.table[b][(j0 + lane * box_rows) / bs]
                     if (box_blk < 0 || box_blk >= p.num_blocks) atomicOr(p.status, kDevBadOffsets);
                 }
 #pragma unroll
                 for (int i = 0; i < kChunk / 32; ++i) {
                     const int t = lane + 32 * i;
                     const int32_t blk = __shfl_sync(0xffffffffu, box_blk, t / p.box_rows);
-                    ok_row[i] = t < n && blk >= 0 && blk < p.num_blocks;
+                    ok_row[i] = t < n && blk >= 0 && blk < p.num_blocks && !(WIN && t >= h0 && t < h1);
                     off[i] = -1;
                 }
             } else {
@@ -257,7 +304,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 for (int i = 0; i < kChunk / 32; ++i) {
                     const int t = lane + 32 * i;
                     off[i] = -1;
-                    if (t < n) {
+                    if (t < n && !(WIN && t >= h0 && t < h1)) {
                         const int j = j0 + t;
                         const int64_t blk = p.table[b * p.max_blocks + j / p.bs];
                         if (blk >= 0 && blk < p.num_blocks)
@@ -286,7 +333,8 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             const uint16_t *qsrc = p.Q + (b * p.Hq + g * G) * kD;
             if (p.box_rows > 0) {
                 // one box per cache block (box_rows tokens), both halves
-                const int kv_bytes = nbox * p.box_rows * 2 * 128;   // the K rows, or the V rows
+                const int boxes = WIN ? __popc(__ballot_sync(0xffffffffu, box)) : nbox;
+                const int kv_bytes = boxes * p.box_rows * 2 * 128;  // the K rows, or the V rows
                 const int tok = (j0 + lane * p.box_rows) % p.bs;
                 // V rows no box reaches (a chunk past the sequence's end) become
                 // zero, so that p = 0 meets finite values there; each lane's
@@ -315,7 +363,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 if (kSplitKV) {
                     // q and K first: the scores need them before p.V needs V
                     if (lane == 0) bulk_load(qs, qsrc, G * kRowBytes, fb);
-                    if (lane < nbox) {                // a block outside the cache arrives as zeros
+                    if (box) {                        // a block outside the cache arrives as zeros
 #pragma unroll
                         for (int half = 0; half < 2; ++half)
                             tma_load_4d_hint(Ks + half * kHalfTile + lane * p.box_rows * 128, &tmK, fb, half * 64, g,
@@ -327,7 +375,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     else
                         mbar_arrive(fbv);
                     __syncwarp();
-                    if (lane < nbox) {
+                    if (box) {
 #pragma unroll
                         for (int half = 0; half < 2; ++half)
                             tma_load_4d_hint(Vs + half * kHalfTile + lane * p.box_rows * 128, &tmV, fbv, half * 64, g,
@@ -335,7 +383,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     }
                 } else {
                     // the ring consumes a slot whole: K and V boxes in turn, then q
-                    if (lane < nbox) {
+                    if (box) {
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             const int dst = half * kHalfTile + lane * p.box_rows * 128;
@@ -391,8 +439,8 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     int k = 0;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         int64_t b;
-        int g, c, n;
-        if (!item(it, b, g, c, n)) continue;
+        int g, c, j0, n, h0, h1;
+        if (!item(it, b, g, c, j0, n, h0, h1)) continue;
         if (k % NG != grp) {
             ++k;
             continue;
@@ -457,6 +505,11 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             for (int t = lane; t < n; t += 32) m = fmaxf(m, Sh[t]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (WIN) {                                        // no visible token in the cache
+                int any = 0;
+                for (int t = lane; t < n; t += 32) any |= vrow[t];
+                if (!__any_sync(0xffffffffu, any)) m = kNoScore;
+            }
             float l = 0.0f;
             for (int t = lane; t < n; t += 32) {
                 const float e = expf(Sh[t] - m);
@@ -472,11 +525,18 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         }
         const bool ok_v = !kSplitKV || mbar_wait(&fullV[slot * NG + grp], (k / (kSlots * NG)) & 1, abort_flag);
         // rows behind the sequence's end that came with its last box (of 8, 16, 32,
-        // 64 or 128 rows): whatever stands there, p = 0 has to meet finite values
+        // 64 or 128 rows), and rows out of sight: whatever stands there, p = 0 has to
+        // meet finite values
         if (n < kChunk && p.box_rows > 0) {
             for (int i = gw * 32 + lane; i < (-n & (p.box_rows - 1)) * (kRowBytes / 16); i += 32 * GW)
                 st_shared_v4(smem_u32(Vs + kv_piece(n + i / (kRowBytes / 16), i % (kRowBytes / 16))), 0u, 0u, 0u, 0u);
             fence_proxy_async_smem();                     // before later bulk copies into these rows
+        }
+        if (WIN && h1 > h0 && p.box_rows > 0) {
+            const int hn = min(h1, n) - h0;
+            for (int i = gw * 32 + lane; i < hn * (kRowBytes / 16); i += 32 * GW)
+                st_shared_v4(smem_u32(Vs + kv_piece(h0 + i / (kRowBytes / 16), i % (kRowBytes / 16))), 0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
         }
         if (kSplitKV) {
             if (group_sync_or<GW>(grp, !ok_v)) {              // the V rows did not land
@@ -550,6 +610,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     }
 }
 
+template <bool WIN>
 __global__ void __launch_bounds__(kCombineThreads)
 attn_combine_kernel(const AttnParams p) {
     grid_dep_wait();      // earlier work of the stream is complete and visible
@@ -580,7 +641,7 @@ attn_combine_kernel(const AttnParams p) {
     const float lc0 = d < nt0 ? w[static_cast<int64_t>(d) * (kD + 2) + 1] : 0.0f;
     int L;
     if (!seq_ok(p, b, L)) return;
-    const int nc = (L + kChunk - 1) / kChunk;
+    const int nc = WIN ? Seen(L - p.window, p.sinks).chunks(L) : (L + kChunk - 1) / kChunk;
     if (!BI_IN_BOUNDS(nc <= p.chunks, p.status)) return;   // debug build: inside the workspace
     float o = 0.0f, l = 0.0f, m_run = -INFINITY;           // m_run: warp 0's copy of the running maximum
     // merge chunks c0 .. c0 + nt - 1 (their o values in ov; (m_c, l_c) of
@@ -657,6 +718,7 @@ struct ExtParams {
     uint16_t *O;             // [total_q][Hq][D]
     int64_t num_blocks, batch;
     int32_t total_q, max_blocks, Hq, Hkv, bs, max_len, max_q;
+    int32_t window, sinks;   // windowed form
     float scale;
     unsigned *status;
 };
@@ -671,7 +733,13 @@ __device__ __forceinline__ void turn_pass(int id) { asm volatile("bar.arrive %0,
 // tile that the bf16 form copies, so everything after the tile is shared. The
 // expansion is about 6 % of a chunk's time (1 x 4096 new over 8192 cached tokens,
 // 32 heads over 8: 2.09 ms, 197 TFLOP/s).
-template <int G, bool I4>
+//
+// WIN: the windowed form (bf16 cache). The CTA walks the chunks in which a token
+// of its tile sees something; rows mask what is out of their own window. V rows
+// that every token of the tile is blind to are zeros; in a chunk that is masked
+// for some token and holds a value that is not finite, p.V runs once a token over
+// V rows that are zero where that token is blind (0 * NaN would reach it).
+template <int G, bool I4, bool WIN>
 __global__ void __launch_bounds__(kExtThreads, 1)
 attn_extend_kernel(const ExtParams p) {
     constexpr int kRowBufs = I4 ? 4 : 3;               // chunks whose row offsets are held
@@ -705,7 +773,9 @@ attn_extend_kernel(const ExtParams p) {
     const int ntok = static_cast<int>(qlen - i0 < kTQ ? qlen - i0 : static_cast<int64_t>(kTQ));
     const int base = L - static_cast<int>(qlen);       // position of query token 0
     const int L_last = base + i0 + ntok;               // the last token's causal length
-    const int nchunks = (L_last + kChunk - 1) / kChunk;
+    const Seen w(WIN ? base + i0 + 1 - p.window : 0, WIN ? p.sinks : 0);   // of the tile's tokens together
+    const int nchunks = WIN ? w.chunks(L_last) : (L_last + kChunk - 1) / kChunk;
+    auto chunk_start = [&](int c) { return WIN ? w.start(c) : c * kChunk; };   // of the c-th chunk walked
 
     // q rows: row r = token r / G, head g*G + r % G (zero rows past the
     // tokens); 16-byte piece x of row r at piece x ^ (r % 8). Copied by
@@ -721,9 +791,9 @@ attn_extend_kernel(const ExtParams p) {
     auto chunk_rows = [&](int c) -> int {
         int bad = 0;
         if (tid < kChunk) {
-            const int j = c * kChunk + tid;
+            const int j = chunk_start(c) + tid;
             int64_t off = -1;
-            if (j < L_last) {
+            if (j < L_last && (!WIN || w.has(j))) {
                 const int64_t blk = p.table[b * p.max_blocks + j / p.bs];
                 if (blk >= 0 && blk < p.num_blocks) {
                     off = I4 ? ((blk * p.Hkv + g) * p.bs + j % p.bs) * 4 + i4_place(0, j % p.bs)   // row, segment 0's place
@@ -848,7 +918,7 @@ attn_extend_kernel(const ExtParams p) {
     const int len_b = rb / G < ntok ? base + i0 + rb / G + 1 : 0;
 
     for (int c = 0; c < nchunks; ++c) {
-        const int j0 = c * kChunk;
+        const int j0 = chunk_start(c);
         const int64_t *ro = rowoff + (c % kRowBufs) * kChunk;
         const uint8_t *Ks = KV + (2 * (c & 1)) * kTileBytes;
         const uint8_t *Vs = KV + (2 * (c & 1) + 1) * kTileBytes;
@@ -866,11 +936,32 @@ attn_extend_kernel(const ExtParams p) {
         } else {
             cp_async_wait<0>();
         }
-        __syncthreads();                               // everyone's
+        bool odd = false;                              // WIN: masked, with a value of V that is not finite
+        if (WIN) {
+            // masked for some token: the first one's length, or the last one's window
+            const bool masked = j0 + kChunk > base + i0 + 1 || (j0 < L_last - p.window && j0 + kChunk > p.sinks);
+            int bad_v = 0;
+            if (masked) {
+                for (int i = tid; i < kTileBytes / 16; i += kExtThreads) {   // the vectors that this thread copied
+                    uint32_t x[4];
+                    ld_shared_v4(smem_u32(Vs) + (i >> 4) * kRowBytes + (((i & 15) ^ ((i >> 4) & 7)) << 4), x[0], x[1], x[2], x[3]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        bad_v |= (x[k] & 0x7F80u) == 0x7F80u || (x[k] & 0x7F800000u) == 0x7F800000u;
+                }
+            }
+            odd = __syncthreads_or(bad_v) != 0;
+        } else {
+            __syncthreads();                           // everyone's
+        }
         if (I4 && c + 1 < nchunks) expand_chunk(c + 1);
 
         // tokens of this chunk each row sees (decode of the sequence cut after the row's token)
         const int na = max(0, min(kChunk, len_a - j0)), nb = max(0, min(kChunk, len_b - j0));
+        // WIN: of them, those before s0 or from fa (fb) on
+        const int s0 = WIN ? p.sinks - j0 : 0, fa = WIN ? len_a - p.window - j0 : 0, fb = WIN ? len_b - p.window - j0 : 0;
+        auto sees = [&](int h, int t) { return t < (h ? nb : na) && (!WIN || t < s0 || t >= (h ? fb : fa)); };
+        auto sees_any = [&](int h) { return (h ? nb : na) > 0 && (!WIN || s0 > 0 || (h ? fb : fa) < (h ? nb : na)); };
         // The two warp groups (warps 0-3, 4-7; warp w and w + 4 share a
         // scheduler) take turns on the tensor pipe: A's q.k, B's q.k, A's p.V,
         // B's p.V, ..., each group's softmax and merge running under the other
@@ -912,7 +1003,8 @@ attn_extend_kernel(const ExtParams p) {
         turn_pass(wg == 0 ? 2 : 1);
         // a chunk every row of the tile sees whole, with every block valid,
         // needs no masks
-        const bool whole = !bad && __all_sync(0xffffffffu, na == kChunk && nb == kChunk);
+        const bool whole = !bad && __all_sync(0xffffffffu, na == kChunk && nb == kChunk &&
+                                                           (!WIN || s0 >= kChunk || (fa <= 0 && fb <= 0)));
         float m[2] = {-INFINITY, -INFINITY};
         if (whole) {
 #pragma unroll
@@ -928,8 +1020,8 @@ attn_extend_kernel(const ExtParams p) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = nt * 8 + 2 * cq + (e & 1);
-                    s[nt][e] = t < (e < 2 ? na : nb) ? (ro[t] >= 0 ? __fmul_rn(s[nt][e], p.scale) : -INFINITY)
-                                                     : -INFINITY;
+                    s[nt][e] = sees(e >> 1, t) ? (ro[t] >= 0 ? __fmul_rn(s[nt][e], p.scale) : -INFINITY)
+                                               : -INFINITY;
                     m[e >> 1] = fmaxf(m[e >> 1], s[nt][e]);
                 }
         }
@@ -941,6 +1033,22 @@ attn_extend_kernel(const ExtParams p) {
                             : in[3] ? __ffs(in[3]) + 95 : kChunk;
             m[0] = fmaxf(m[0], first < na ? -INFINITY : kNoScore);
             m[1] = fmaxf(m[1], first < nb ? -INFINITY : kNoScore);
+        }
+        if (WIN && bad) {                              // the same, where a row's tokens need not be the first ones
+            int any[2] = {0, 0};
+#pragma unroll
+            for (int nt = 0; nt < kChunk / 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = nt * 8 + 2 * cq + (e & 1);
+                    any[e >> 1] |= sees(e >> 1, t) && ro[t] >= 0;
+                }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                any[h] |= __shfl_xor_sync(0xffffffffu, any[h], 1);
+                any[h] |= __shfl_xor_sync(0xffffffffu, any[h], 2);
+                if (!any[h]) m[h] = kNoScore;
+            }
         }
         // per row: max (any order gives the same value), then e^(s - m) for the
         // tokens it sees (0 past them)
@@ -960,7 +1068,7 @@ attn_extend_kernel(const ExtParams p) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = nt * 8 + 2 * cq + (e & 1);
-                    s[nt][e] = t < (e < 2 ? na : nb) ? expf(s[nt][e] - m[e >> 1]) : 0.0f;
+                    s[nt][e] = sees(e >> 1, t) ? expf(s[nt][e] - m[e >> 1]) : 0.0f;
                 }
         }
         // per row: the sum in decode's order. Lane L of decode sums tokens
@@ -993,6 +1101,19 @@ attn_extend_kernel(const ExtParams p) {
             l[h] = x[0] + x[1];                                           // step 1
         }
 
+        for (int pass = 0; pass < (WIN && odd ? ntok : 1); ++pass) {
+        if (WIN && odd) {                              // V as this token may see it
+            const int n = base + i0 + pass + 1 - j0, f = n - p.window;
+            __syncthreads();                           // the pass before has been computed (all read V)
+            for (int i = tid; i < kTileBytes / 16; i += kExtThreads) {
+                const int t = i >> 4, x = i & 15;
+                const bool in = ro[t] >= 0 && t < n && (t < s0 || t >= f);
+                cp_async_16(smem_u32(Vs) + t * kRowBytes + ((x ^ (t & 7)) << 4), in ? p.V + ro[t] + x * 8 : p.V, in ? 16u : 0u);
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+            __syncthreads();
+        }
         turn_wait(wg == 0 ? 1 : 2);
         // values: O_c = sum_t p_t v_t for all 128 dimensions, p = hi + lo
         // (two bf16 MMAs per step), tokens ascending in 16-token steps; the
@@ -1040,7 +1161,7 @@ attn_extend_kernel(const ExtParams p) {
         // merge this chunk into the rows' running state, in chunk order
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if ((h ? nb : na) == 0) continue;
+            if (!sees_any(h) || (WIN && odd && (h ? rb : ra) / G != pass)) continue;
             float mn, al, be;
             merge_factors(m_run[h], m[h], mn, al, be);
             m_run[h] = mn;
@@ -1050,6 +1171,7 @@ attn_extend_kernel(const ExtParams p) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                     o_run[nt][2 * h + e] = merge_value(o_run[nt][2 * h + e], acc[nt][2 * h + e], al, be);
+        }
         }
     }
 
@@ -1073,9 +1195,19 @@ attn_extend_kernel(const ExtParams p) {
 
 }  // namespace
 
-int64_t attention_decode_workspace_bytes(int64_t B, int32_t Hq, int32_t max_len) {
+namespace {
+// The most chunks in which a token of at most max_len sees something.
+int64_t seen_chunks(int32_t max_len, int32_t window, int32_t sinks) {
+    const int64_t all = (static_cast<int64_t>(max_len) + kChunk - 1) / kChunk;
+    if (window == 0) return all;                     // no window
+    const int64_t some = (static_cast<int64_t>(window) + kChunk - 2) / kChunk + 1 + (static_cast<int64_t>(sinks) + kChunk - 1) / kChunk;
+    return some < all ? some : all;
+}
+}  // namespace
+
+int64_t attention_decode_workspace_bytes(int64_t B, int32_t Hq, int32_t max_len, int32_t window, int32_t sinks) {
     if (B < 0 || Hq < 1 || max_len < 1) return -1;
-    const int64_t chunks = (static_cast<int64_t>(max_len) + kChunk - 1) / kChunk;
+    const int64_t chunks = seen_chunks(max_len, window, sinks);
     constexpr int64_t kRecord = (kD + 2) * static_cast<int64_t>(sizeof(float));   // (m, l, o) of one head and chunk
     // -1 when the size does not fit in an int64_t
     const int64_t records_max = INT64_MAX / kRecord;
@@ -1083,33 +1215,39 @@ int64_t attention_decode_workspace_bytes(int64_t B, int32_t Hq, int32_t max_len)
     return B * Hq * chunks * kRecord;
 }
 
-template <int G, int SLOTS, int NG>
+template <int G, int SLOTS, int NG, bool WIN>
 bi_status launch_split_shape(const dim3 &grid, const CUtensorMap &tmK, const CUtensorMap &tmV, const AttnParams &p,
                              cudaStream_t s) {
     static unsigned long long configured = 0;
     constexpr int smem = dec_smem<SLOTS, NG>();
-    if (ensure_smem_attr(reinterpret_cast<const void *>(attn_split_kernel<G, SLOTS, NG>), smem, &configured) != BI_OK)
+    if (ensure_smem_attr(reinterpret_cast<const void *>(attn_split_kernel<G, SLOTS, NG, WIN>), smem, &configured) != BI_OK)
         return BI_ERR_CUDA;
-    return launch_pdl(attn_split_kernel<G, SLOTS, NG>, grid, dim3(dec_threads<SLOTS>()), smem, s, tmK, tmV, p);
+    return launch_pdl(attn_split_kernel<G, SLOTS, NG, WIN>, grid, dim3(dec_threads<SLOTS>()), smem, s, tmK, tmV, p);
 }
 // At most two items per SM: one item per CTA, two CTAs per SM; else the ring.
-template <int G>
+template <int G, bool WIN>
 bi_status launch_split(int64_t items, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, const AttnParams &p,
                        cudaStream_t s) {
     if (items <= 2 * static_cast<int64_t>(sms))
-        return launch_split_shape<G, 1, 1>(dim3(static_cast<unsigned>(items)), tmK, tmV, p, s);
-    return launch_split_shape<G, 3, 2>(dim3(static_cast<unsigned>(sms)), tmK, tmV, p, s);
+        return launch_split_shape<G, 1, 1, WIN>(dim3(static_cast<unsigned>(items)), tmK, tmV, p, s);
+    return launch_split_shape<G, 3, 2, WIN>(dim3(static_cast<unsigned>(sms)), tmK, tmV, p, s);
 }
-#define SPLIT_LAUNCH(G)                                              \
-    do {                                                             \
-        const bi_status st_ = launch_split<G>(items, info->sm_count, tmK, tmV, p, s); \
-        if (st_ != BI_OK) return st_;                                \
-    } while (0)
+template <bool WIN>
+bi_status launch_split_win(int G, int64_t items, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                           const AttnParams &p, cudaStream_t s) {
+    switch (G) {
+        case 1: return launch_split<1, WIN>(items, sms, tmK, tmV, p, s);
+        case 2: return launch_split<2, WIN>(items, sms, tmK, tmV, p, s);
+        case 4: return launch_split<4, WIN>(items, sms, tmK, tmV, p, s);
+        case 8: return launch_split<8, WIN>(items, sms, tmK, tmV, p, s);
+        default: return BI_ERR_UNSUPPORTED;
+    }
+}
 
 bi_status launch_attention_decode(const void *Q, const void *K, const void *V, const int32_t *table,
                                   int32_t max_blocks, int64_t num_blocks, const int32_t *lens, int64_t B, int32_t Hq,
-                                  int32_t Hkv, int32_t D, int32_t bs, int32_t max_len, float scale, void *workspace,
-                                  void *O, cudaStream_t s) {
+                                  int32_t Hkv, int32_t D, int32_t bs, int32_t max_len, float scale, int32_t window,
+                                  int32_t sinks, void *workspace, void *O, cudaStream_t s) {
     (void)D;
     AttnParams p{};
     p.Q = static_cast<const uint16_t *>(Q);
@@ -1125,8 +1263,10 @@ bi_status launch_attention_decode(const void *Q, const void *K, const void *V, c
     p.Hq = Hq;
     p.Hkv = Hkv;
     p.bs = bs;
-    p.chunks = static_cast<int32_t>((static_cast<int64_t>(max_len) + kChunk - 1) / kChunk);
+    p.chunks = static_cast<int32_t>(seen_chunks(max_len, window, sinks));
     p.max_len = max_len;
+    p.window = window;
+    p.sinks = sinks;
     p.scale = scale;
     p.status = device_status_word();
     const int G = Hq / Hkv;
@@ -1149,32 +1289,32 @@ bi_status launch_attention_decode(const void *Q, const void *K, const void *V, c
                          CU_TENSOR_MAP_SWIZZLE_128B) != BI_OK)
             p.box_rows = 0;                          // the per-row copies need no tensor map
     }
-    switch (G) {
-        case 1: SPLIT_LAUNCH(1); break;
-        case 2: SPLIT_LAUNCH(2); break;
-        case 4: SPLIT_LAUNCH(4); break;
-        case 8: SPLIT_LAUNCH(8); break;
-        default: return BI_ERR_UNSUPPORTED;
-    }
-    return launch_pdl(attn_combine_kernel, dim3(Hq, static_cast<unsigned>(B)), dim3(kCombineThreads), 0, s, p);
+    const bool win = window > 0;
+    const bi_status st = win ? launch_split_win<true>(G, items, info->sm_count, tmK, tmV, p, s)
+                             : launch_split_win<false>(G, items, info->sm_count, tmK, tmV, p, s);
+    if (st != BI_OK) return st;
+    return launch_pdl(win ? attn_combine_kernel<true> : attn_combine_kernel<false>, dim3(Hq, static_cast<unsigned>(B)),
+                      dim3(kCombineThreads), 0, s, p);
 }
 
-template <int G, bool I4>
+template <int G, bool I4, bool WIN>
 bi_status launch_extend_g(const dim3 &grid, const ExtParams &p, cudaStream_t s) {
     static unsigned long long configured = 0;
     constexpr int smem = I4 ? kExtSmemI4 : kExtSmem;
-    if (ensure_smem_attr(reinterpret_cast<const void *>(attn_extend_kernel<G, I4>), smem, &configured) != BI_OK)
+    if (ensure_smem_attr(reinterpret_cast<const void *>(attn_extend_kernel<G, I4, WIN>), smem, &configured) != BI_OK)
         return BI_ERR_CUDA;
-    return launch_pdl(attn_extend_kernel<G, I4>, grid, dim3(kExtThreads), smem, s, p);
+    return launch_pdl(attn_extend_kernel<G, I4, WIN>, grid, dim3(kExtThreads), smem, s, p);
 }
 
 // K and V (bf16 cache) or c (4-bit cache)
-template <bool I4>
+template <bool I4, bool WIN>
 bi_status launch_extend(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K, const void *V,
                         const KvInt4 &c, const int32_t *table, int32_t max_blocks, int64_t num_blocks,
                         const int32_t *lens, int64_t B, int32_t Hq, int32_t Hkv, int32_t bs, int32_t max_len,
-                        int32_t max_q, float scale, void *O, cudaStream_t s) {
+                        int32_t max_q, float scale, int32_t window, int32_t sinks, void *O, cudaStream_t s) {
     ExtParams p{};
+    p.window = window;
+    p.sinks = sinks;
     p.Q = static_cast<const uint16_t *>(Q);
     p.cu_q = cu_q;
     p.K = static_cast<const uint16_t *>(K);
@@ -1200,10 +1340,10 @@ bi_status launch_extend(const void *Q, const int32_t *cu_q, int32_t total_q, con
     if (ctas_x > 0x7fffffff) return BI_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(ctas_x));
     switch (G) {
-        case 1: return launch_extend_g<1, I4>(grid, p, s);
-        case 2: return launch_extend_g<2, I4>(grid, p, s);
-        case 4: return launch_extend_g<4, I4>(grid, p, s);
-        case 8: return launch_extend_g<8, I4>(grid, p, s);
+        case 1: return launch_extend_g<1, I4, WIN>(grid, p, s);
+        case 2: return launch_extend_g<2, I4, WIN>(grid, p, s);
+        case 4: return launch_extend_g<4, I4, WIN>(grid, p, s);
+        case 8: return launch_extend_g<8, I4, WIN>(grid, p, s);
         default: return BI_ERR_UNSUPPORTED;
     }
 }
@@ -1211,16 +1351,18 @@ bi_status launch_extend(const void *Q, const int32_t *cu_q, int32_t total_q, con
 bi_status launch_attention_extend(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K, const void *V,
                                   const int32_t *table, int32_t max_blocks, int64_t num_blocks, const int32_t *lens,
                                   int64_t B, int32_t Hq, int32_t Hkv, int32_t bs, int32_t max_len, int32_t max_q,
-                                  float scale, void *O, cudaStream_t s) {
-    return launch_extend<false>(Q, cu_q, total_q, K, V, KvInt4{}, table, max_blocks, num_blocks, lens, B, Hq, Hkv, bs,
-                                max_len, max_q, scale, O, s);
+                                  float scale, int32_t window, int32_t sinks, void *O, cudaStream_t s) {
+    return window > 0 ? launch_extend<false, true>(Q, cu_q, total_q, K, V, KvInt4{}, table, max_blocks, num_blocks, lens, B,
+                                                   Hq, Hkv, bs, max_len, max_q, scale, window, sinks, O, s)
+                      : launch_extend<false, false>(Q, cu_q, total_q, K, V, KvInt4{}, table, max_blocks, num_blocks, lens, B,
+                                                    Hq, Hkv, bs, max_len, max_q, scale, 0, 0, O, s);
 }
 
 bi_status launch_attention_extend_int4(const void *Q, const int32_t *cu_q, int32_t total_q, const KvInt4 &c,
                                        const int32_t *table, int32_t max_blocks, const int32_t *lens, int64_t B,
                                        int32_t Hq, int32_t max_len, int32_t max_q, float scale, void *O, cudaStream_t s) {
-    return launch_extend<true>(Q, cu_q, total_q, nullptr, nullptr, c, table, max_blocks, c.num_blocks, lens, B, Hq, c.Hkv,
-                               c.bs, max_len, max_q, scale, O, s);
+    return launch_extend<true, false>(Q, cu_q, total_q, nullptr, nullptr, c, table, max_blocks, c.num_blocks, lens, B, Hq,
+                                      c.Hkv, c.bs, max_len, max_q, scale, 0, 0, O, s);
 }
 
 }  // namespace bi
@@ -1300,6 +1442,6 @@ extern "C" bi_status bi_attention_decode_noalloc(const void *Q, const void *K_ca
     st = noalloc_scratch(&scratch);
     if (st != BI_OK) return st;
     return launch_attention_decode(Q, K_cache, V_cache, block_table, max_blocks_per_seq, num_blocks, seq_lens, B, Hq,
-                                   Hkv, head_dim, block_size, max_seq_len, scale, scratch, O,
+                                   Hkv, head_dim, block_size, max_seq_len, scale, 0, 0, scratch, O,
                                    static_cast<cudaStream_t>(stream));
 }

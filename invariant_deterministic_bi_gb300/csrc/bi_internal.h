@@ -81,6 +81,25 @@ struct KvInt4 {
     int32_t Hkv, bs;
 };
 
+// Heads of T tokens for the row kernel of rope.cu: token t's [heads][D] at src + t * lds, the result at dst + t * ldd,
+// or (cache) at dst + slots[t] * ldd.
+struct Heads {
+    const uint16_t *src;
+    uint16_t *dst;
+    const uint16_t *w;       // [D] norm weights, or null
+    int64_t lds, ldd;
+    int32_t heads, cache;
+};
+struct HeadsParams {
+    Heads part[3];           // queries, keys (both normed and turned), values (copied)
+    const int64_t *pos, *slots;
+    const uint64_t *turns;   // [R / 2] turns per position, in units of 2^-64
+    int64_t T, cache_rows;   // (without slots: one row)
+    float factor, eps, inv_d;
+    int32_t D, R, splits, groups, first[3];   // splits: warps a token; groups of heads, each part's first
+    unsigned *status;
+};
+
 // Kernel launchers (defined in the .cu files); arguments already validated.
 bi_status launch_gemm_bf16(const void *X, int64_t ldx, const void *W, int64_t ldw, void *Y, int64_t ldy,
                            int64_t M, int64_t N, int64_t K, cudaStream_t s);
@@ -108,15 +127,16 @@ bi_status launch_rmsnorm(const void *x, void *residual, const void *w, void *out
                          float eps, cudaStream_t s);
 bi_status launch_rank_sum_rmsnorm(const void *const *parts, int32_t R, void *residual, const void *w, void *sum_out,
                                   void *out, int64_t M, int64_t H, float eps, cudaStream_t s);
-int64_t attention_decode_workspace_bytes(int64_t B, int32_t Hq, int32_t max_len);
+// window 0: none (a token sees every token up to itself)
+int64_t attention_decode_workspace_bytes(int64_t B, int32_t Hq, int32_t max_len, int32_t window = 0, int32_t sinks = 0);
 bi_status launch_attention_decode(const void *Q, const void *K, const void *V, const int32_t *table,
                                   int32_t max_blocks, int64_t num_blocks, const int32_t *lens, int64_t B, int32_t Hq,
-                                  int32_t Hkv, int32_t D, int32_t bs, int32_t max_len, float scale, void *workspace,
-                                  void *O, cudaStream_t s);
+                                  int32_t Hkv, int32_t D, int32_t bs, int32_t max_len, float scale, int32_t window,
+                                  int32_t sinks, void *workspace, void *O, cudaStream_t s);
 bi_status launch_attention_extend(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K, const void *V,
                                   const int32_t *table, int32_t max_blocks, int64_t num_blocks, const int32_t *lens,
                                   int64_t B, int32_t Hq, int32_t Hkv, int32_t bs, int32_t max_len, int32_t max_q,
-                                  float scale, void *O, cudaStream_t s);
+                                  float scale, int32_t window, int32_t sinks, void *O, cudaStream_t s);
 bi_status launch_kv_int4_append(const KvInt4 &c, const int64_t *slots, const void *K, int64_t ldk, const void *V,
                                 int64_t ldv, int64_t T, cudaStream_t s);
 bi_status launch_kv_int4_read(const KvInt4 &c, const int64_t *slots, void *K, int64_t ldk, void *V, int64_t ldv,
@@ -133,6 +153,7 @@ bi_status launch_attention_extend_int4_few(const void *Q, const int32_t *cu_q, i
                                            void *O, cudaStream_t s);
 // Bytes the split over chunks wants for these sizes; 0: the tiled kernel is used and wants none; -1: past int64_t.
 int64_t attention_extend_int4_workspace_bytes(int64_t total_q, int32_t Hq, int32_t Hkv, int32_t max_len, int32_t max_q);
+bi_status launch_heads(HeadsParams p, bool interleaved, cudaStream_t s);
 bi_status launch_gemm_int4(const void *X, int64_t ldx, const uint8_t *W, const void *scales, const uint8_t *zeros, void *Y,
                            int64_t ldy, int64_t M, int64_t N, int64_t K, int64_t group, cudaStream_t s);
 bi_status launch_bounds_check(int32_t index, int32_t limit, cudaStream_t s);
