@@ -688,7 +688,7 @@ class _Rope(ctypes.Structure):
 class RopeFreqs:
     """The frequencies of a rotation (made by ``rope_freqs``): turns int64 [rotary_dim / 2] on the GPU, turns per
     position in units of 2^-64, and how they are used."""
-    __slots__ = ("turns", "rotary_dim", "interleaved", "factor", "_c")
+    __slots__ = ("turns", "rotary_dim", "interleaved", "factor", "_ref")
 
     def __init__(self, turns, rotary_dim: int, interleaved: bool = False, factor: float = 1.0):
         import torch
@@ -697,7 +697,7 @@ class RopeFreqs:
             raise ValueError(f"turns must be [rotary_dim / 2] = [{rotary_dim / 2:g}], got {tuple(turns.shape)}")
         for n, v in (("turns", turns), ("rotary_dim", int(rotary_dim)), ("interleaved", bool(interleaved)), ("factor", float(factor))):
             object.__setattr__(self, n, v)
-        object.__setattr__(self, "_c", _Rope(turns.data_ptr(), self.rotary_dim, self.interleaved, self.factor))
+        object.__setattr__(self, "_ref", ctypes.byref(_Rope(turns.data_ptr(), self.rotary_dim, self.interleaved, self.factor)))
 
     def __setattr__(self, name, value):
         raise AttributeError("a RopeFreqs is fixed; make a new one")
@@ -731,57 +731,84 @@ def rope_freqs(rotary_dim: int, base: float = 10000.0, interleaved: bool = False
     return RopeFreqs(turns.to(device), rotary_dim, interleaved, m.value if factor is None else factor)
 
 
-def _heads(t, name, T=None, D=None):
-    """(T, heads, D, token stride) of bf16 heads [T, H, D] that are contiguous within a token."""
+# A call's checks are a good part of its time where it is short, so each of the following looks at a tensor once and
+# leaves the wording of what is wrong to _refuse.
+def _current_device() -> int:
     import torch
-    _typed(t, torch.bfloat16, name, contiguous=False)
-    shape = t.shape
-    if len(shape) != 3 or (T is not None and (shape[0] != T or shape[2] != D)):
-        raise ValueError(f"{name} must be [T, heads, head_dim]" + ("" if T is None else f" with T = {T}, head_dim = {D}") +
-                         f", got {tuple(shape)}")
-    T, H, D = shape
-    st = t.stride()
-    if T * H and ((D > 1 and st[2] != 1) or (H > 1 and st[1] != D)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous (a token stride is allowed)")
-    return T, H, D, st[0] if T > 1 else H * D
+    get = getattr(torch._C, "_cuda_getDevice", None)
+    return get() if get is not None else torch.cuda.current_device()
 
 
-def _rope_args(positions, freqs, T):
-    """(pointers of positions and rotation, tensors to check) -- both or neither given."""
+def _refuse(t, dtype, name, cur, what):
+    """Raises what is wrong with a tensor that should be contiguous, of this type and on this device, else ValueError(what)."""
+    _typed(t, dtype, name, contiguous=False)
+    if t.get_device() != cur:
+        raise ValueError(f"tensors must be on the current device cuda:{cur}, {name} is on {t.device}")
+    raise ValueError(f"{name} must be {what}, got {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _tensor(t, dtype, shape, name, cur):
+    """Checks a contiguous tensor of this type, device and shape (None: any)."""
+    try:
+        if t.dtype is dtype and t.get_device() == cur and t.is_contiguous() and (shape is None or t.shape == shape):
+            return
+    except AttributeError:
+        pass                                             # not a tensor
+    _refuse(t, dtype, name, cur, "contiguous" + (f" {tuple(shape)}" if shape is not None else ""))
+
+
+def _heads(t, name, cur, T=-1, D=-1, H=-1):
+    """(T, heads, D, token stride) of bf16 heads [T, H, D] that are contiguous within a token (-1: any size)."""
+    import torch
+    try:
+        (t_, h, d), (st, sh, sd) = t.shape, t.stride()
+        if (t.dtype is torch.bfloat16 and t.get_device() == cur and (T < 0 or (t_ == T and d == D)) and (H < 0 or h == H) and
+                ((sd == 1 and (sh == d or h == 1)) or not t_ * h)):
+            return t_, h, d, st if t_ > 1 else h * d
+    except (AttributeError, TypeError, ValueError):
+        pass                                             # not a tensor, or not of three dimensions
+    sizes = ", ".join(n if v < 0 else str(v) for n, v in (("T", T), ("heads", H), ("head_dim", D)))
+    _refuse(t, torch.bfloat16, name, cur, f"[{sizes}], the heads of a token contiguous (a token stride is allowed)")
+
+
+def _rope_args(positions, freqs, T, cur):
+    """Pointers of the positions and the rotation, both or neither given."""
     import torch
     if freqs is None:
         if positions is not None:
             raise ValueError("positions without freqs")
-        return None, None, ()
+        return None, None
     if not isinstance(freqs, RopeFreqs):
         raise TypeError("freqs must be a RopeFreqs")
-    if _typed(positions, torch.int64, "positions").shape != (T,):
-        raise ValueError(f"positions must be [T] = [{T}], got {tuple(positions.shape)}")
-    return positions.data_ptr(), ctypes.byref(freqs._c), (positions, freqs.turns)
+    _tensor(positions, torch.int64, (T,), "positions", cur)
+    if freqs.turns.get_device() != cur:
+        raise ValueError(f"freqs must be on the current device cuda:{cur}, they are on {freqs.turns.device}")
+    return positions.data_ptr(), freqs._ref
 
 
-def _weight(w, D, name):
+def _out(like, stream):
+    """A new tensor of a checked tensor's shape and type, contiguous, for a call on `stream`."""
     import torch
-    if _typed(w, torch.bfloat16, name).shape != (D,):
-        raise ValueError(f"{name} must be [head_dim] = [{D}], got {tuple(w.shape)}")
-    return w
+    return torch.empty_like(like) if stream is None else _new(like.shape, like.dtype, like, stream)
 
 
 def rope(X, positions, freqs: RopeFreqs, Y=None, stream=None):
     """Rotary positions: Y[t, h] = X[t, h] turned by positions[t].
 
     X bf16 [T, H, head_dim] (a token stride is allowed); positions int64 [T]. Y may be X (in place)."""
-    import torch
-    T, H, D, ldx = _heads(X, "X")
+    cur = _current_device()
+    T, H, D, ldx = _heads(X, "X", cur)
     if freqs is None:
         raise TypeError("freqs must be a RopeFreqs")
-    pos, c, used = _rope_args(positions, freqs, T)
-    if Y is not None and _heads(Y, "Y", T, D)[1] != H:
-        raise ValueError("Y must have X's shape")
-    raw, _ = _launch_on(None, (X, Y, *used), stream)
+    pos, c = _rope_args(positions, freqs, T, cur)
     if Y is None:
-        Y = _new((T, H, D), torch.bfloat16, X, stream)
-    _check(load().bi_rope(X.data_ptr(), ldx, pos, T, H, D, c, Y.data_ptr(), _heads(Y, "Y")[3], raw), "bi_rope")
+        Y, ldy = _out(X, stream), H * D
+    else:
+        ldy = _heads(Y, "Y", cur, T, D, H)[3]
+    raw = _current_raw_stream(cur) if stream is None else stream.cuda_stream
+    st = load().bi_rope(X.data_ptr(), ldx, pos, T, H, D, c, Y.data_ptr(), ldy, raw)
+    if st:
+        raise BiError(st, "bi_rope")
     return Y
 
 
@@ -791,21 +818,25 @@ def qk_norm_rope(Q, K, q_weight, k_weight, eps: float, positions=None, freqs=Non
     Q bf16 [T, Hq, head_dim], K [T, Hkv, head_dim] (token strides allowed); weights bf16 [head_dim];
     positions int64 [T]; freqs None: the norms alone. Q_out may be Q and K_out K (in place)."""
     import torch
-    T, Hq, D, ldq = _heads(Q, "Q")
-    _, Hkv, _, ldk = _heads(K, "K", T, D)
-    _weight(q_weight, D, "q_weight"), _weight(k_weight, D, "k_weight")
-    pos, c, used = _rope_args(positions, freqs, T)
-    for t, H, n in ((Q_out, Hq, "Q_out"), (K_out, Hkv, "K_out")):
-        if t is not None and _heads(t, n, T, D)[1] != H:
-            raise ValueError(f"{n} must be {(T, H, D)}, got {tuple(t.shape)}")
-    raw, _ = _launch_on(None, (Q, K, q_weight, k_weight, Q_out, K_out, *used), stream)
+    cur = _current_device()
+    T, Hq, D, ldq = _heads(Q, "Q", cur)
+    _, Hkv, _, ldk = _heads(K, "K", cur, T, D)
+    _tensor(q_weight, torch.bfloat16, (D,), "q_weight", cur)
+    _tensor(k_weight, torch.bfloat16, (D,), "k_weight", cur)
+    pos, c = _rope_args(positions, freqs, T, cur)
     if Q_out is None:
-        Q_out = _new((T, Hq, D), torch.bfloat16, Q, stream)
+        Q_out, ldqo = _out(Q, stream), Hq * D
+    else:
+        ldqo = _heads(Q_out, "Q_out", cur, T, D, Hq)[3]
     if K_out is None:
-        K_out = _new((T, Hkv, D), torch.bfloat16, K, stream)
-    _check(load().bi_qk_norm_rope(Q.data_ptr(), ldq, K.data_ptr(), ldk, q_weight.data_ptr(), k_weight.data_ptr(), float(eps),
-                                  pos, T, Hq, Hkv, D, c, Q_out.data_ptr(), _heads(Q_out, "Q_out")[3], K_out.data_ptr(),
-                                  _heads(K_out, "K_out")[3], raw), "bi_qk_norm_rope")
+        K_out, ldko = _out(K, stream), Hkv * D
+    else:
+        ldko = _heads(K_out, "K_out", cur, T, D, Hkv)[3]
+    raw = _current_raw_stream(cur) if stream is None else stream.cuda_stream
+    st = load().bi_qk_norm_rope(Q.data_ptr(), ldq, K.data_ptr(), ldk, q_weight.data_ptr(), k_weight.data_ptr(), eps, pos, T,
+                                Hq, Hkv, D, c, Q_out.data_ptr(), ldqo, K_out.data_ptr(), ldko, raw)
+    if st:
+        raise BiError(st, "bi_qk_norm_rope")
     return Q_out, K_out
 
 
@@ -818,48 +849,65 @@ def kv_append(K, V, slots, K_cache, V_cache, positions=None, freqs=None, k_weigh
     slots int64 [T]: block * block_size + offset, -1 to store nothing for a token (its query is computed all the
     same). The slots of one call must differ. K_cache, V_cache bf16 [blocks, block_size, Hkv, head_dim]. Q_out may be Q."""
     import torch
-    T, Hkv, D, ldk = _heads(K, "K")
-    _, Hv, _, ldv = _heads(V, "V", T, D)
-    if Hv != Hkv or _slots(slots) != T:
-        raise ValueError(f"shape mismatch K{tuple(K.shape)} V{tuple(V.shape)} slots{tuple(slots.shape)}")
-    shape = _typed(K_cache, torch.bfloat16, "K_cache").shape
-    if len(shape) != 4 or tuple(shape[2:]) != (Hkv, D) or _typed(V_cache, torch.bfloat16, "V_cache").shape != shape:
-        raise ValueError(f"K_cache and V_cache must be [blocks, block_size, {Hkv}, {D}], got {tuple(shape)} and {tuple(V_cache.shape)}")
+    cur = _current_device()
+    T, Hkv, D, ldk = _heads(K, "K", cur)
+    ldv = _heads(V, "V", cur, T, D, Hkv)[3]
+    _tensor(slots, torch.int64, (T,), "slots", cur)
+    _tensor(K_cache, torch.bfloat16, None, "K_cache", cur)
+    shape = K_cache.shape
+    if len(shape) != 4 or shape[2] != Hkv or shape[3] != D:
+        raise ValueError(f"K_cache must be [blocks, block_size, {Hkv}, {D}], got {tuple(shape)}")
+    _tensor(V_cache, torch.bfloat16, shape, "V_cache", cur)
     if k_weight is not None:
-        _weight(k_weight, D, "k_weight")
-    pos, c, used = _rope_args(positions, freqs, T)
-    Hq = ldq = 0
+        _tensor(k_weight, torch.bfloat16, (D,), "k_weight", cur)
+    pos, c = _rope_args(positions, freqs, T, cur)
     if Q is not None:
-        _, Hq, _, ldq = _heads(Q, "Q", T, D)
+        _, Hq, _, ldq = _heads(Q, "Q", cur, T, D)
         if q_weight is not None:
-            _weight(q_weight, D, "q_weight")
-        if Q_out is not None and _heads(Q_out, "Q_out", T, D)[1] != Hq:
-            raise ValueError(f"Q_out must be {(T, Hq, D)}, got {tuple(Q_out.shape)}")
+            _tensor(q_weight, torch.bfloat16, (D,), "q_weight", cur)
+        if Q_out is None:
+            Q_out, ldqo = _out(Q, stream), Hq * D
+        else:
+            ldqo = _heads(Q_out, "Q_out", cur, T, D, Hq)[3]
+        queries = Q.data_ptr(), ldq, None if q_weight is None else q_weight.data_ptr(), Hq, Q_out.data_ptr(), ldqo
     elif q_weight is not None or Q_out is not None:
         raise ValueError("q_weight and Q_out belong to Q")
-    raw, _ = _launch_on(None, (K, V, slots, K_cache, V_cache, k_weight, Q, q_weight, Q_out, *used), stream)
-    if Q is not None and Q_out is None:
-        Q_out = _new((T, Hq, D), torch.bfloat16, Q, stream)
-    ptr = lambda t: None if t is None else t.data_ptr()
-    _check(load().bi_kv_append(K.data_ptr(), ldk, V.data_ptr(), ldv, T, slots.data_ptr(), ptr(k_weight), float(eps), pos, c,
-                               K_cache.data_ptr(), V_cache.data_ptr(), shape[0], Hkv, D, shape[1], ptr(Q), ldq, ptr(q_weight), Hq,
-                               ptr(Q_out), 0 if Q_out is None else _heads(Q_out, "Q_out")[3], raw), "bi_kv_append")
+    else:
+        queries = None, 0, None, 0, None, 0
+    raw = _current_raw_stream(cur) if stream is None else stream.cuda_stream
+    st = load().bi_kv_append(K.data_ptr(), ldk, V.data_ptr(), ldv, T, slots.data_ptr(),
+                             None if k_weight is None else k_weight.data_ptr(), eps, pos, c, K_cache.data_ptr(),
+                             V_cache.data_ptr(), shape[0], Hkv, D, shape[1], *queries, raw)
+    if st:
+        raise BiError(st, "bi_kv_append")
     return Q_out
 
 
-def _attention_window_args(Q, K_cache, V_cache, block_table, seq_lens, workspace, O):
-    """Checks shared by the windowed calls: Q's and the cache's shapes."""
+def _attention_window_args(Q, K_cache, V_cache, block_table, seq_lens, workspace, O, cur):
+    """Checks shared by the windowed calls: Q's and the cache's shapes, the rows of the table."""
     import torch
-    shape = _attention_int4_args(Q, block_table, seq_lens, workspace, O)
-    cache = _typed(K_cache, torch.bfloat16, "K_cache").shape
-    if len(cache) != 4 or cache[3] != 128 or _typed(V_cache, torch.bfloat16, "V_cache").shape != cache:
-        raise ValueError(f"K_cache and V_cache must be [blocks, block_size, Hkv, 128], got {tuple(cache)} and {tuple(V_cache.shape)}")
-    return shape, cache
+    _tensor(Q, torch.bfloat16, None, "Q", cur)
+    _tensor(K_cache, torch.bfloat16, None, "K_cache", cur)
+    _tensor(block_table, torch.int32, None, "block_table", cur)
+    shape, cache, table = Q.shape, K_cache.shape, block_table.shape
+    if len(shape) != 3 or shape[2] != 128 or len(cache) != 4 or cache[3] != 128 or len(table) != 2:
+        raise ValueError(f"Q must be [tokens, Hq, 128], K_cache [blocks, block_size, Hkv, 128], block_table [B, max_blocks]; got "
+                         f"{tuple(shape)}, {tuple(cache)}, {tuple(table)}")
+    _tensor(V_cache, torch.bfloat16, cache, "V_cache", cur)
+    _tensor(seq_lens, torch.int32, (table[0],), "seq_lens", cur)
+    if workspace is not None:
+        _tensor(workspace, torch.uint8, None, "workspace", cur)
+    if O is not None:
+        _tensor(O, torch.bfloat16, shape, "O", cur)
+    return shape, cache, table
 
 
 def _window(window, sinks):
     """Both as 32-bit numbers: anything past the longest sequence counts as that, anything below 0 is refused by the call."""
-    return tuple(max(-1, min(operator.index(x), 1 << 30)) for x in (window, sinks))
+    window, sinks = operator.index(window), operator.index(sinks)
+    if 0 < window <= 1 << 30 and 0 <= sinks <= 1 << 30:
+        return window, sinks
+    return max(-1, min(window, 1 << 30)), max(-1, min(sinks, 1 << 30))
 
 
 def attention_decode_window_workspace_size(B: int, Hq: int, max_seq_len: int, window: int, sinks: int = 0) -> int:
@@ -874,19 +922,21 @@ def attention_decode_window(Q, K_cache, V_cache, block_table, seq_lens, max_seq_
     Table entries of blocks out of sight may be anything (-1 once given back). The workspace (uint8,
     ``attention_decode_window_workspace_size`` bytes) is allocated with torch if not given."""
     import torch
-    (B, Hq, D), (nblk, bs, Hkv, _) = _attention_window_args(Q, K_cache, V_cache, block_table, seq_lens, workspace, O)
-    if seq_lens.shape != (B,):
-        raise ValueError("one query token a sequence: seq_lens must be [B], B the rows of Q")
+    cur = _current_device()
+    (B, Hq, D), (nblk, bs, Hkv, _), table = _attention_window_args(Q, K_cache, V_cache, block_table, seq_lens, workspace, O, cur)
+    if table[0] != B:
+        raise ValueError("one query token a sequence: block_table must be [B, max_blocks], B the rows of Q")
     window, sinks = _window(window, sinks)
-    raw, _ = _launch_on(None, (Q, K_cache, V_cache, block_table, seq_lens, workspace, O), stream)
     if workspace is None:
         workspace = _new(max(attention_decode_window_workspace_size(B, Hq, max_seq_len, window, sinks), 16), torch.uint8, Q, stream)
     if O is None:
-        O = _new((B, Hq, D), torch.bfloat16, Q, stream)
-    _check(load().bi_attention_decode_window(Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), block_table.data_ptr(),
-                                             block_table.shape[1], nblk, seq_lens.data_ptr(), B, Hq, Hkv, D, bs, max_seq_len,
-                                             float(scale), window, sinks, workspace.data_ptr(), workspace.numel(), O.data_ptr(),
-                                             raw), "bi_attention_decode_window")
+        O = _out(Q, stream)
+    raw = _current_raw_stream(cur) if stream is None else stream.cuda_stream
+    st = load().bi_attention_decode_window(Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), block_table.data_ptr(),
+                                           table[1], nblk, seq_lens.data_ptr(), B, Hq, Hkv, D, bs, max_seq_len, scale, window,
+                                           sinks, workspace.data_ptr(), workspace.numel(), O.data_ptr(), raw)
+    if st:
+        raise BiError(st, "bi_attention_decode_window")
     return O
 
 
@@ -904,23 +954,24 @@ def attention_extend_window(Q, cu_q, K_cache, V_cache, block_table, seq_lens, ma
     Table entries of blocks out of every new token's sight may be anything. The workspace (uint8,
     ``attention_extend_window_workspace_size`` bytes) is allocated with torch if not given."""
     import torch
-    (T, Hq, D), (nblk, bs, Hkv, _) = _attention_window_args(Q, K_cache, V_cache, block_table, seq_lens, workspace, O)
-    B = _typed(cu_q, torch.int32, "cu_q").numel() - 1
-    if seq_lens.shape != (B,):
-        raise ValueError("cu_q must have one entry more than seq_lens")
+    cur = _current_device()
+    (T, Hq, D), (nblk, bs, Hkv, _), table = _attention_window_args(Q, K_cache, V_cache, block_table, seq_lens, workspace, O, cur)
+    B = table[0]
+    _tensor(cu_q, torch.int32, (B + 1,), "cu_q", cur)
     window, sinks = _window(window, sinks)
-    raw, _ = _launch_on(None, (Q, cu_q, K_cache, V_cache, block_table, seq_lens, workspace, O), stream)
     if workspace is None:
         need = attention_extend_window_workspace_size(T, Hq, Hkv, max_seq_len, max_q_len, window, sinks)
         workspace = _new(need, torch.uint8, Q, stream) if need > 0 else None
     if O is None:
-        O = _new((T, Hq, D), torch.bfloat16, Q, stream)
-    _check(load().bi_attention_extend_window(Q.data_ptr(), cu_q.data_ptr(), T, K_cache.data_ptr(), V_cache.data_ptr(),
-                                             block_table.data_ptr(), block_table.shape[1], nblk, seq_lens.data_ptr(), B, Hq, Hkv,
-                                             D, bs, max_seq_len, max_q_len, float(scale), window, sinks,
-                                             workspace.data_ptr() if workspace is not None else None,
-                                             workspace.numel() if workspace is not None else 0, O.data_ptr(), raw),
-           "bi_attention_extend_window")
+        O = _out(Q, stream)
+    raw = _current_raw_stream(cur) if stream is None else stream.cuda_stream
+    st = load().bi_attention_extend_window(Q.data_ptr(), cu_q.data_ptr(), T, K_cache.data_ptr(), V_cache.data_ptr(),
+                                           block_table.data_ptr(), table[1], nblk, seq_lens.data_ptr(), B, Hq, Hkv, D, bs,
+                                           max_seq_len, max_q_len, scale, window, sinks,
+                                           workspace.data_ptr() if workspace is not None else None,
+                                           workspace.numel() if workspace is not None else 0, O.data_ptr(), raw)
+    if st:
+        raise BiError(st, "bi_attention_extend_window")
     return O
 
 

@@ -96,7 +96,7 @@ struct HeadsParams {
     const uint64_t *turns;   // [R / 2] turns per position, in units of 2^-64
     int64_t T, cache_rows;   // (without slots: one row)
     float factor, eps, inv_d;
-    int32_t D, R, splits, groups, first[3];   // splits: warps a token; groups of heads, each part's first
+    int32_t D, R, splits;    // splits: warps a token
     unsigned *status;
 };
 

@@ -171,6 +171,10 @@ def test_append(bi, T, Hq, Hkv, D, bs, R, inter, normed):
         want = pattern_cache((blocks * bs, Hkv, D), fill)
         want[slots[good]] = rows[good]
         assert torch.equal(cache.view(blocks * bs, Hkv, D), want)
+    if normed and Hq:                                     # only the keys normed: the queries are turned alone
+        K3, V3 = pattern_cache(Kc.shape, 3.0), pattern_cache(Kc.shape, -5.0)
+        out3 = bi.kv_append(k, v, slots, K3, V3, pos, fr, k_weight=kw, eps=1e-5, Q=q)
+        assert torch.equal(out3, bi.rope(q, pos, fr)) and torch.equal(K3, Kc) and torch.equal(V3, Vc)
     # slots outside: skipped and reported; a position that does not fit in 32 bits: nothing of the token
     if T > 5:
         slots[2], slots[3] = blocks * bs, -7
