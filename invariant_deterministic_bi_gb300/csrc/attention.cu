@@ -224,11 +224,35 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     // item -> (sequence b, KV head g, record c), the chunk's first token j0 and
     // its tokens n (of which [h0, h1) are out of sight); false when the chunk is
     // past the sequence (or the sequence is invalid)
-    auto item = [&](int64_t it, int64_t &b, int &g, int &c, int &j0, int &n, int &h0, int &h1) {
-        g = static_cast<int>(it % p.Hkv);               // KV head fastest: the heads of one
+    // The windowed form steps from item to item without divisions (64-bit ones
+    // cost the consumers, which visit the other group's items too, a tenth of their time).
+    struct Place {
+        int g, c;
+        int64_t b;
+    };
+    auto place = [&](int64_t it) {
+        Place x;
+        x.g = static_cast<int>(it % p.Hkv);             // KV head fastest: the heads of one
         const int64_t r = it / p.Hkv;                    // cache block are read together
-        c = static_cast<int>(r % walk);
-        b = r / walk;
+        x.c = static_cast<int>(r % walk);
+        x.b = r / walk;
+        return x;
+    };
+    Place now = place(blockIdx.x);
+    const Place by = place(gridDim.x);
+    auto advance = [&] {
+        now.g += by.g;
+        int carry = now.g >= p.Hkv;
+        now.g -= carry ? p.Hkv : 0;
+        now.c += by.c + carry;
+        carry = now.c >= walk;
+        now.c -= carry ? walk : 0;
+        now.b += by.b + carry;
+    };
+    auto item = [&](int64_t it, int64_t &b, int &g, int &c, int &j0, int &n, int &h0, int &h1) {
+        const Place x = WIN ? now : place(it);
+        if (WIN) advance();
+        g = x.g, c = x.c, b = x.b;
         int L;
         if (!seq_ok(p, b, L)) {
             if (warp == kDecConsumers && lane == 0 && c == 0 && g == 0) atomicOr(p.status, kDevBadOffsets);   // loader 0
@@ -475,16 +499,18 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             // the NT n-tiles' chains interleaved, each in ascending dimension order
             float acc[NT][4] = {};
 #pragma unroll
-            for (int ks = 0; ks < kD / 16; ++ks) {
-                uint32_t bf[NT][2];
+            for (int kp = 0; kp < kD / 32; ++kp) {             // two 16-dimension steps per ldmatrix
+                uint32_t bf[NT][4];
 #pragma unroll
                 for (int nb = 0; nb < NT; ++nb) {
-                    const int t = gw * 8 * NT + nb * 8 + gq;   // the K row of this lane's B fragment
-                    bf[nb][0] = *reinterpret_cast<const uint32_t *>(Ks + cq * 4 + kv_piece(t, 2 * ks));
-                    bf[nb][1] = *reinterpret_cast<const uint32_t *>(Ks + cq * 4 + kv_piece(t, 2 * ks + 1));
+                    const int t = gw * 8 * NT + nb * 8 + (lane & 7);   // the K row this lane addresses
+                    ldmatrix_x4(bf[nb][0], bf[nb][1], bf[nb][2], bf[nb][3], smem_u32(Ks + kv_piece(t, 4 * kp + (lane >> 3))));
                 }
 #pragma unroll
-                for (int nb = 0; nb < NT; ++nb) mma_16816(acc[nb], qa[ks][0], 0u, qa[ks][1], 0u, bf[nb][0], bf[nb][1]);
+                for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+                    for (int nb = 0; nb < NT; ++nb)
+                        mma_16816(acc[nb], qa[2 * kp + k2][0], 0u, qa[2 * kp + k2][1], 0u, bf[nb][2 * k2], bf[nb][2 * k2 + 1]);
             }
             if (gq < G) {
 #pragma unroll
@@ -502,19 +528,26 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         for (int h = gw; h < G; h += GW) {
             float m = -INFINITY;
             const float *Sh = S + h * kDecSStride;
-            for (int t = lane; t < n; t += 32) m = fmaxf(m, Sh[t]);
+            float sc[kChunk / 32];                            // -inf past the chunk's tokens: p = 0 there
+#pragma unroll
+            for (int k = 0; k < kChunk / 32; ++k) {
+                sc[k] = lane + 32 * k < n ? Sh[lane + 32 * k] : -INFINITY;
+                m = fmaxf(m, sc[k]);
+            }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             if (WIN) {                                        // no visible token in the cache
                 int any = 0;
-                for (int t = lane; t < n; t += 32) any |= vrow[t];
+#pragma unroll
+                for (int k = 0; k < kChunk / 32; ++k) any |= vrow[lane + 32 * k];   // (0 past the chunk's tokens)
                 if (!__any_sync(0xffffffffu, any)) m = kNoScore;
             }
             float l = 0.0f;
-            for (int t = lane; t < n; t += 32) {
-                const float e = expf(Sh[t] - m);
-                S[h * kDecSStride + t] = e;
-                l += e;
+#pragma unroll
+            for (int k = 0; k < kChunk / 32; ++k) {
+                const float e = expf(sc[k] - m);
+                S[h * kDecSStride + lane + 32 * k] = lane + 32 * k < n ? e : 0.0f;
+                if (lane + 32 * k < n) l += e;
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -566,12 +599,10 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 if (gq < G) {
                     const int t0 = ks * 16 + 2 * cq, t2 = t0 + 8;
                     const float *Sq = S + gq * kDecSStride;
-                    const float p00 = t0 < n ? Sq[t0] : 0.0f;
-                    const float p01 = t0 + 1 < n ? Sq[t0 + 1] : 0.0f;
-                    const float p20 = t2 < n ? Sq[t2] : 0.0f;
-                    const float p21 = t2 + 1 < n ? Sq[t2 + 1] : 0.0f;
-                    split_bf16x2(p00, p01, ph[ks][0], pl[ks][0]);
-                    split_bf16x2(p20, p21, ph[ks][1], pl[ks][1]);
+                    const float2 p0 = *reinterpret_cast<const float2 *>(Sq + t0);
+                    const float2 p2 = *reinterpret_cast<const float2 *>(Sq + t2);
+                    split_bf16x2(p0.x, p0.y, ph[ks][0], pl[ks][0]);
+                    split_bf16x2(p2.x, p2.y, ph[ks][1], pl[ks][1]);
                 }
             }
 #pragma unroll
