@@ -115,21 +115,20 @@ __device__ __forceinline__ bool seq_ok(const AttnParams &p, int64_t b, int &L) {
 // flight: per item it resolves the chunk's block-table entries and loads the
 // chunk's K and V rows of KV head g with TMA, one box per cache block (a 4-D
 // tensor map over [blocks][block size][KV heads][128], two 64-dimension
-// halves per box, 128-byte swizzle), plus the G q rows by a bulk copy, all
-// counted on the slot's "full" barrier. Block sizes that boxes cannot tile
+// halves per box, 128-byte swizzle), plus the G q rows by a bulk copy, counted
+// on "full" barriers of the slot's K (and q) and V halves. Block sizes that boxes cannot tile
 // (not a multiple of 128 and not 8, 16, 32 or 64) take 16-byte cp.async
 // copies per row instead. Blocks outside the cache arrive as zeros and their
 // tokens score -inf. Eight consumer warps, in NG groups, compute the chunks
-// and hand each slot back through its "empty" barrier.
+// and hand each half back through its "empty" barrier: the next item's K loads
+// while the softmax and p.V of this one run.
 //
 // Two shapes of the kernel, the same arithmetic per item:
 //   - many items: SLOTS = 3 ring slots, NG = 2 groups of four warps on
 //     alternate items (two items in compute while up to three load), one CTA
 //     per SM;
 //   - few items (at most two CTAs' worth per SM): SLOTS = 1, NG = 1, one item
-//     per CTA on all eight warps, two CTAs per SM; the V rows are counted on
-//     a second "full" barrier, so that the scores start as soon as K and q
-//     have landed.
+//     per CTA on all eight warps, two CTAs per SM.
 constexpr int kHalfTile = kChunk * 128;                  // one 64-dimension half of a K or V tile (swizzled)
 constexpr int kSlotBytes = 4 * kHalfTile + 8 * kRowBytes; // K, V, up to 8 q rows
 constexpr int kDecConsumers = kThreads / 32;             // 8 warps
@@ -139,7 +138,7 @@ template <int SLOTS>
 constexpr int dec_threads() { return kThreads + 32 * SLOTS; }   // + one loading warp per slot
 template <int SLOTS, int NG>
 constexpr int dec_smem() {
-    return 1024 + SLOTS * kSlotBytes + 2 * NG * kDecSFloats * 4 + SLOTS * kChunk + (2 * NG + 1) * SLOTS * 8 + 16;
+    return 1024 + SLOTS * kSlotBytes + 2 * NG * kDecSFloats * 4 + 2 * SLOTS * kChunk + (2 * NG + 2) * SLOTS * 8 + 16;
 }
 static_assert(kSlotBytes % 1024 == 0, "slot alignment (128-byte swizzle atoms)");
 static_assert(2 * dec_smem<1, 1>() <= 232448, "two few-item CTAs per SM");
@@ -183,27 +182,34 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     float *S0 = reinterpret_cast<float *>(smem + kSlots * kSlotBytes);     // [group][2][G][kDecSStride] scores
-    uint8_t *valid = reinterpret_cast<uint8_t *>(S0 + 2 * NG * kDecSFloats); // [kSlots][kChunk]: row has K/V
+    uint8_t *valid = reinterpret_cast<uint8_t *>(S0 + 2 * NG * kDecSFloats); // [2][kSlots][kChunk]: row has K/V
+    // A slot is two halves: K rows (with q), and V rows. Each has its own "full" and
+    // "empty" barriers, so that the scores start once K and q have landed, and the
+    // next item's K loads once the scores are computed, while V is still in use.
+    // The row flags, which are written with K and read until the softmax, alternate
+    // between two sets: the set of item k is written again for item k + 2 kSlots, whose
+    // K is loaded only after V of item k + kSlots, and so after item k was done with.
     // Barriers. Every waiter waits only for the phase right after one it has
     // seen complete (a parity wait cannot tell a phase from the one two
     // later): slot s is filled by one loading warp in item order, so one
-    // "empty" barrier per slot serves it; the items of a slot alternate
-    // between the consumer groups, so each (slot, group) has its own "full"
+    // "empty" barrier per half serves it; the items of a slot alternate
+    // between the consumer groups, so each (half, group) has its own "full"
     // barrier, whose phases are that group's items on that slot in order.
-    // With one item per CTA (kSlots = 1) the V rows have a "full" barrier of
-    // their own (fullV); the ring counts them with the K rows.
-    constexpr bool kSplitKV = kSlots == 1;
-    uint64_t *full = reinterpret_cast<uint64_t *>(valid + kSlots * kChunk);   // [kSlots][NG]
-    uint64_t *fullV = full + kSlots * NG;                                     // [kSlots][NG], kSplitKV only
-    uint64_t *empty = fullV + kSlots * NG;                                    // [kSlots]
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(empty + kSlots);
+    uint64_t *full = reinterpret_cast<uint64_t *>(valid + 2 * kSlots * kChunk);   // [kSlots][NG]: K, q
+    uint64_t *fullV = full + kSlots * NG;                                     // [kSlots][NG]
+    uint64_t *empty = fullV + kSlots * NG;                                    // [kSlots]: K, q
+    uint64_t *emptyV = empty + kSlots;                                        // [kSlots]
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(emptyV + kSlots);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < kSlots * NG; ++s) {
             mbar_init(&full[s], p.box_rows > 0 ? 32 : 64);
             mbar_init(&fullV[s], p.box_rows > 0 ? 32 : 64);
         }
-        for (int s = 0; s < kSlots; ++s) mbar_init(&empty[s], kDecConsumers / NG);
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(&empty[s], kDecConsumers / NG);
+            mbar_init(&emptyV[s], kDecConsumers / NG);
+        }
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -224,8 +230,8 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     // item -> (sequence b, KV head g, record c), the chunk's first token j0 and
     // its tokens n (of which [h0, h1) are out of sight); false when the chunk is
     // past the sequence (or the sequence is invalid)
-    // The windowed form steps from item to item without divisions (64-bit ones
-    // cost the consumers, which visit the other group's items too, a tenth of their time).
+    // Called once an item, in turn: steps without divisions (64-bit ones cost the
+    // consumers, which visit the other group's items too, a tenth of their time).
     struct Place {
         int g, c;
         int64_t b;
@@ -249,10 +255,9 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         now.c -= carry ? walk : 0;
         now.b += by.b + carry;
     };
-    auto item = [&](int64_t it, int64_t &b, int &g, int &c, int &j0, int &n, int &h0, int &h1) {
-        const Place x = WIN ? now : place(it);
-        if (WIN) advance();
-        g = x.g, c = x.c, b = x.b;
+    auto item = [&](int64_t &b, int &g, int &c, int &j0, int &n, int &h0, int &h1) {
+        g = now.g, c = now.c, b = now.b;
+        advance();
         int L;
         if (!seq_ok(p, b, L)) {
             if (warp == kDecConsumers && lane == 0 && c == 0 && g == 0) atomicOr(p.status, kDevBadOffsets);   // loader 0
@@ -283,22 +288,20 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         // K and V rows are read once: evict them from L2 first, so that the
         // chunk partials the combine step reads stay there
         const uint64_t kv_policy = l2_policy_evict_first();
-        int k = 0, last = -1;
+        int k = 0, last = -1, lastV = -1;                // this warp's last item whose K, V were issued
         for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
             // the item's block-table entries (boxes: lane i < kChunk / box_rows
             // reads box i's) are requested before its sequence length is
             // known, so the two reads overlap instead of following each other
             int32_t spec_blk = -1;
             if (!WIN && p.box_rows > 0) {
-                const int64_t r = it / p.Hkv;
-                const int64_t bb = r / p.chunks;
-                const int64_t bi = ((r % p.chunks) * kChunk + lane * p.box_rows) / p.bs;
-                if (lane < kChunk / p.box_rows && bb < p.batch && bi < p.max_blocks)
-                    spec_blk = ld_nc_s32(p.table + bb * p.max_blocks + bi);
+                const int bi = (now.c * kChunk + lane * p.box_rows) / p.bs;
+                if (lane < kChunk / p.box_rows && bi < p.max_blocks)
+                    spec_blk = ld_nc_s32(p.table + now.b * p.max_blocks + bi);
             }
             int64_t b;
             int g, c, j0, n, h0, h1;
-            if (!item(it, b, g, c, j0, n, h0, h1)) continue;
+            if (!item(b, g, c, j0, n, h0, h1)) continue;
             if (k % kSlots != lw) {
                 ++k;
                 continue;
@@ -340,114 +343,97 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 }
             }
             const int slot = k % kSlots;
-            uint64_t *fb = &full[slot * NG + k % NG];   // the consuming group's barrier for this slot
-            uint64_t *fbv = kSplitKV ? &fullV[slot * NG + k % NG] : fb;   // the one counting the V rows
-            if (k >= kSlots && !mbar_wait(&empty[slot], ((k / kSlots) - 1) & 1, abort_flag)) {
+            uint64_t *fb = &full[slot * NG + k % NG];    // the consuming group's barriers for this slot
+            uint64_t *fbv = &fullV[slot * NG + k % NG];
+            auto freed = [&](uint64_t *bar) {              // the half's last item is done with it
+                if (k < kSlots || mbar_wait(bar, ((k / kSlots) - 1) & 1, abort_flag)) return true;
                 if (lane == 0) {
                     atomicOr(p.status, kDevTimeout);
                     *abort_flag = 1;
                 }
-                break;
-            }
+                return false;
+            };
+            if (!freed(&empty[slot])) break;
             uint8_t *Ks = smem + slot * kSlotBytes;
             uint8_t *Vs = Ks + 2 * kHalfTile;
             uint8_t *qs = Vs + 2 * kHalfTile;
+            uint8_t *flags = valid + (((k / kSlots) & 1) * kSlots + slot) * kChunk;
 #pragma unroll
-            for (int i = 0; i < kChunk / 32; ++i) valid[slot * kChunk + lane + 32 * i] = ok_row[i];
+            for (int i = 0; i < kChunk / 32; ++i) flags[lane + 32 * i] = ok_row[i];
             const uint16_t *qsrc = p.Q + (b * p.Hq + g * G) * kD;
             if (p.box_rows > 0) {
                 // one box per cache block (box_rows tokens), both halves
                 const int boxes = WIN ? __popc(__ballot_sync(0xffffffffu, box)) : nbox;
                 const int kv_bytes = boxes * p.box_rows * 2 * 128;  // the K rows, or the V rows
                 const int tok = (j0 + lane * p.box_rows) % p.bs;
-                // V rows no box reaches (a chunk past the sequence's end) become
-                // zero, so that p = 0 meets finite values there; each lane's
-                // arrival on the barrier counting the V rows releases its zeros
-                auto zero_v_tail = [&] {
-                    for (int r = nbox * p.box_rows + lane; r < kChunk; r += 32) {
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint4 *v = reinterpret_cast<uint4 *>(Vs + half * kHalfTile + r * 128);
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) v[x] = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                    }
-                    fence_proxy_async_smem();         // before later bulk copies into these rows
-                    __syncwarp();
-                };
-                if (!kSplitKV) zero_v_tail();
                 __syncwarp();
                 // each lane's arrival releases its shared-memory writes; lane 0
                 // also sets the bytes to expect, before any copy is issued
                 if (lane == 0)
-                    mbar_arrive_expect_tx(fb, (kSplitKV ? 1 : 2) * kv_bytes + G * kRowBytes);
+                    mbar_arrive_expect_tx(fb, kv_bytes + G * kRowBytes);
                 else
                     mbar_arrive(fb);
                 __syncwarp();
-                if (kSplitKV) {
-                    // q and K first: the scores need them before p.V needs V
-                    if (lane == 0) bulk_load(qs, qsrc, G * kRowBytes, fb);
-                    if (box) {                        // a block outside the cache arrives as zeros
+                if (lane == 0) bulk_load(qs, qsrc, G * kRowBytes, fb);
+                if (box) {                            // a block outside the cache arrives as zeros
 #pragma unroll
-                        for (int half = 0; half < 2; ++half)
-                            tma_load_4d_hint(Ks + half * kHalfTile + lane * p.box_rows * 128, &tmK, fb, half * 64, g,
-                                             tok, box_blk, kv_policy);
-                    }
-                    zero_v_tail();
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(fbv, kv_bytes);
-                    else
-                        mbar_arrive(fbv);
-                    __syncwarp();
-                    if (box) {
+                    for (int half = 0; half < 2; ++half)
+                        tma_load_4d_hint(Ks + half * kHalfTile + lane * p.box_rows * 128, &tmK, fb, half * 64, g,
+                                         tok, box_blk, kv_policy);
+                }
+                last = k;
+                if (!freed(&emptyV[slot])) break;
+                // V rows no box reaches (a chunk past the sequence's end) become
+                // zero, so that p = 0 meets finite values there; each lane's
+                // arrival on the V rows' barrier releases its zeros
+                for (int r = nbox * p.box_rows + lane; r < kChunk; r += 32) {
 #pragma unroll
-                        for (int half = 0; half < 2; ++half)
-                            tma_load_4d_hint(Vs + half * kHalfTile + lane * p.box_rows * 128, &tmV, fbv, half * 64, g,
-                                             tok, box_blk, kv_policy);
-                    }
-                } else {
-                    // the ring consumes a slot whole: K and V boxes in turn, then q
-                    if (box) {
+                    for (int half = 0; half < 2; ++half) {
+                        uint4 *v = reinterpret_cast<uint4 *>(Vs + half * kHalfTile + r * 128);
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const int dst = half * kHalfTile + lane * p.box_rows * 128;
-                            tma_load_4d_hint(Ks + dst, &tmK, fb, half * 64, g, tok, box_blk, kv_policy);
-                            tma_load_4d_hint(Vs + dst, &tmV, fb, half * 64, g, tok, box_blk, kv_policy);
-                        }
+                        for (int x = 0; x < 8; ++x) v[x] = make_uint4(0u, 0u, 0u, 0u);
                     }
-                    if (lane == 0) bulk_load(qs, qsrc, G * kRowBytes, fb);
+                }
+                fence_proxy_async_smem();             // before later bulk copies into these rows
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_expect_tx(fbv, kv_bytes);
+                else
+                    mbar_arrive(fbv);
+                __syncwarp();
+                if (box) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+                        tma_load_4d_hint(Vs + half * kHalfTile + lane * p.box_rows * 128, &tmV, fbv, half * 64, g,
+                                         tok, box_blk, kv_policy);
                 }
             } else {
                 // 16-byte copies per row (rows without K/V zero-filled); each lane
-                // arrives twice: now, and once its copies have landed (both on
-                // the V rows' barrier too, when it has its own)
+                // arrives twice on a half's barrier: now, and once its copies have landed
+                auto rows = [&](uint8_t *dst, const uint16_t *src, uint64_t *bar) {
 #pragma unroll
-                for (int i = 0; i < kChunk / 32; ++i) {
-                    const int t = lane + 32 * i;
-                    for (int x = 0; x < kRowBytes / 16; ++x) {
-                        const uint32_t so = kv_piece(t, x);
-                        cp_async_16(smem_u32(Ks) + so, off[i] >= 0 ? p.K + off[i] + x * 8 : p.K, off[i] >= 0 ? 16u : 0u);
-                        cp_async_16(smem_u32(Vs) + so, off[i] >= 0 ? p.V + off[i] + x * 8 : p.V, off[i] >= 0 ? 16u : 0u);
+                    for (int i = 0; i < kChunk / 32; ++i) {
+                        const int t = lane + 32 * i;
+                        for (int x = 0; x < kRowBytes / 16; ++x)
+                            cp_async_16(smem_u32(dst) + kv_piece(t, x), off[i] >= 0 ? src + off[i] + x * 8 : src, off[i] >= 0 ? 16u : 0u);
                     }
-                }
+                    mbar_arrive(bar);                 // releases this lane's row flags
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+                };
                 for (int x = lane; x < G * kRowBytes / 16; x += 32) cp_async_16(smem_u32(qs) + x * 16, qsrc + x * 8, 16u);
-                mbar_arrive(fb);                      // releases this lane's row flags
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(fb)) : "memory");
-                if (kSplitKV) {
-                    mbar_arrive(fbv);
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(fbv)) : "memory");
-                }
+                rows(Ks, p.K, fb);
+                last = k;
+                if (!freed(&emptyV[slot])) break;
+                rows(Vs, p.V, fbv);
             }
-            last = k;
+            lastV = k;
             ++k;
         }
         // the copies of this warp's last item must land before the CTA exits
         // (the consumers normally waited for them already; every earlier item
         // of the slot was consumed before the slot was filled again)
-        if (last >= 0) {
-            mbar_wait(&full[(last % kSlots) * NG + last % NG], (last / (kSlots * NG)) & 1, nullptr);
-            if (kSplitKV) mbar_wait(&fullV[(last % kSlots) * NG + last % NG], (last / (kSlots * NG)) & 1, nullptr);
-        }
+        if (last >= 0) mbar_wait(&full[(last % kSlots) * NG + last % NG], (last / (kSlots * NG)) & 1, nullptr);
+        if (lastV >= 0) mbar_wait(&fullV[(lastV % kSlots) * NG + lastV % NG], (lastV / (kSlots * NG)) & 1, nullptr);
         return;
     }
 
@@ -464,7 +450,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         int64_t b;
         int g, c, j0, n, h0, h1;
-        if (!item(it, b, g, c, j0, n, h0, h1)) continue;
+        if (!item(b, g, c, j0, n, h0, h1)) continue;
         if (k % NG != grp) {
             ++k;
             continue;
@@ -481,7 +467,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         const uint8_t *Ks = smem + slot * kSlotBytes;
         const uint8_t *Vs = Ks + 2 * kHalfTile;
         const uint16_t *qb = reinterpret_cast<const uint16_t *>(Vs + 2 * kHalfTile);
-        const uint8_t *vrow = valid + slot * kChunk;
+        const uint8_t *vrow = valid + (((k / kSlots) & 1) * kSlots + slot) * kChunk;
         float *S = S0 + (grp * 2 + ((k / NG) & 1)) * kDecSFloats;
         float *wsh = p.ws + ((b * p.Hq + g * G) * p.chunks + c) * static_cast<int64_t>(kD + 2);
         if (!BI_IN_BOUNDS(b < p.batch && c < p.chunks, p.status)) break;
@@ -522,6 +508,8 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     }
             }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);         // this warp is done with K and q
         group_sync<GW>(grp);
 
         // per head: max, exponentials, sum (head h on warp h % GW); (m, l) to the workspace
@@ -556,7 +544,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 wsh[h * ws_head + 1] = l;
             }
         }
-        const bool ok_v = !kSplitKV || mbar_wait(&fullV[slot * NG + grp], (k / (kSlots * NG)) & 1, abort_flag);
+        const bool ok_v = mbar_wait(&fullV[slot * NG + grp], (k / (kSlots * NG)) & 1, abort_flag);
         // rows behind the sequence's end that came with its last box (of 8, 16, 32,
         // 64 or 128 rows), and rows out of sight: whatever stands there, p = 0 has to
         // meet finite values
@@ -571,16 +559,12 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 st_shared_v4(smem_u32(Vs + kv_piece(h0 + i / (kRowBytes / 16), i % (kRowBytes / 16))), 0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
         }
-        if (kSplitKV) {
-            if (group_sync_or<GW>(grp, !ok_v)) {              // the V rows did not land
-                if (gw == 0 && lane == 0) {
-                    atomicOr(p.status, kDevTimeout);
-                    *abort_flag = 1;
-                }
-                break;
+        if (group_sync_or<GW>(grp, !ok_v)) {                  // the V rows did not land
+            if (gw == 0 && lane == 0) {
+                atomicOr(p.status, kDevTimeout);
+                *abort_flag = 1;
             }
-        } else {
-            group_sync<GW>(grp);
+            break;
         }
 
         // values O[h][d] = sum_t p_t v_t[d] on the tensor cores: A = p (rows =
@@ -636,7 +620,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[slot]);         // this warp is done with the slot
+        if (lane == 0) mbar_arrive(&emptyV[slot]);        // this warp is done with V
         ++k;
     }
 }
