@@ -348,9 +348,12 @@ bi_status attention_extend(const void *Q, const int32_t *cu_q, int32_t total_q, 
         return BI_ERR_MISALIGNED;
     bi_status st = require_device();
     if (st != BI_OK) return st;
+    if (window > 0)
+        return launch_attention_extend_window(Q, cu_q, total_q, K_cache, V_cache, block_table, max_blocks_per_seq, num_blocks,
+                                              seq_lens, B, Hq, Hkv, block_size, max_seq_len, max_q_len, scale, window, sinks,
+                                              O, as_stream(stream));
     return launch_attention_extend(Q, cu_q, total_q, K_cache, V_cache, block_table, max_blocks_per_seq, num_blocks,
-                                   seq_lens, B, Hq, Hkv, block_size, max_seq_len, max_q_len, scale, window, sinks, O,
-                                   as_stream(stream));
+                                   seq_lens, B, Hq, Hkv, block_size, max_seq_len, max_q_len, scale, O, as_stream(stream));
 }
 }  // namespace
 

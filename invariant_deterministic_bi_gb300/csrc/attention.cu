@@ -60,8 +60,6 @@ namespace {
 
 constexpr int kThreads = 256;                  // split kernel
 constexpr int kCombineThreads = 128;           // one thread per output dimension
-constexpr int kRowBytes = kD * 2;              // one token's K (or V) row of one KV head
-constexpr int kTileBytes = kChunk * kRowBytes; // 32 KB
 
 struct AttnParams {
     const uint16_t *Q;       // [B][Hq][D]
@@ -77,23 +75,6 @@ struct AttnParams {
     int32_t window, sinks;   // windowed form (chunks then counts the records a head)
     float scale;
     unsigned *status;
-};
-
-// Sliding window: a token at position p sees the tokens j <= p with j > p - window
-// or j < sinks. For the earliest of some tokens (its length n, n - window = from)
-// and all after it: first tokens [0, first), then from `lo` on; of the chunks,
-// the `ns` that hold first tokens before lo's chunk c0, then c0 and the rest.
-struct Seen {
-    int first, lo, ns, c0;
-    __device__ __forceinline__ Seen(int from, int sinks) {
-        lo = max(0, from);
-        first = min(sinks, lo);
-        c0 = lo / kChunk;
-        ns = min((first + kChunk - 1) / kChunk, c0);
-    }
-    __device__ __forceinline__ int chunks(int n) const { return ns + (n + kChunk - 1) / kChunk - c0; }
-    __device__ __forceinline__ int start(int i) const { return (i < ns ? i : c0 + i - ns) * kChunk; }   // of the i-th chunk
-    __device__ __forceinline__ bool has(int j) const { return j < first || j >= lo; }
 };
 
 // A read-only load issued where it stands (the table is not written while a
@@ -129,7 +110,6 @@ __device__ __forceinline__ bool seq_ok(const AttnParams &p, int64_t b, int &L) {
 //     per SM;
 //   - few items (at most two CTAs' worth per SM): SLOTS = 1, NG = 1, one item
 //     per CTA on all eight warps, two CTAs per SM.
-constexpr int kHalfTile = kChunk * 128;                  // one 64-dimension half of a K or V tile (swizzled)
 constexpr int kSlotBytes = 4 * kHalfTile + 8 * kRowBytes; // K, V, up to 8 q rows
 constexpr int kDecConsumers = kThreads / 32;             // 8 warps
 constexpr int kDecSStride = kChunk + 8;                 // scores of one head (padded)
@@ -142,11 +122,6 @@ constexpr int dec_smem() {
 }
 static_assert(kSlotBytes % 1024 == 0, "slot alignment (128-byte swizzle atoms)");
 static_assert(2 * dec_smem<1, 1>() <= 232448, "two few-item CTAs per SM");
-
-// Byte offset of 16-byte piece x (0..15) of token row t in a swizzled K or V tile.
-__device__ __forceinline__ int kv_piece(int t, int x) {
-    return (x >> 3) * kHalfTile + t * 128 + (((x & 7) ^ (t & 7)) << 4);
-}
 
 // bar.sync on the named barrier (1 + grp) of consumer group grp's GW warps
 template <int GW>
@@ -733,7 +708,6 @@ struct ExtParams {
     uint16_t *O;             // [total_q][Hq][D]
     int64_t num_blocks, batch;
     int32_t total_q, max_blocks, Hq, Hkv, bs, max_len, max_q;
-    int32_t window, sinks;   // windowed form
     float scale;
     unsigned *status;
 };
@@ -748,13 +722,7 @@ __device__ __forceinline__ void turn_pass(int id) { asm volatile("bar.arrive %0,
 // tile that the bf16 form copies, so everything after the tile is shared. The
 // expansion is about 6 % of a chunk's time (1 x 4096 new over 8192 cached tokens,
 // 32 heads over 8: 2.09 ms, 197 TFLOP/s).
-//
-// WIN: the windowed form (bf16 cache). The CTA walks the chunks in which a token
-// of its tile sees something; rows mask what is out of their own window. V rows
-// that every token of the tile is blind to are zeros; in a chunk that is masked
-// for some token and holds a value that is not finite, p.V runs once a token over
-// V rows that are zero where that token is blind (0 * NaN would reach it).
-template <int G, bool I4, bool WIN>
+template <int G, bool I4>
 __global__ void __launch_bounds__(kExtThreads, 1)
 attn_extend_kernel(const ExtParams p) {
     constexpr int kRowBufs = I4 ? 4 : 3;               // chunks whose row offsets are held
@@ -788,9 +756,7 @@ attn_extend_kernel(const ExtParams p) {
     const int ntok = static_cast<int>(qlen - i0 < kTQ ? qlen - i0 : static_cast<int64_t>(kTQ));
     const int base = L - static_cast<int>(qlen);       // position of query token 0
     const int L_last = base + i0 + ntok;               // the last token's causal length
-    const Seen w(WIN ? base + i0 + 1 - p.window : 0, WIN ? p.sinks : 0);   // of the tile's tokens together
-    const int nchunks = WIN ? w.chunks(L_last) : (L_last + kChunk - 1) / kChunk;
-    auto chunk_start = [&](int c) { return WIN ? w.start(c) : c * kChunk; };   // of the c-th chunk walked
+    const int nchunks = (L_last + kChunk - 1) / kChunk;
 
     // q rows: row r = token r / G, head g*G + r % G (zero rows past the
     // tokens); 16-byte piece x of row r at piece x ^ (r % 8). Copied by
@@ -806,9 +772,9 @@ attn_extend_kernel(const ExtParams p) {
     auto chunk_rows = [&](int c) -> int {
         int bad = 0;
         if (tid < kChunk) {
-            const int j = chunk_start(c) + tid;
+            const int j = c * kChunk + tid;
             int64_t off = -1;
-            if (j < L_last && (!WIN || w.has(j))) {
+            if (j < L_last) {
                 const int64_t blk = p.table[b * p.max_blocks + j / p.bs];
                 if (blk >= 0 && blk < p.num_blocks) {
                     off = I4 ? ((blk * p.Hkv + g) * p.bs + j % p.bs) * 4 + i4_place(0, j % p.bs)   // row, segment 0's place
@@ -933,7 +899,7 @@ attn_extend_kernel(const ExtParams p) {
     const int len_b = rb / G < ntok ? base + i0 + rb / G + 1 : 0;
 
     for (int c = 0; c < nchunks; ++c) {
-        const int j0 = chunk_start(c);
+        const int j0 = c * kChunk;
         const int64_t *ro = rowoff + (c % kRowBufs) * kChunk;
         const uint8_t *Ks = KV + (2 * (c & 1)) * kTileBytes;
         const uint8_t *Vs = KV + (2 * (c & 1) + 1) * kTileBytes;
@@ -951,32 +917,11 @@ attn_extend_kernel(const ExtParams p) {
         } else {
             cp_async_wait<0>();
         }
-        bool odd = false;                              // WIN: masked, with a value of V that is not finite
-        if (WIN) {
-            // masked for some token: the first one's length, or the last one's window
-            const bool masked = j0 + kChunk > base + i0 + 1 || (j0 < L_last - p.window && j0 + kChunk > p.sinks);
-            int bad_v = 0;
-            if (masked) {
-                for (int i = tid; i < kTileBytes / 16; i += kExtThreads) {   // the vectors that this thread copied
-                    uint32_t x[4];
-                    ld_shared_v4(smem_u32(Vs) + (i >> 4) * kRowBytes + (((i & 15) ^ ((i >> 4) & 7)) << 4), x[0], x[1], x[2], x[3]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        bad_v |= (x[k] & 0x7F80u) == 0x7F80u || (x[k] & 0x7F800000u) == 0x7F800000u;
-                }
-            }
-            odd = __syncthreads_or(bad_v) != 0;
-        } else {
-            __syncthreads();                           // everyone's
-        }
+        __syncthreads();                               // everyone's
         if (I4 && c + 1 < nchunks) expand_chunk(c + 1);
 
         // tokens of this chunk each row sees (decode of the sequence cut after the row's token)
         const int na = max(0, min(kChunk, len_a - j0)), nb = max(0, min(kChunk, len_b - j0));
-        // WIN: of them, those before s0 or from fa (fb) on
-        const int s0 = WIN ? p.sinks - j0 : 0, fa = WIN ? len_a - p.window - j0 : 0, fb = WIN ? len_b - p.window - j0 : 0;
-        auto sees = [&](int h, int t) { return t < (h ? nb : na) && (!WIN || t < s0 || t >= (h ? fb : fa)); };
-        auto sees_any = [&](int h) { return (h ? nb : na) > 0 && (!WIN || s0 > 0 || (h ? fb : fa) < (h ? nb : na)); };
         // The two warp groups (warps 0-3, 4-7; warp w and w + 4 share a
         // scheduler) take turns on the tensor pipe: A's q.k, B's q.k, A's p.V,
         // B's p.V, ..., each group's softmax and merge running under the other
@@ -1018,8 +963,7 @@ attn_extend_kernel(const ExtParams p) {
         turn_pass(wg == 0 ? 2 : 1);
         // a chunk every row of the tile sees whole, with every block valid,
         // needs no masks
-        const bool whole = !bad && __all_sync(0xffffffffu, na == kChunk && nb == kChunk &&
-                                                           (!WIN || s0 >= kChunk || (fa <= 0 && fb <= 0)));
+        const bool whole = !bad && __all_sync(0xffffffffu, na == kChunk && nb == kChunk);
         float m[2] = {-INFINITY, -INFINITY};
         if (whole) {
 #pragma unroll
@@ -1035,8 +979,8 @@ attn_extend_kernel(const ExtParams p) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = nt * 8 + 2 * cq + (e & 1);
-                    s[nt][e] = sees(e >> 1, t) ? (ro[t] >= 0 ? __fmul_rn(s[nt][e], p.scale) : -INFINITY)
-                                               : -INFINITY;
+                    s[nt][e] = t < (e < 2 ? na : nb) ? (ro[t] >= 0 ? __fmul_rn(s[nt][e], p.scale) : -INFINITY)
+                                                     : -INFINITY;
                     m[e >> 1] = fmaxf(m[e >> 1], s[nt][e]);
                 }
         }
@@ -1048,22 +992,6 @@ attn_extend_kernel(const ExtParams p) {
                             : in[3] ? __ffs(in[3]) + 95 : kChunk;
             m[0] = fmaxf(m[0], first < na ? -INFINITY : kNoScore);
             m[1] = fmaxf(m[1], first < nb ? -INFINITY : kNoScore);
-        }
-        if (WIN && bad) {                              // the same, where a row's tokens need not be the first ones
-            int any[2] = {0, 0};
-#pragma unroll
-            for (int nt = 0; nt < kChunk / 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = nt * 8 + 2 * cq + (e & 1);
-                    any[e >> 1] |= sees(e >> 1, t) && ro[t] >= 0;
-                }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                any[h] |= __shfl_xor_sync(0xffffffffu, any[h], 1);
-                any[h] |= __shfl_xor_sync(0xffffffffu, any[h], 2);
-                if (!any[h]) m[h] = kNoScore;
-            }
         }
         // per row: max (any order gives the same value), then e^(s - m) for the
         // tokens it sees (0 past them)
@@ -1083,7 +1011,7 @@ attn_extend_kernel(const ExtParams p) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = nt * 8 + 2 * cq + (e & 1);
-                    s[nt][e] = sees(e >> 1, t) ? expf(s[nt][e] - m[e >> 1]) : 0.0f;
+                    s[nt][e] = t < (e < 2 ? na : nb) ? expf(s[nt][e] - m[e >> 1]) : 0.0f;
                 }
         }
         // per row: the sum in decode's order. Lane L of decode sums tokens
@@ -1116,19 +1044,6 @@ attn_extend_kernel(const ExtParams p) {
             l[h] = x[0] + x[1];                                           // step 1
         }
 
-        for (int pass = 0; pass < (WIN && odd ? ntok : 1); ++pass) {
-        if (WIN && odd) {                              // V as this token may see it
-            const int n = base + i0 + pass + 1 - j0, f = n - p.window;
-            __syncthreads();                           // the pass before has been computed (all read V)
-            for (int i = tid; i < kTileBytes / 16; i += kExtThreads) {
-                const int t = i >> 4, x = i & 15;
-                const bool in = ro[t] >= 0 && t < n && (t < s0 || t >= f);
-                cp_async_16(smem_u32(Vs) + t * kRowBytes + ((x ^ (t & 7)) << 4), in ? p.V + ro[t] + x * 8 : p.V, in ? 16u : 0u);
-            }
-            cp_async_commit();
-            cp_async_wait<0>();
-            __syncthreads();
-        }
         turn_wait(wg == 0 ? 1 : 2);
         // values: O_c = sum_t p_t v_t for all 128 dimensions, p = hi + lo
         // (two bf16 MMAs per step), tokens ascending in 16-token steps; the
@@ -1176,7 +1091,7 @@ attn_extend_kernel(const ExtParams p) {
         // merge this chunk into the rows' running state, in chunk order
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if (!sees_any(h) || (WIN && odd && (h ? rb : ra) / G != pass)) continue;
+            if ((h ? nb : na) == 0) continue;
             float mn, al, be;
             merge_factors(m_run[h], m[h], mn, al, be);
             m_run[h] = mn;
@@ -1186,7 +1101,6 @@ attn_extend_kernel(const ExtParams p) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                     o_run[nt][2 * h + e] = merge_value(o_run[nt][2 * h + e], acc[nt][2 * h + e], al, be);
-        }
         }
     }
 
@@ -1228,6 +1142,21 @@ int64_t attention_decode_workspace_bytes(int64_t B, int32_t Hq, int32_t max_len,
     const int64_t records_max = INT64_MAX / kRecord;
     if (B > records_max / Hq || B * Hq > records_max / chunks) return -1;
     return B * Hq * chunks * kRecord;
+}
+
+// TMA boxes of whole cache blocks (box start rows on 1024-byte swizzle atoms): tokens a box, 0 without boxes.
+int32_t kv_box_maps(const void *K, const void *V, int64_t num_blocks, int32_t bs, int32_t Hkv, CUtensorMap *tmK, CUtensorMap *tmV) {
+    const int32_t rows = bs % kChunk == 0 ? kChunk : (kChunk % bs == 0 && bs >= 8 ? bs : 0);
+    if (rows == 0) return 0;
+    const uint64_t dims[4] = {static_cast<uint64_t>(kD), static_cast<uint64_t>(Hkv), static_cast<uint64_t>(bs),
+                              static_cast<uint64_t>(num_blocks)};
+    const uint64_t strides[3] = {static_cast<uint64_t>(kRowBytes), static_cast<uint64_t>(Hkv) * kRowBytes,
+                                 static_cast<uint64_t>(bs) * Hkv * kRowBytes};
+    const uint32_t box[4] = {64, 1, static_cast<uint32_t>(rows), 1};
+    if (make_tmap_4d(tmK, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, K, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != BI_OK ||
+        make_tmap_4d(tmV, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, V, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != BI_OK)
+        return 0;                                    // the per-row copies need no tensor map
+    return rows;
 }
 
 template <int G, int SLOTS, int NG, bool WIN>
@@ -1289,21 +1218,8 @@ bi_status launch_attention_decode(const void *Q, const void *K, const void *V, c
     const DeviceInfo *info = nullptr;
     if (current_device(&dev, &info) != BI_OK) return BI_ERR_CUDA;
     const int64_t items = B * Hkv * static_cast<int64_t>(p.chunks);
-    // TMA boxes of whole cache blocks (box start rows on 1024-byte swizzle atoms)
     CUtensorMap tmK{}, tmV{};
-    p.box_rows = bs % kChunk == 0 ? kChunk : (kChunk % bs == 0 && bs >= 8 ? bs : 0);
-    if (p.box_rows > 0) {
-        const uint64_t dims[4] = {static_cast<uint64_t>(kD), static_cast<uint64_t>(Hkv), static_cast<uint64_t>(bs),
-                                  static_cast<uint64_t>(num_blocks)};
-        const uint64_t strides[3] = {static_cast<uint64_t>(kRowBytes), static_cast<uint64_t>(Hkv) * kRowBytes,
-                                     static_cast<uint64_t>(bs) * Hkv * kRowBytes};
-        const uint32_t box[4] = {64, 1, static_cast<uint32_t>(p.box_rows), 1};
-        if (make_tmap_4d(&tmK, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, K, dims, strides, box,
-                         CU_TENSOR_MAP_SWIZZLE_128B) != BI_OK ||
-            make_tmap_4d(&tmV, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, V, dims, strides, box,
-                         CU_TENSOR_MAP_SWIZZLE_128B) != BI_OK)
-            p.box_rows = 0;                          // the per-row copies need no tensor map
-    }
+    p.box_rows = kv_box_maps(K, V, num_blocks, bs, Hkv, &tmK, &tmV);
     const bool win = window > 0;
     const bi_status st = win ? launch_split_win<true>(G, items, info->sm_count, tmK, tmV, p, s)
                              : launch_split_win<false>(G, items, info->sm_count, tmK, tmV, p, s);
@@ -1312,24 +1228,22 @@ bi_status launch_attention_decode(const void *Q, const void *K, const void *V, c
                       dim3(kCombineThreads), 0, s, p);
 }
 
-template <int G, bool I4, bool WIN>
+template <int G, bool I4>
 bi_status launch_extend_g(const dim3 &grid, const ExtParams &p, cudaStream_t s) {
     static unsigned long long configured = 0;
     constexpr int smem = I4 ? kExtSmemI4 : kExtSmem;
-    if (ensure_smem_attr(reinterpret_cast<const void *>(attn_extend_kernel<G, I4, WIN>), smem, &configured) != BI_OK)
+    if (ensure_smem_attr(reinterpret_cast<const void *>(attn_extend_kernel<G, I4>), smem, &configured) != BI_OK)
         return BI_ERR_CUDA;
-    return launch_pdl(attn_extend_kernel<G, I4, WIN>, grid, dim3(kExtThreads), smem, s, p);
+    return launch_pdl(attn_extend_kernel<G, I4>, grid, dim3(kExtThreads), smem, s, p);
 }
 
 // K and V (bf16 cache) or c (4-bit cache)
-template <bool I4, bool WIN>
+template <bool I4>
 bi_status launch_extend(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K, const void *V,
                         const KvInt4 &c, const int32_t *table, int32_t max_blocks, int64_t num_blocks,
                         const int32_t *lens, int64_t B, int32_t Hq, int32_t Hkv, int32_t bs, int32_t max_len,
-                        int32_t max_q, float scale, int32_t window, int32_t sinks, void *O, cudaStream_t s) {
+                        int32_t max_q, float scale, void *O, cudaStream_t s) {
     ExtParams p{};
-    p.window = window;
-    p.sinks = sinks;
     p.Q = static_cast<const uint16_t *>(Q);
     p.cu_q = cu_q;
     p.K = static_cast<const uint16_t *>(K);
@@ -1355,10 +1269,10 @@ bi_status launch_extend(const void *Q, const int32_t *cu_q, int32_t total_q, con
     if (ctas_x > 0x7fffffff) return BI_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(ctas_x));
     switch (G) {
-        case 1: return launch_extend_g<1, I4, WIN>(grid, p, s);
-        case 2: return launch_extend_g<2, I4, WIN>(grid, p, s);
-        case 4: return launch_extend_g<4, I4, WIN>(grid, p, s);
-        case 8: return launch_extend_g<8, I4, WIN>(grid, p, s);
+        case 1: return launch_extend_g<1, I4>(grid, p, s);
+        case 2: return launch_extend_g<2, I4>(grid, p, s);
+        case 4: return launch_extend_g<4, I4>(grid, p, s);
+        case 8: return launch_extend_g<8, I4>(grid, p, s);
         default: return BI_ERR_UNSUPPORTED;
     }
 }
@@ -1366,18 +1280,16 @@ bi_status launch_extend(const void *Q, const int32_t *cu_q, int32_t total_q, con
 bi_status launch_attention_extend(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K, const void *V,
                                   const int32_t *table, int32_t max_blocks, int64_t num_blocks, const int32_t *lens,
                                   int64_t B, int32_t Hq, int32_t Hkv, int32_t bs, int32_t max_len, int32_t max_q,
-                                  float scale, int32_t window, int32_t sinks, void *O, cudaStream_t s) {
-    return window > 0 ? launch_extend<false, true>(Q, cu_q, total_q, K, V, KvInt4{}, table, max_blocks, num_blocks, lens, B,
-                                                   Hq, Hkv, bs, max_len, max_q, scale, window, sinks, O, s)
-                      : launch_extend<false, false>(Q, cu_q, total_q, K, V, KvInt4{}, table, max_blocks, num_blocks, lens, B,
-                                                    Hq, Hkv, bs, max_len, max_q, scale, 0, 0, O, s);
+                                  float scale, void *O, cudaStream_t s) {
+    return launch_extend<false>(Q, cu_q, total_q, K, V, KvInt4{}, table, max_blocks, num_blocks, lens, B, Hq, Hkv, bs,
+                                max_len, max_q, scale, O, s);
 }
 
 bi_status launch_attention_extend_int4(const void *Q, const int32_t *cu_q, int32_t total_q, const KvInt4 &c,
                                        const int32_t *table, int32_t max_blocks, const int32_t *lens, int64_t B,
                                        int32_t Hq, int32_t max_len, int32_t max_q, float scale, void *O, cudaStream_t s) {
-    return launch_extend<true, false>(Q, cu_q, total_q, nullptr, nullptr, c, table, max_blocks, c.num_blocks, lens, B, Hq,
-                                      c.Hkv, c.bs, max_len, max_q, scale, 0, 0, O, s);
+    return launch_extend<true>(Q, cu_q, total_q, nullptr, nullptr, c, table, max_blocks, c.num_blocks, lens, B, Hq, c.Hkv,
+                               c.bs, max_len, max_q, scale, O, s);
 }
 
 }  // namespace bi

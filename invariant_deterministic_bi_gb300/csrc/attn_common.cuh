@@ -10,12 +10,37 @@ namespace bi {
 
 constexpr int kD = 128;
 constexpr int kChunk = 128;                    // tokens per chunk: fixed, by position
+constexpr int kRowBytes = kD * 2;              // one token's K (or V) row of one KV head
+constexpr int kTileBytes = kChunk * kRowBytes; // 32 KB
+constexpr int kHalfTile = kChunk * 128;        // one 64-dimension half of a K or V tile (128-byte swizzle)
 // Over the 4-bit cache: the maximum of a chunk of which a row sees no token in
 // the cache (its blocks lie outside). The least number, so that the chunk's sums,
 // which are 0, leave every other chunk's weight as it is, whatever its scores;
 // with -inf its exponentials would be NaN, as they have to be where the scores of
 // tokens in the cache are all -inf (bi_attention_decode gives NaN there).
 constexpr float kNoScore = -0x1.fffffep127f;
+
+// Byte offset of 16-byte piece x (0..15) of token row t in a swizzled K or V tile.
+__device__ __forceinline__ int kv_piece(int t, int x) {
+    return (x >> 3) * kHalfTile + t * 128 + (((x & 7) ^ (t & 7)) << 4);
+}
+
+// Sliding window: a token at position p sees the tokens j <= p with j > p - window
+// or j < sinks. For the earliest of some tokens (its length n, n - window = from)
+// and all after it: first tokens [0, first), then from `lo` on; of the chunks,
+// the `ns` that hold first tokens before lo's chunk c0, then c0 and the rest.
+struct Seen {
+    int first, lo, ns, c0;
+    __device__ __forceinline__ Seen(int from, int sinks) {
+        lo = max(0, from);
+        first = min(sinks, lo);
+        c0 = lo / kChunk;
+        ns = min((first + kChunk - 1) / kChunk, c0);
+    }
+    __device__ __forceinline__ int chunks(int n) const { return ns + (n + kChunk - 1) / kChunk - c0; }
+    __device__ __forceinline__ int start(int i) const { return (i < ns ? i : c0 + i - ns) * kChunk; }   // of the i-th chunk
+    __device__ __forceinline__ bool has(int j) const { return j < first || j >= lo; }
+};
 
 // 16-byte global -> shared copy; src_bytes = 0 writes 16 zero bytes and reads nothing.
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint32_t src_bytes) {

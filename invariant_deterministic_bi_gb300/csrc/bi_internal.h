@@ -136,7 +136,13 @@ bi_status launch_attention_decode(const void *Q, const void *K, const void *V, c
 bi_status launch_attention_extend(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K, const void *V,
                                   const int32_t *table, int32_t max_blocks, int64_t num_blocks, const int32_t *lens,
                                   int64_t B, int32_t Hq, int32_t Hkv, int32_t bs, int32_t max_len, int32_t max_q,
-                                  float scale, int32_t window, int32_t sinks, void *O, cudaStream_t s);
+                                  float scale, void *O, cudaStream_t s);
+bi_status launch_attention_extend_window(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K, const void *V,
+                                         const int32_t *table, int32_t max_blocks, int64_t num_blocks, const int32_t *lens,
+                                         int64_t B, int32_t Hq, int32_t Hkv, int32_t bs, int32_t max_len, int32_t max_q,
+                                         float scale, int32_t window, int32_t sinks, void *O, cudaStream_t s);
+// Tensor maps of a bf16 cache for boxes of whole blocks: tokens a box, 0 without boxes (copy rows).
+int32_t kv_box_maps(const void *K, const void *V, int64_t num_blocks, int32_t bs, int32_t Hkv, CUtensorMap *tmK, CUtensorMap *tmV);
 bi_status launch_kv_int4_append(const KvInt4 &c, const int64_t *slots, const void *K, int64_t ldk, const void *V,
                                 int64_t ldv, int64_t T, cudaStream_t s);
 bi_status launch_kv_int4_read(const KvInt4 &c, const int64_t *slots, void *K, int64_t ldk, void *V, int64_t ldv,
