@@ -333,7 +333,7 @@ bi_status attention_extend(const void *Q, const int32_t *cu_q, int32_t total_q, 
                            const int32_t *block_table, int32_t max_blocks_per_seq, int64_t num_blocks,
                            const int32_t *seq_lens, int64_t B, int32_t Hq, int32_t Hkv, int32_t head_dim,
                            int32_t block_size, int32_t max_seq_len, int32_t max_q_len, float scale, int32_t window,
-                           int32_t sinks, void *O, bi_stream stream) {
+                           int32_t sinks, void *workspace, void *O, bi_stream stream) {
     if (B < 0 || B > 65535 || total_q < 0 || Hq < 1 || Hkv < 1 || block_size < 1 || max_seq_len < 1 ||
         max_seq_len > BI_ATTENTION_MAX_SEQ_LEN || max_q_len < 1 || max_blocks_per_seq < 1 || num_blocks < 1 ||
         !(scale == scale))
@@ -349,9 +349,10 @@ bi_status attention_extend(const void *Q, const int32_t *cu_q, int32_t total_q, 
     bi_status st = require_device();
     if (st != BI_OK) return st;
     if (window > 0)
-        return launch_attention_extend_window(Q, cu_q, total_q, K_cache, V_cache, block_table, max_blocks_per_seq, num_blocks,
-                                              seq_lens, B, Hq, Hkv, block_size, max_seq_len, max_q_len, scale, window, sinks,
-                                              O, as_stream(stream));
+        return launch_attention_extend_window(WindowCall{Q, cu_q, K_cache, V_cache, block_table, seq_lens, O, num_blocks, B,
+                                                         total_q, max_blocks_per_seq, Hq, Hkv, block_size, max_seq_len,
+                                                         max_q_len < total_q ? max_q_len : total_q, window, sinks, scale},
+                                              workspace, as_stream(stream));
     return launch_attention_extend(Q, cu_q, total_q, K_cache, V_cache, block_table, max_blocks_per_seq, num_blocks,
                                    seq_lens, B, Hq, Hkv, block_size, max_seq_len, max_q_len, scale, O, as_stream(stream));
 }
@@ -371,7 +372,7 @@ bi_status bi_attention_extend(const void *Q, const int32_t *cu_q, int32_t total_
                               int32_t head_dim, int32_t block_size, int32_t max_seq_len, int32_t max_q_len, float scale,
                               void *O, bi_stream stream) {
     return attention_extend(Q, cu_q, total_q, K_cache, V_cache, block_table, max_blocks_per_seq, num_blocks, seq_lens, B, Hq,
-                            Hkv, head_dim, block_size, max_seq_len, max_q_len, scale, 0, 0, O, stream);
+                            Hkv, head_dim, block_size, max_seq_len, max_q_len, scale, 0, 0, nullptr, O, stream);
 }
 
 int64_t bi_attention_decode_window_workspace_size(int64_t B, int32_t Hq, int32_t max_seq_len, int32_t window, int32_t sinks) {
@@ -395,7 +396,7 @@ int64_t bi_attention_extend_window_workspace_size(int64_t total_q, int32_t Hq, i
     if (total_q < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || max_q_len < 1 || max_seq_len < 1 ||
         max_seq_len > BI_ATTENTION_MAX_SEQ_LEN || window < 1 || sinks < 0)
         return -1;
-    return 0;
+    return attention_extend_window_workspace_bytes(total_q, Hq, max_seq_len, at_most_max_len(window), at_most_max_len(sinks));
 }
 
 bi_status bi_attention_extend_window(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K_cache,
@@ -406,9 +407,13 @@ bi_status bi_attention_extend_window(const void *Q, const int32_t *cu_q, int32_t
                                      void *O, bi_stream stream) {
     if (window < 1 || sinks < 0 || workspace_bytes < 0) return BI_ERR_INVALID_ARG;
     if (!aligned16(workspace)) return BI_ERR_MISALIGNED;
+    window = at_most_max_len(window), sinks = at_most_max_len(sinks);
+    if (workspace && total_q >= 0 && Hq >= 1 && max_seq_len >= 1 && max_seq_len <= BI_ATTENTION_MAX_SEQ_LEN) {
+        const int64_t need = attention_extend_window_workspace_bytes(total_q, Hq, max_seq_len, window, sinks);
+        if (need <= 0 || workspace_bytes < need) workspace = nullptr;
+    }
     return attention_extend(Q, cu_q, total_q, K_cache, V_cache, block_table, max_blocks_per_seq, num_blocks, seq_lens, B, Hq,
-                            Hkv, head_dim, block_size, max_seq_len, max_q_len, scale, at_most_max_len(window),
-                            at_most_max_len(sinks), O, stream);
+                            Hkv, head_dim, block_size, max_seq_len, max_q_len, scale, window, sinks, workspace, O, stream);
 }
 
 namespace {

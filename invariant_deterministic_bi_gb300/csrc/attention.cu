@@ -123,26 +123,6 @@ constexpr int dec_smem() {
 static_assert(kSlotBytes % 1024 == 0, "slot alignment (128-byte swizzle atoms)");
 static_assert(2 * dec_smem<1, 1>() <= 232448, "two few-item CTAs per SM");
 
-// bar.sync on the named barrier (1 + grp) of consumer group grp's GW warps
-template <int GW>
-__device__ __forceinline__ void group_sync(int grp) {
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * GW) : "memory");
-}
-// the same barrier with an OR vote over the group's threads
-template <int GW>
-__device__ __forceinline__ bool group_sync_or(int grp, bool pred) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, %2, %3, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(static_cast<uint32_t>(pred)), "r"(1 + grp), "n"(32 * GW)
-        : "memory");
-    return r != 0;
-}
-
 // WIN: the windowed form. A sequence's items are the chunks in which its token
 // sees something (record c is the c-th of them); table entries, boxes and rows of
 // tokens out of sight are not read, scores there are -inf, and V rows that came
@@ -605,17 +585,7 @@ __global__ void __launch_bounds__(kCombineThreads)
 attn_combine_kernel(const AttnParams p) {
     grid_dep_wait();      // earlier work of the stream is complete and visible
     grid_dep_launch();
-    // Chunks in tiles of 32. Every thread issues the tile's o loads of its
-    // dimension d at once; meanwhile warp 0 loads the tile's (m_c, l_c), one
-    // chunk per lane: the running maximum before chunk c is a prefix maximum
-    // (exact in any order: a shuffle scan), and chunk c's merge factors
-    // depend only on it and m_c, so each lane computes its chunk's factors.
-    // Then each thread merges its o values in chunk order: the same
-    // operations, in the same order, as a sequential walk over the chunks.
-    constexpr int kTile = 32;
-    __shared__ float fa[kTile];               // alpha of chunk c
-    __shared__ float fb[kTile];               // beta of chunk c
-    __shared__ float fl[kTile];               // l_c
+    __shared__ MergeTile tile;
     const int h = blockIdx.x;
     const int64_t b = blockIdx.y;
     const int d = threadIdx.x;
@@ -623,65 +593,17 @@ attn_combine_kernel(const AttnParams p) {
     // The first tile's loads go out before the sequence length is known: the
     // workspace holds p.chunks records a head, and records past the
     // sequence's chunks are loaded but never used.
-    const int nt0 = min(kTile, p.chunks);
-    float ov0[kTile];
+    const int nt0 = min(kMergeTile, p.chunks);
+    float ov0[kMergeTile];
 #pragma unroll
-    for (int c = 0; c < kTile; ++c) ov0[c] = c < nt0 ? w[static_cast<int64_t>(c) * (kD + 2) + 2 + d] : 0.0f;
+    for (int c = 0; c < kMergeTile; ++c) ov0[c] = c < nt0 ? w[static_cast<int64_t>(c) * (kD + 2) + 2 + d] : 0.0f;
     const float mc0 = d < nt0 ? w[static_cast<int64_t>(d) * (kD + 2)] : -INFINITY;
     const float lc0 = d < nt0 ? w[static_cast<int64_t>(d) * (kD + 2) + 1] : 0.0f;
     int L;
     if (!seq_ok(p, b, L)) return;
     const int nc = WIN ? Seen(L - p.window, p.sinks).chunks(L) : (L + kChunk - 1) / kChunk;
     if (!BI_IN_BOUNDS(nc <= p.chunks, p.status)) return;   // debug build: inside the workspace
-    float o = 0.0f, l = 0.0f, m_run = -INFINITY;           // m_run: warp 0's copy of the running maximum
-    // merge chunks c0 .. c0 + nt - 1 (their o values in ov; (m_c, l_c) of
-    // chunk c0 + d in warp 0's lane d)
-    auto merge_tile = [&](const float (&ov)[kTile], int nt, float mc, float lc) {
-        __syncthreads();                                   // previous tile fully consumed
-        if (d < 32) {
-            mc = d < nt ? mc : -INFINITY;
-            lc = d < nt ? lc : 0.0f;
-            float incl = mc;                               // max(m_c0 .. m_c) over the tile
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const float v = __shfl_up_sync(0xffffffffu, incl, off);
-                if (d >= off) incl = fmaxf(incl, v);
-            }
-            float before = __shfl_up_sync(0xffffffffu, incl, 1);
-            before = d == 0 ? m_run : fmaxf(m_run, before);   // running maximum before chunk c0 + d
-            float mn, a, bt;
-            merge_factors(before, mc, mn, a, bt);
-            if (d < nt) {
-                fa[d] = a;
-                fb[d] = bt;
-                fl[d] = lc;
-            }
-            m_run = fmaxf(m_run, __shfl_sync(0xffffffffu, incl, 31));
-        }
-        __syncthreads();
-#pragma unroll
-        for (int c = 0; c < kTile; ++c) {
-            if (c < nt) {
-                o = merge_value(o, ov[c], fa[c], fb[c]);
-                l = merge_value(l, fl[c], fa[c], fb[c]);
-            }
-        }
-    };
-    merge_tile(ov0, min(kTile, nc), mc0, lc0);
-    for (int c0 = kTile; c0 < nc; c0 += kTile) {
-        const int nt = min(kTile, nc - c0);
-        const float *oc = w + static_cast<int64_t>(c0) * (kD + 2) + 2 + d;
-        float ov[kTile];                                   // in flight while warp 0 prepares the factors
-#pragma unroll
-        for (int c = 0; c < kTile; ++c) ov[c] = c < nt ? oc[static_cast<int64_t>(c) * (kD + 2)] : 0.0f;
-        const float *wc = w + static_cast<int64_t>(c0 + d) * (kD + 2);
-        const float mc = d < nt ? wc[0] : -INFINITY;       // read by warp 0 only
-        const float lc = d < nt ? wc[1] : 0.0f;
-        merge_tile(ov, nt, mc, lc);
-    }
-    const float r = __fdiv_rn(o, l);
-    const uint32_t packed = pack_bf16x2(__float_as_uint(r), 0u);
-    p.O[(b * p.Hq + h) * kD + d] = static_cast<uint16_t>(packed & 0xFFFFu);
+    p.O[(b * p.Hq + h) * kD + d] = merge_records(w, nc, ov0, mc0, lc0, tile);
 }
 
 // ------------------------------------------------------------------ extend
@@ -1124,15 +1046,12 @@ attn_extend_kernel(const ExtParams p) {
 
 }  // namespace
 
-namespace {
-// The most chunks in which a token of at most max_len sees something.
 int64_t seen_chunks(int32_t max_len, int32_t window, int32_t sinks) {
     const int64_t all = (static_cast<int64_t>(max_len) + kChunk - 1) / kChunk;
     if (window == 0) return all;                     // no window
     const int64_t some = (static_cast<int64_t>(window) + kChunk - 2) / kChunk + 1 + (static_cast<int64_t>(sinks) + kChunk - 1) / kChunk;
     return some < all ? some : all;
 }
-}  // namespace
 
 int64_t attention_decode_workspace_bytes(int64_t B, int32_t Hq, int32_t max_len, int32_t window, int32_t sinks) {
     if (B < 0 || Hq < 1 || max_len < 1) return -1;

@@ -32,8 +32,6 @@
 // an SM is busy) and the eight warps' ldmatrix of K and V, then by what surrounds a tile's 18
 // chunks (some 10 of 107 us) and the last round of tiles. Without a window that matters, 4096 tokens over 8192:
 // 1714 us (240 TFLOP/s); attention.cu's kernel 1909.
-#include <type_traits>
-
 #include "attn_common.cuh"
 #include "bi_internal.h"
 
@@ -64,12 +62,11 @@ struct ExtParams {
     uint16_t *O;             // [total_q][Hq][D]
     int64_t num_blocks, batch;
     int32_t total_q, max_blocks, Hq, Hkv, bs, max_len, max_q;
+    int32_t few;             // sequences of at most this many new tokens are computed elsewhere
     int32_t window, sinks, box_rows;
     float scale;
     unsigned *status;
 };
-
-__device__ __forceinline__ bool finite_pair(uint32_t x) { return (x & 0x7F80u) != 0x7F80u && (x & 0x7F800000u) != 0x7F800000u; }
 
 template <int G>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -88,23 +85,31 @@ attn_extend_window_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     volatile int *odd_of = bad_of + kFlagSets;                                          // [kStages]: p.V by tokens
     volatile int *abort_flag = odd_of + kStages;
     __shared__ uint32_t tmem_base;
-    // blockIdx.x = (tile from the last, sequence, KV head): the tiles with the
-    // latest tokens of every sequence start first, so the light ones fill the tail
-    const int64_t per_tile = static_cast<int64_t>(p.batch) * p.Hkv;
+    // blockIdx.x = (tile from the last, KV head): late tokens, which see more, start first. Sequence b's tiles are numbered from cu_q[b] / kTQ + b on, so that there are
+    // no more of them than tokens / kTQ + sequences, whatever the longest: the last b that begins at or before this one, 32 at a time.
     const int g = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.Hkv));
-    const int64_t b = (blockIdx.x / static_cast<unsigned>(p.Hkv)) % p.batch;
-    const int tile = static_cast<int>(gridDim.x / per_tile - 1 - blockIdx.x / per_tile);
+    const int64_t v = (gridDim.x - 1 - blockIdx.x) / static_cast<unsigned>(p.Hkv);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
+    int64_t b = 0;
+    for (int64_t span = p.batch; span > 1;) {
+        const int64_t step = (span + 31) / 32, at = b + lane * step;
+        const bool starts = lane * step < span && (lane == 0 || p.cu_q[at] / kTQ + at <= v);
+        const int last = 31 - __clz(static_cast<int>(__ballot_sync(0xffffffffu, starts)));
+        b += last * step;
+        span = min(step, span - last * step);
+    }
+    const int64_t q0 = p.cu_q[b], q1 = p.cu_q[b + 1], tile = v - (q0 / kTQ + b);
     const int L = p.lens[b];
     const int64_t qlen = q1 - q0;
-    if (q0 < 0 || q1 < q0 || q1 > p.total_q || qlen > p.max_q || L < qlen || L > p.max_len ||
-        L > static_cast<int64_t>(p.max_blocks) * p.bs) {
-        if (tid == 0 && tile == 0 && g == 0) atomicOr(p.status, kDevBadOffsets);
-        return;
-    }
-    const int i0 = tile * kTQ;                         // first query token of this CTA
-    if (i0 >= qlen) return;
+    auto wrong = [&](int64_t x0, int64_t x1, int n) {
+        return x0 < 0 || x1 < x0 || x1 > p.total_q || x1 - x0 > p.max_q || n < x1 - x0 || n > p.max_len ||
+               n > static_cast<int64_t>(p.max_blocks) * p.bs;
+    };
+    if (blockIdx.x == 0)                               // one CTA looks at every sequence
+        for (int64_t x = tid; x < p.batch; x += kThreads)
+            if (wrong(p.cu_q[x], p.cu_q[x + 1], p.lens[x])) atomicOr(p.status, kDevBadOffsets);
+    if (wrong(q0, q1, L) || qlen <= p.few || tile < 0 || tile * kTQ >= qlen) return;
+    const int i0 = static_cast<int>(tile) * kTQ;       // first query token of this CTA
     const int ntok = static_cast<int>(qlen - i0 < kTQ ? qlen - i0 : static_cast<int64_t>(kTQ));
     const int base = L - static_cast<int>(qlen);       // position of query token 0
     const int first_n = base + i0 + 1, last_n = base + i0 + ntok;   // what the first and the last token would see without a window
@@ -604,36 +609,70 @@ bi_status launch_g(const dim3 &grid, const CUtensorMap &tmK, const CUtensorMap &
 
 }  // namespace
 
-bi_status launch_attention_extend_window(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K, const void *V,
-                                         const int32_t *table, int32_t max_blocks, int64_t num_blocks, const int32_t *lens,
-                                         int64_t B, int32_t Hq, int32_t Hkv, int32_t bs, int32_t max_len, int32_t max_q,
-                                         float scale, int32_t window, int32_t sinks, void *O, cudaStream_t s) {
+// The chunk results of the split take at most kFewBytes.
+constexpr int64_t kFewBytes = 512ll << 20;
+
+int64_t attention_extend_window_workspace_bytes(int64_t total_q, int32_t Hq, int32_t max_len, int32_t window, int32_t sinks) {
+    const int64_t bytes = attention_decode_workspace_bytes(total_q, Hq, max_len, window, sinks);
+    return bytes > kFewBytes ? 0 : bytes;
+}
+
+// Which sequences are split over the chunks: all, where that should take less time for the call; else those of at most
+// kFewRows query rows, for which it takes less of an SM's time (a chunk of a tile of 16 rows 1.2 us, of 128 rows 5.3).
+// In us, on the sums that the host knows: drafts 16 x 5 over 4000, window 1024, 80 tiled, 31 split.
+static int32_t few_tokens(const WindowCall &a, int sms) {
+    constexpr int kFewRows = 64;
+    const int G = a.Hq / a.Hkv;
+    const double chunks = static_cast<double>(seen_chunks(a.max_len, a.window, a.sinks));
+    const int64_t rows = static_cast<int64_t>(a.total_q) * G, seqs = (a.total_q + a.max_q - 1) / a.max_q;   // of these at least
+    const int64_t tiles = (rows + kRows - 1) / kRows > seqs ? (rows + kRows - 1) / kRows : seqs;
+    const double tiled = static_cast<double>((tiles * a.Hkv + sms - 1) / sms) * (10.0 + 5.3 * chunks);
+    const double split = 10.0 + static_cast<double>(((rows + 15) / 16 + seqs) * a.Hkv) * chunks * 1.2 / sms;
+    return split < tiled ? a.max_q : kFewRows / G;
+}
+
+bi_status launch_attention_extend_window(const WindowCall &a, void *workspace, cudaStream_t s) {
+    int32_t few = 0;
+    if (workspace) {
+        int dev = 0;
+        const DeviceInfo *info = nullptr;
+        const bi_status st = current_device(&dev, &info);
+        if (st != BI_OK) return st;
+        few = few_tokens(a, info->sm_count);
+        const int32_t most = few < a.max_q ? few : a.max_q;
+        // one sequence of more tokens, or too many results to merge in one launch: the tiled kernel alone
+        if ((a.B == 1 && a.max_q > few) || a.B * most > 0x7fffffff / a.Hq) few = 0;
+        if (few > 0) {
+            const bi_status st2 = launch_attention_few_window(a, few, workspace, s);
+            if (st2 != BI_OK || a.max_q <= few) return st2;
+        }
+    }
     ExtParams p{};
-    p.Q = static_cast<const uint16_t *>(Q);
-    p.cu_q = cu_q;
-    p.K = static_cast<const uint16_t *>(K);
-    p.V = static_cast<const uint16_t *>(V);
-    p.table = table;
-    p.lens = lens;
-    p.O = static_cast<uint16_t *>(O);
-    p.num_blocks = num_blocks;
-    p.batch = B;
-    p.total_q = total_q;
-    p.max_blocks = max_blocks;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.bs = bs;
-    p.max_len = max_len;
-    p.max_q = max_q;
-    p.window = window;
-    p.sinks = sinks;
-    p.scale = scale;
+    p.Q = static_cast<const uint16_t *>(a.Q);
+    p.cu_q = a.cu_q;
+    p.K = static_cast<const uint16_t *>(a.K);
+    p.V = static_cast<const uint16_t *>(a.V);
+    p.table = a.table;
+    p.lens = a.lens;
+    p.O = static_cast<uint16_t *>(a.O);
+    p.num_blocks = a.num_blocks;
+    p.batch = a.B;
+    p.total_q = a.total_q;
+    p.max_blocks = a.max_blocks;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.bs = a.bs;
+    p.max_len = a.max_len;
+    p.max_q = a.max_q;
+    p.few = few;
+    p.window = a.window;
+    p.sinks = a.sinks;
+    p.scale = a.scale;
     p.status = device_status_word();
     CUtensorMap tmK{}, tmV{};
-    p.box_rows = kv_box_maps(K, V, num_blocks, bs, Hkv, &tmK, &tmV);
-    const int G = Hq / Hkv;
-    const int tq = kRows / G;
-    const int64_t ctas = (static_cast<int64_t>(max_q) + tq - 1) / tq * B * Hkv;   // (tile, sequence, KV head)
+    p.box_rows = kv_box_maps(a.K, a.V, a.num_blocks, a.bs, a.Hkv, &tmK, &tmV);
+    const int G = a.Hq / a.Hkv;
+    const int64_t ctas = (a.total_q / (kRows / G) + a.B) * a.Hkv;   // (tile, KV head)
     if (ctas > 0x7fffffff) return BI_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(ctas));
     switch (G) {

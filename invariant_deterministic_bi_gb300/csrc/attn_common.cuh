@@ -3,6 +3,7 @@
 // One definition of each keeps their results the same bits.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 
 #include "bi_ptx.cuh"
 
@@ -95,6 +96,94 @@ __device__ __forceinline__ void merge_factors(float m, float m_c, float &m_new, 
 }
 __device__ __forceinline__ float merge_value(float run, float chunk, float alpha, float beta) {
     return __fmaf_rn(chunk, beta, __fmul_rn(run, alpha));
+}
+
+// bar.sync on the named barrier (1 + grp) of consumer group grp's GW warps
+template <int GW>
+__device__ __forceinline__ void group_sync(int grp) {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * GW) : "memory");
+}
+// the same barrier with an OR vote over the group's threads
+template <int GW>
+__device__ __forceinline__ bool group_sync_or(int grp, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(pred)), "r"(1 + grp), "n"(32 * GW)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ bool finite_pair(uint32_t x) { return (x & 0x7F80u) != 0x7F80u && (x & 0x7F800000u) != 0x7F800000u; }
+
+// The merge of a query row's chunk records (m, l, o[kD]) in chunk order by a CTA
+// of kD threads, one per dimension: the output's bf16 bits. The first tile's values
+// are loaded by the caller: o of dimension threadIdx.x, and (m, l) of record threadIdx.x.
+// Chunks in tiles of 32. Every thread issues the tile's o loads of its
+// dimension d at once; meanwhile warp 0 loads the tile's (m_c, l_c), one
+// chunk per lane: the running maximum before chunk c is a prefix maximum
+// (exact in any order: a shuffle scan), and chunk c's merge factors
+// depend only on it and m_c, so each lane computes its chunk's factors.
+// Then each thread merges its o values in chunk order: the same
+// operations, in the same order, as a sequential walk over the chunks.
+constexpr int kMergeTile = 32;
+struct MergeTile {
+    float fa[kMergeTile], fb[kMergeTile], fl[kMergeTile];   // alpha, beta and l of the tile's chunks
+};
+__device__ __forceinline__ uint16_t merge_records(const float *w, int nc, const float (&first)[kMergeTile], float mc0, float lc0,
+                                                  MergeTile &t) {
+    const int d = threadIdx.x;
+    float o = 0.0f, l = 0.0f, m_run = -INFINITY;           // m_run: warp 0's copy of the running maximum
+    // merge chunks c0 .. c0 + nt - 1 (their o values in ov; (m_c, l_c) of
+    // chunk c0 + d in warp 0's lane d)
+    auto merge_tile = [&](const float (&ov)[kMergeTile], int nt, float mc, float lc) {
+        __syncthreads();                                   // previous tile fully consumed
+        if (d < 32) {
+            mc = d < nt ? mc : -INFINITY;
+            lc = d < nt ? lc : 0.0f;
+            float incl = mc;                               // max(m_c0 .. m_c) over the tile
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float v = __shfl_up_sync(0xffffffffu, incl, off);
+                if (d >= off) incl = fmaxf(incl, v);
+            }
+            float before = __shfl_up_sync(0xffffffffu, incl, 1);
+            before = d == 0 ? m_run : fmaxf(m_run, before);   // running maximum before chunk c0 + d
+            float mn, a, bt;
+            merge_factors(before, mc, mn, a, bt);
+            if (d < nt) {
+                t.fa[d] = a;
+                t.fb[d] = bt;
+                t.fl[d] = lc;
+            }
+            m_run = fmaxf(m_run, __shfl_sync(0xffffffffu, incl, 31));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < kMergeTile; ++c) {
+            if (c < nt) {
+                o = merge_value(o, ov[c], t.fa[c], t.fb[c]);
+                l = merge_value(l, t.fl[c], t.fa[c], t.fb[c]);
+            }
+        }
+    };
+    merge_tile(first, min(kMergeTile, nc), mc0, lc0);
+    for (int c0 = kMergeTile; c0 < nc; c0 += kMergeTile) {
+        const int nt = min(kMergeTile, nc - c0);
+        const float *oc = w + static_cast<int64_t>(c0) * (kD + 2) + 2 + d;
+        float ov[kMergeTile];                                   // in flight while warp 0 prepares the factors
+#pragma unroll
+        for (int c = 0; c < kMergeTile; ++c) ov[c] = c < nt ? oc[static_cast<int64_t>(c) * (kD + 2)] : 0.0f;
+        const float *wc = w + static_cast<int64_t>(c0 + d) * (kD + 2);
+        const float mc = d < nt ? wc[0] : -INFINITY;       // read by warp 0 only
+        const float lc = d < nt ? wc[1] : 0.0f;
+        merge_tile(ov, nt, mc, lc);
+    }
+    return static_cast<uint16_t>(pack_bf16x2(__float_as_uint(__fdiv_rn(o, l)), 0u) & 0xFFFFu);
 }
 
 }  // namespace bi

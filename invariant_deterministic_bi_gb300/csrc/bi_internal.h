@@ -137,10 +137,25 @@ bi_status launch_attention_extend(const void *Q, const int32_t *cu_q, int32_t to
                                   const int32_t *table, int32_t max_blocks, int64_t num_blocks, const int32_t *lens,
                                   int64_t B, int32_t Hq, int32_t Hkv, int32_t bs, int32_t max_len, int32_t max_q,
                                   float scale, void *O, cudaStream_t s);
-bi_status launch_attention_extend_window(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K, const void *V,
-                                         const int32_t *table, int32_t max_blocks, int64_t num_blocks, const int32_t *lens,
-                                         int64_t B, int32_t Hq, int32_t Hkv, int32_t bs, int32_t max_len, int32_t max_q,
-                                         float scale, int32_t window, int32_t sinks, void *O, cudaStream_t s);
+// Arguments of a windowed extend call.
+struct WindowCall {
+    const void *Q;
+    const int32_t *cu_q;
+    const void *K, *V;
+    const int32_t *table, *lens;
+    void *O;
+    int64_t num_blocks, B;
+    int32_t total_q, max_blocks, Hq, Hkv, bs, max_len, max_q, window, sinks;
+    float scale;
+};
+// workspace: null, or attention_extend_window_workspace_bytes() > 0 of them
+bi_status launch_attention_extend_window(const WindowCall &a, void *workspace, cudaStream_t s);
+// The sequences of at most `few` new tokens, split over the cache's chunks.
+bi_status launch_attention_few_window(const WindowCall &a, int32_t few, void *workspace, cudaStream_t s);
+// Bytes the split wants for these sizes; 0: the tiled kernel alone is used; -1: past int64_t.
+int64_t attention_extend_window_workspace_bytes(int64_t total_q, int32_t Hq, int32_t max_len, int32_t window, int32_t sinks);
+// The most chunks in which a token of at most max_len sees something (window 0: none).
+int64_t seen_chunks(int32_t max_len, int32_t window, int32_t sinks);
 // Tensor maps of a bf16 cache for boxes of whole blocks: tokens a box, 0 without boxes (copy rows).
 int32_t kv_box_maps(const void *K, const void *V, int64_t num_blocks, int32_t bs, int32_t Hkv, CUtensorMap *tmK, CUtensorMap *tmV);
 bi_status launch_kv_int4_append(const KvInt4 &c, const int64_t *slots, const void *K, int64_t ldk, const void *V,

@@ -61,6 +61,11 @@ class Case:
         return bi.attention_extend_window(a["Q"], a["cu"], a["K"], a["V"], a["table"], a["lens"], a["max_len"], a["max_q"], SCALE,
                                           W, S, O=a.get("O"), workspace=a.get("ws"))
 
+    def tiled(self, bi, W, S, **kw):
+        """Without room for the split over chunks."""
+        import torch
+        return self.extend(bi, W, S, ws=torch.empty(16, dtype=torch.uint8, device="cuda"), **kw)
+
     def cut(self, bi, W, S, tokens=None, **kw):
         """Every new token (or these) decoded over its cut sequence."""
         import torch
@@ -90,6 +95,7 @@ def test_extend(bi, Hq, Hkv, bs, W, S):
     assert_close_rel(f64_of(got), c.reference(W, S), RTOL, ATOL, f"W={W} S={S}")
     import torch
     assert torch.equal(got, c.cut(bi, W, S))                            # and decode's bits, token by token
+    assert torch.equal(got, c.tiled(bi, W, S))
     assert bi.device_status() == bi.BI_OK
 
 
@@ -104,7 +110,20 @@ def test_a_window_that_holds_everything_changes_no_bit(bi, B):
     c = Case([700, 130, 64], [400, 1, 64], 32, 8, 16, seed=1)
     plain = bi.attention_extend(c.Q, c.cu, c.K, c.V, c.table, c.len_t, c.max_len, 400, SCALE)
     for W, S in ((700, 0), (1 << 31, 7), (1, 700)):
-        assert torch.equal(c.extend(bi, W, S), plain)
+        assert torch.equal(c.extend(bi, W, S), plain) and torch.equal(c.tiled(bi, W, S), plain)
+    assert bi.device_status() == bi.BI_OK
+
+
+@pytest.mark.parametrize("Hq,Hkv,bs", [(8, 2, 16), (4, 4, 24), (16, 2, 64)])
+@pytest.mark.parametrize("W,S", [(200, 5), (1000, 0)])
+def test_prompts_and_single_tokens_in_one_batch(bi, Hq, Hkv, bs, W, S):
+    """Sequences of a few tokens go to the split, the others to the tiles, in one call; a generous most costs nothing."""
+    import torch
+    c = Case([900, 7, 1300, 129, 1, 1000, 64, 300], [700, 1, 900, 3, 1, 0, 64, 17], Hq, Hkv, bs, seed=W)
+    got = c.extend(bi, W, S)
+    assert torch.equal(got, c.tiled(bi, W, S)) and torch.equal(got, c.extend(bi, W, S, max_q=100000))
+    rows = np.concatenate([np.arange(0, 700, 37), np.arange(700, 1700, 61), np.arange(1600, len(got))])
+    assert torch.equal(got[torch.from_numpy(rows).cuda()], c.cut(bi, W, S, tokens=rows))
     assert bi.device_status() == bi.BI_OK
 
 
@@ -160,6 +179,8 @@ def test_what_is_out_of_sight_has_no_effect(bi, value, W, S, bs):
         K, V, table = hide(c, W, S, value)
         call = c.decode if max(q) == 1 else c.extend
         assert torch.equal(call(bi, W, S, K=K, V=V, table=table), call(bi, W, S))
+        if max(q) > 1:
+            assert torch.equal(c.tiled(bi, W, S, K=K, V=V, table=table), c.tiled(bi, W, S))
         assert bi.device_status() == bi.BI_OK
 
 
@@ -179,13 +200,12 @@ def test_values_that_are_not_finite_reach_only_tokens_that_see_them(bi, Hq, Hkv)
         t[c.table_np[b, j // 16], j % 16, h, d] = float(x)
         p = np.arange(c.lens[b] - c.q[b], c.lens[b])
         hit[c.cu_np[b]:c.cu_np[b + 1], h] |= (j <= p) & ((j > p - W) | (j < S))
-    got = c.extend(bi, W, S, K=K, V=V)
-    cut = c.cut(bi, W, S, K=K, V=V)
-    a, b = got.float(), cut.float()
-    assert torch.equal(torch.nan_to_num(a, nan=123.0), torch.nan_to_num(b, nan=123.0))
+    cut = c.cut(bi, W, S, K=K, V=V).float()
     rows = torch.from_numpy(np.repeat(hit, Hq // Hkv, axis=1)).cuda()
-    assert torch.equal(got[~rows], clean[~rows])
-    assert not torch.isfinite(a[rows]).all(-1).any()
+    for got in (c.extend(bi, W, S, K=K, V=V), c.tiled(bi, W, S, K=K, V=V)):
+        assert torch.equal(torch.nan_to_num(got.float(), nan=123.0), torch.nan_to_num(cut, nan=123.0))
+        assert torch.equal(got[~rows], clean[~rows])
+        assert not torch.isfinite(got.float()[rows]).all(-1).any()
     assert bi.device_status() == bi.BI_OK
 
 
@@ -200,6 +220,8 @@ def test_blocks_outside_the_cache(bi, bs):
     for n, (b, i) in enumerate(bad):
         table[b, i] = [-1, 1 << 30, c.K.shape[0]][n % 3]
     got = c.extend(bi, W, S, table=to_dev(table))
+    assert bi.device_status() == bi.BI_ERR_INVALID_ARG
+    assert torch.equal(torch.nan_to_num(c.tiled(bi, W, S, table=to_dev(table)).float(), nan=9.0), torch.nan_to_num(got.float(), nan=9.0))
     assert bi.device_status() == bi.BI_ERR_INVALID_ARG
     old, c.table = c.table, to_dev(table)
     cut = c.cut(bi, W, S)
@@ -236,12 +258,13 @@ def test_sequences_out_of_range_are_left_as_they_were(bi):
     assert torch.equal(O[[0, 3]], want[[0, 3]]) and (O[[1, 2]] == 7.0).all()
     c = Case([300, 200, 100], [20, 30, 5], 8, 2, 16, seed=4)
     want = c.extend(bi, 50, 4)
-    O = torch.full((60, 8, D), 7.0, dtype=torch.bfloat16, device="cuda")
     Q = torch.cat([c.Q, c.Q[:5]])
-    c.extend(bi, 50, 4, Q=Q, O=O, lens=torch.tensor([300, 29, 100], dtype=torch.int32, device="cuda"))
-    assert bi.device_status() == bi.BI_ERR_INVALID_ARG
     keep = torch.tensor(list(range(20)) + list(range(50, 55)), device="cuda")
-    assert torch.equal(O[keep], want[keep]) and (O[20:50] == 7.0).all() and (O[55:] == 7.0).all()   # rows behind the last one stay
+    for call in (c.extend, c.tiled):
+        O = torch.full((60, 8, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        call(bi, 50, 4, Q=Q, O=O, lens=torch.tensor([300, 29, 100], dtype=torch.int32, device="cuda"))
+        assert bi.device_status() == bi.BI_ERR_INVALID_ARG
+        assert torch.equal(O[keep], want[keep]) and (O[20:50] == 7.0).all() and (O[55:] == 7.0).all()   # rows behind the last one stay
 
 
 def test_a_cache_past_2_31(bi):
@@ -256,6 +279,7 @@ def test_a_cache_past_2_31(bi):
     K[blocks - n:], V[blocks - n:] = c.K, c.V
     table = c.table + (blocks - n)
     assert torch.equal(c.extend(bi, 200, 3, K=K, V=V, table=table), c.extend(bi, 200, 3))
+    assert torch.equal(c.tiled(bi, 200, 3, K=K, V=V, table=table), c.extend(bi, 200, 3))
     assert torch.equal(c.cut(bi, 200, 3), c.extend(bi, 200, 3))
     old, c.table = c.table, table
     assert torch.equal(c.cut(bi, 200, 3, K=K, V=V), c.extend(bi, 200, 3, K=K, V=V))

@@ -3,7 +3,9 @@ halves a slot, under random interleavings. A loading warp per slot fills K (with
 q and the row flags), then V, each once the half's "empty" barrier has released
 it; each (half, consumer group) has its own "full" barrier; a group gives K back
 after the scores and V after p.V, and reads the row flags, of which there are two
-sets a slot, until the softmax. Checked: no deadlock, every half and flag set that
+sets a slot, until the softmax. With `handed` (csrc/attention_few.cu) only the
+loading warps find the items: a consumer takes the next one that is handed on with
+K, until one says that there are no more. Checked: no deadlock, every half and flag set that
 is read holds the reader's own item, nothing lands in what is being read. The
 form with one flag set has to break."""
 import random
@@ -13,7 +15,7 @@ import pytest
 from test_barrier_protocols import _Bar
 
 
-def _run(slots, groups, items, seed, flag_sets=2):
+def _run(slots, groups, items, seed, flag_sets=2, handed=False):
     rng = random.Random(seed)
     bars = lambda n: [_Bar(1) for _ in range(n)]
     full = {h: bars(slots * groups) for h in "KV"}
@@ -37,13 +39,23 @@ def _run(slots, groups, items, seed, flag_sets=2):
                 bar_of(h, k).arrive(tx=1)
                 pending.append((h, k % slots, k, bar_of(h, k)))
                 yield
+        if handed:                                       # no more items
+            k = next(k for k in range(items, items + slots) if k % slots == lw)
+            if k >= slots:
+                while not empty["K"][k % slots].try_wait(((k // slots) - 1) & 1):
+                    yield
+            flag_of(k)[k % slots] = "none"
+            bar_of("K", k).arrive()
 
     def consumer(g):
-        for k in range(g, items, groups):
+        for k in range(g, items + slots * groups if handed else items, groups):
             s = k % slots
             for h in "KV":
                 while not bar_of(h, k).try_wait(parity(k)):
                     yield
+                if handed and h == "K" and flag_of(k)[s] == "none":
+                    assert k >= items
+                    return
                 if data[h][s] != k:
                     raise AssertionError(f"item {k}: {h} holds {data[h][s]}")
                 reading[h][s] = k
@@ -82,6 +94,12 @@ def _run(slots, groups, items, seed, flag_sets=2):
 def test_ring_of_halves(slots, groups, items):
     for seed in range(150):
         assert _run(slots, groups, items, seed) == "ok", f"seed={seed}"
+
+
+@pytest.mark.parametrize("items", [0, 1, 2, 3, 4, 5, 6, 7, 13, 40])
+def test_items_handed_on(items):
+    for seed in range(150):
+        assert _run(3, 2, items, seed, handed=True) == "ok", f"seed={seed}"
 
 
 def test_the_model_catches_a_single_flag_set():
