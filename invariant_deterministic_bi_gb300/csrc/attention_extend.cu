@@ -618,8 +618,8 @@ int64_t attention_extend_window_workspace_bytes(int64_t total_q, int32_t Hq, int
 }
 
 // Which sequences are split over the chunks: all, where that should take less time for the call; else those of at most
-// kFewRows query rows, for which it takes less of an SM's time (a chunk of a tile of 16 rows 1.2 us, of 128 rows 5.3).
-// In us, on the sums that the host knows: drafts 16 x 5 over 4000, window 1024, 80 tiled, 31 split.
+// kFewRows query rows, for which it takes less of an SM's time (a chunk of a tile of 16 rows 1.4 us, of 128 rows 5.3).
+// In us, on the sums that the host knows: drafts 16 x 5 over 4000, window 1024, 80 tiled, 40 split.
 static int32_t few_tokens(const WindowCall &a, int sms) {
     constexpr int kFewRows = 64;
     const int G = a.Hq / a.Hkv;
@@ -627,7 +627,7 @@ static int32_t few_tokens(const WindowCall &a, int sms) {
     const int64_t rows = static_cast<int64_t>(a.total_q) * G, seqs = (a.total_q + a.max_q - 1) / a.max_q;   // of these at least
     const int64_t tiles = (rows + kRows - 1) / kRows > seqs ? (rows + kRows - 1) / kRows : seqs;
     const double tiled = static_cast<double>((tiles * a.Hkv + sms - 1) / sms) * (10.0 + 5.3 * chunks);
-    const double split = 10.0 + static_cast<double>(((rows + 15) / 16 + seqs) * a.Hkv) * chunks * 1.2 / sms;
+    const double split = 10.0 + static_cast<double>(((rows + 15) / 16 + seqs) * a.Hkv) * chunks * 1.4 / sms;
     return split < tiled ? a.max_q : kFewRows / G;
 }
 

@@ -16,8 +16,8 @@
 // V holds a value that is not finite out of some token's sight, p.V token by token with
 // zeros there.
 //
-// 16 sequences of 5 drafts over 100 to 4000 tokens, window 1024, 32 heads over 8: 31 us for
-// both kernels (the tiled kernel, one CTA a sequence and KV head: 80).
+// 16 sequences of 5 drafts over 100 to 4000 tokens, window 1024, 32 heads over 8: 40 us for
+// both kernels (the tiled kernel, one CTA a sequence and KV head: 80); 64 single tokens over 4000, 60 (271).
 #include "attn_common.cuh"
 #include "bi_internal.h"
 
@@ -339,7 +339,12 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         // scores of the 16 rows: warp gw takes tokens 8 NT gw .. 8 NT gw + 8 NT - 1, K ascending in 16-dimension steps
         {
             float acc[NT][4] = {};
-            const uint8_t *qa0 = qb + gq * kQStride + 4 * cq, *qa1 = qa0 + 8 * kQStride;
+            uint32_t qa[kD / 16][4];                       // rows gq, gq + 8; dimensions + 0, + 8
+#pragma unroll
+            for (int ks = 0; ks < kD / 16; ++ks)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    qa[ks][i] = *reinterpret_cast<const uint32_t *>(qb + (gq + 8 * (i & 1)) * kQStride + 32 * ks + 16 * (i >> 1) + 4 * cq);
 #pragma unroll
             for (int kp = 0; kp < kD / 32; ++kp) {         // two 16-dimension steps per ldmatrix
                 uint32_t bf[NT][4];
@@ -350,24 +355,31 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 }
 #pragma unroll
                 for (int k2 = 0; k2 < 2; ++k2) {
-                    const int at = 32 * (2 * kp + k2);     // bytes: 16 dimensions a step
-                    const uint32_t a0 = *reinterpret_cast<const uint32_t *>(qa0 + at), a1 = *reinterpret_cast<const uint32_t *>(qa1 + at),
-                                   a2 = *reinterpret_cast<const uint32_t *>(qa0 + at + 16), a3 = *reinterpret_cast<const uint32_t *>(qa1 + at + 16);
+                    const uint32_t(&a)[4] = qa[2 * kp + k2];
 #pragma unroll
-                    for (int nb = 0; nb < NT; ++nb) mma_16816(acc[nb], a0, a1, a2, a3, bf[nb][2 * k2], bf[nb][2 * k2 + 1]);
+                    for (int nb = 0; nb < NT; ++nb) mma_16816(acc[nb], a[0], a[1], a[2], a[3], bf[nb][2 * k2], bf[nb][2 * k2 + 1]);
                 }
             }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = gq + 8 * h, end = end_of(r);
-                if (r >= rows) continue;
+            float *Sw = S + gq * kSStride + gw * 8 * NT + 2 * cq;
+            if (whole) {                                   // (rows that do not exist are written too, and not read)
 #pragma unroll
                 for (int nb = 0; nb < NT; ++nb)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int t = gw * 8 * NT + nb * 8 + 2 * cq + e;
-                        S[r * kSStride + t] = whole || (sees(end, t) && vrow[t]) ? __fmul_rn(acc[nb][2 * h + e], p.scale) : -INFINITY;
-                    }
+                    for (int h = 0; h < 2; ++h)
+                        *reinterpret_cast<float2 *>(Sw + 8 * h * kSStride + 8 * nb) =
+                            make_float2(__fmul_rn(acc[nb][2 * h], p.scale), __fmul_rn(acc[nb][2 * h + 1], p.scale));
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int end = end_of(gq + 8 * h);
+#pragma unroll
+                    for (int nb = 0; nb < NT; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int t = gw * 8 * NT + nb * 8 + 2 * cq + e;
+                            Sw[8 * h * kSStride + 8 * nb + e] = sees(end, t) && vrow[t] ? __fmul_rn(acc[nb][2 * h + e], p.scale) : -INFINITY;
+                        }
+                }
             }
         }
         __syncwarp();
@@ -413,11 +425,15 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
                 for (int y = 0; y < R; ++y) l[y] += __shfl_xor_sync(0xffffffffu, l[y], o);
+            float ml = m[0], ll = l[0];                    // lane y stores row y's
 #pragma unroll
-            for (int y = 0; y < R; ++y) {
-                if (lane != y) continue;
-                float *rec = record(gw + GW * y);
-                if (rec) rec[0] = m[y], rec[1] = l[y];
+            for (int y = 1; y < R; ++y) {
+                ml = lane == y ? m[y] : ml;
+                ll = lane == y ? l[y] : ll;
+            }
+            if (lane < R) {
+                float *rec = record(gw + GW * lane);
+                if (rec) *reinterpret_cast<float2 *>(rec) = make_float2(ml, ll);
             }
         };
         if (rows > GW)
@@ -527,32 +543,33 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     }
 }
 
-// One CTA per (sequence, new token, query head).
+// One CTA per (sequence, `per` new tokens, query head).
 __global__ void __launch_bounds__(kD)
-attn_few_merge_kernel(const FewParams p) {
+attn_few_merge_kernel(const FewParams p, const int per) {
     grid_dep_wait();      // earlier work of the stream is complete and visible
     grid_dep_launch();
     __shared__ MergeTile tile;
-    const int most = min(p.few, p.max_q);
+    const unsigned groups = (min(p.few, p.max_q) + per - 1) / per;
     const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.Hq));
     const unsigned r = blockIdx.x / static_cast<unsigned>(p.Hq);
-    const int64_t b = r / static_cast<unsigned>(most);
-    const int i = static_cast<int>(r % static_cast<unsigned>(most)), d = threadIdx.x;
+    const int64_t b = r / groups;
+    const int i0 = static_cast<int>(r % groups) * per, d = threadIdx.x;
     int64_t q0;
     int L;
     bool bad;
     const int q = sequence(p, b, q0, L, bad);
-    if (i >= q) return;
-    const int n = L - q + i + 1, nc = Seen(n - p.window, p.sinks).chunks(n);
-    if (!BI_IN_BOUNDS(nc <= p.chunks, p.status)) return;
-    const float *w = p.ws + ((q0 + i) * p.Hq + h) * p.chunks * (kD + 2);
-    float ov[kMergeTile];
-    const int nt = min(kMergeTile, nc);
+    for (int i = i0; i < min(q, i0 + per); ++i) {
+        const int n = L - q + i + 1, nc = Seen(n - p.window, p.sinks).chunks(n);
+        if (!BI_IN_BOUNDS(nc <= p.chunks, p.status)) return;
+        const float *w = p.ws + ((q0 + i) * p.Hq + h) * p.chunks * (kD + 2);
+        float ov[kMergeTile];
+        const int nt = min(kMergeTile, nc);
 #pragma unroll
-    for (int c = 0; c < kMergeTile; ++c) ov[c] = c < nt ? w[static_cast<int64_t>(c) * (kD + 2) + 2 + d] : 0.0f;
-    const float mc = d < nt ? w[static_cast<int64_t>(d) * (kD + 2)] : -INFINITY;
-    const float lc = d < nt ? w[static_cast<int64_t>(d) * (kD + 2) + 1] : 0.0f;
-    p.O[((q0 + i) * p.Hq + h) * kD + d] = merge_records(w, nc, ov, mc, lc, tile);
+        for (int c = 0; c < kMergeTile; ++c) ov[c] = c < nt ? w[static_cast<int64_t>(c) * (kD + 2) + 2 + d] : 0.0f;
+        const float mc = d < nt ? w[static_cast<int64_t>(d) * (kD + 2)] : -INFINITY;
+        const float lc = d < nt ? w[static_cast<int64_t>(d) * (kD + 2) + 1] : 0.0f;
+        p.O[((q0 + i) * p.Hq + h) * kD + d] = merge_records(w, nc, ov, mc, lc, tile);
+    }
 }
 
 template <int G>
@@ -605,7 +622,10 @@ bi_status launch_attention_few_window(const WindowCall &a, int32_t few, void *wo
         default: return BI_ERR_UNSUPPORTED;
     }
     if (st != BI_OK) return st;
-    return launch_pdl(attn_few_merge_kernel, dim3(static_cast<unsigned>(a.B * most * a.Hq)), dim3(kD), 0, s, p);
+    // Where single tokens stand among longer sequences, most of the places for tokens are empty: then a CTA takes four
+    // (64 sequences, 16 places each, 32 heads).
+    const int per = a.B * most * a.Hq > 64ll * info->sm_count ? 4 : 1;
+    return launch_pdl(attn_few_merge_kernel, dim3(static_cast<unsigned>(a.B * ((most + per - 1) / per) * a.Hq)), dim3(kD), 0, s, p, per);
 }
 
 }  // namespace bi
