@@ -48,6 +48,7 @@
 // (m, l, o) in registers.
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "attn_common.cuh"
@@ -120,6 +121,11 @@ template <int SLOTS, int NG>
 constexpr int dec_smem() {
     return 1024 + SLOTS * kSlotBytes + 2 * NG * kDecSFloats * 4 + 2 * SLOTS * kChunk + (2 * NG + 2) * SLOTS * 8 + 16;
 }
+// The cluster form: a CTA's chunk records (m, l, o) of up to 8 heads, behind the rest.
+constexpr int kClusterRecords = dec_smem<1, 1>() - 1024;
+constexpr int kClusterSmem = 1024 + kClusterRecords + 8 * (kD + 2) * 4;
+constexpr int kClusterMost = 16;
+static_assert(kClusterRecords % 16 == 0 && 2 * kClusterSmem <= 232448, "two CTAs per SM");
 static_assert(kSlotBytes % 1024 == 0, "slot alignment (128-byte swizzle atoms)");
 static_assert(2 * dec_smem<1, 1>() <= 232448, "two few-item CTAs per SM");
 
@@ -128,12 +134,11 @@ static_assert(2 * dec_smem<1, 1>() <= 232448, "two few-item CTAs per SM");
 // tokens out of sight are not read, scores there are -inf, and V rows that came
 // along are zeroed. A chunk of whose visible tokens none is in the cache counts
 // nothing (kNoScore).
-template <int G, int kSlots, int NG, bool WIN>
-__global__ void __launch_bounds__(dec_threads<kSlots>(), kSlots == 1 ? 2 : 1)
-attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                  const AttnParams p) {
-    grid_dep_wait();      // earlier work of the stream is complete and visible
-    grid_dep_launch();
+// CLUSTER: one item per CTA, a KV head's chunks in one cluster (rank c has record
+// c); the results stay in shared memory.
+template <int G, int kSlots, int NG, bool WIN, bool CLUSTER>
+__device__ __forceinline__ void split_items(const CUtensorMap &tmK, const CUtensorMap &tmV, const AttnParams &p) {
+    static_assert(!CLUSTER || kSlots == 1, "one item per CTA");
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     float *S0 = reinterpret_cast<float *>(smem + kSlots * kSlotBytes);     // [group][2][G][kDecSStride] scores
@@ -193,6 +198,13 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     };
     auto place = [&](int64_t it) {
         Place x;
+        if (CLUSTER) {
+            x.c = static_cast<int>(it % walk);
+            const int64_t r = it / walk;
+            x.g = static_cast<int>(r % p.Hkv);
+            x.b = r / p.Hkv;
+            return x;
+        }
         x.g = static_cast<int>(it % p.Hkv);             // KV head fastest: the heads of one
         const int64_t r = it / p.Hkv;                    // cache block are read together
         x.c = static_cast<int>(r % walk);
@@ -400,7 +412,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     constexpr int DW = kD / GW;                           // value dimensions per warp
     const int grp = warp / GW, gw = warp % GW;
     const int gq = lane >> 2, cq = lane & 3;              // fragment row group, column pair
-    const int64_t ws_head = static_cast<int64_t>(p.chunks) * (kD + 2);   // next query head's record
+    const int64_t ws_head = CLUSTER ? kD + 2 : static_cast<int64_t>(p.chunks) * (kD + 2);   // next query head's record
     int k = 0;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         int64_t b;
@@ -424,7 +436,8 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         const uint16_t *qb = reinterpret_cast<const uint16_t *>(Vs + 2 * kHalfTile);
         const uint8_t *vrow = valid + (((k / kSlots) & 1) * kSlots + slot) * kChunk;
         float *S = S0 + (grp * 2 + ((k / NG) & 1)) * kDecSFloats;
-        float *wsh = p.ws + ((b * p.Hq + g * G) * p.chunks + c) * static_cast<int64_t>(kD + 2);
+        float *wsh = CLUSTER ? reinterpret_cast<float *>(smem + kClusterRecords)
+                             : p.ws + ((b * p.Hq + g * G) * p.chunks + c) * static_cast<int64_t>(kD + 2);
         if (!BI_IN_BOUNDS(b < p.batch && c < p.chunks, p.status)) break;
 
         // scores S[h][t] = q_h . k_t on the tensor cores: A = q (rows = the G
@@ -578,6 +591,61 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         if (lane == 0) mbar_arrive(&emptyV[slot]);        // this warp is done with V
         ++k;
     }
+}
+
+template <int G, int kSlots, int NG, bool WIN>
+__global__ void __launch_bounds__(dec_threads<kSlots>(), kSlots == 1 ? 2 : 1)
+attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const AttnParams p) {
+    grid_dep_wait();      // earlier work of the stream is complete and visible
+    grid_dep_launch();
+    split_items<G, kSlots, NG, WIN, false>(tmK, tmV, p);
+}
+
+// Windowed decode of few sequences in one launch: a cluster has a KV head's
+// chunks, at most 16 (a window of 1024 has ten), and its CTAs merge a share of the outputs each,
+// reading the chunk records from each other's shared memory, by the same operations in the same order as
+// attn_combine_kernel. 1 x 32768 tokens, window 1024, 32 heads over 8: 4.9 us, in two launches 6.6.
+template <int G>
+__global__ void __launch_bounds__(dec_threads<1>(), 2)
+attn_cluster_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
+    grid_dep_wait();      // earlier work of the stream is complete and visible
+    grid_dep_launch();
+    split_items<G, 1, 1, true, true>(tmK, tmV, p);
+    cluster_sync();                                      // every CTA's records are there
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    const uint32_t rec = smem_u32(smem_raw) + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u) + kClusterRecords;
+    const int64_t head = blockIdx.x / static_cast<unsigned>(p.chunks), b = head / p.Hkv;
+    const int g = static_cast<int>(head % p.Hkv), rank = static_cast<int>(cluster_ctarank());
+    int L;
+    if (seq_ok(p, b, L)) {
+        const int nc = Seen(L - p.window, p.sinks).chunks(L);
+        for (int i = rank * dec_threads<1>() + threadIdx.x; i < G * kD; i += p.chunks * dec_threads<1>()) {
+            const int h = i / kD, d = i % kD;
+            float m[kClusterMost], l[kClusterMost], o[kClusterMost];
+#pragma unroll
+            for (int c = 0; c < kClusterMost; ++c) {
+                if (c >= nc || !BI_IN_BOUNDS(nc <= p.chunks, p.status)) break;
+                const uint32_t at = mapa_shared(rec + h * (kD + 2) * 4, c);
+                m[c] = ld_cluster_f32(at);
+                l[c] = ld_cluster_f32(at + 4);
+                o[c] = ld_cluster_f32(at + 8 + 4 * d);
+            }
+            float m_run = -INFINITY, l_run = 0.0f, o_run = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kClusterMost; ++c) {
+                if (c >= nc) break;
+                float mn, al, be;
+                merge_factors(m_run, m[c], mn, al, be);
+                m_run = mn;
+                o_run = merge_value(o_run, o[c], al, be);
+                l_run = merge_value(l_run, l[c], al, be);
+            }
+            p.O[(b * p.Hq + g * G + h) * kD + d] =
+                static_cast<uint16_t>(pack_bf16x2(__float_as_uint(__fdiv_rn(o_run, l_run)), 0u) & 0xFFFFu);
+        }
+    }
+    cluster_sync();                                      // nobody reads this CTA's records any more
 }
 
 template <bool WIN>
@@ -1087,6 +1155,42 @@ bi_status launch_split_shape(const dim3 &grid, const CUtensorMap &tmK, const CUt
         return BI_ERR_CUDA;
     return launch_pdl(attn_split_kernel<G, SLOTS, NG, WIN>, grid, dim3(dec_threads<SLOTS>()), smem, s, tmK, tmV, p);
 }
+// The cluster form for these sizes, if a cluster that large fits the GPU: BI_OK, or BI_ERR_UNSUPPORTED.
+template <int G>
+bi_status launch_cluster(int64_t items, const CUtensorMap &tmK, const CUtensorMap &tmV, const AttnParams &p, cudaStream_t s) {
+    static unsigned long long configured = 0;
+    static std::atomic<signed char> fits[kMaxDevices][kClusterMost + 1];   // 0: not asked yet
+    const void *kernel = reinterpret_cast<const void *>(attn_cluster_kernel<G>);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return BI_ERR_CUDA;
+    if (ensure_smem_attr(kernel, kClusterSmem, &configured) != BI_OK) return BI_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(items));
+    cfg.blockDim = dim3(dec_threads<1>());
+    cfg.dynamicSmemBytes = kClusterSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(p.chunks);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    std::atomic<signed char> &fit = fits[dev][p.chunks];
+    if (fit.load(std::memory_order_acquire) == 0) {
+        int clusters = 0;
+        cfg.numAttrs = 1;
+        const bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                        cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0;
+        cudaGetLastError();
+        fit.store(ok ? 1 : -1, std::memory_order_release);
+    }
+    if (fit.load(std::memory_order_acquire) < 0) return BI_ERR_UNSUPPORTED;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, attn_cluster_kernel<G>, tmK, tmV, p) == cudaSuccess) return BI_OK;
+    cudaGetLastError();
+    return BI_ERR_CUDA;
+}
 // At most two items per SM: one item per CTA, two CTAs per SM; else the ring.
 template <int G, bool WIN>
 bi_status launch_split(int64_t items, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, const AttnParams &p,
@@ -1140,6 +1244,14 @@ bi_status launch_attention_decode(const void *Q, const void *K, const void *V, c
     CUtensorMap tmK{}, tmV{};
     p.box_rows = kv_box_maps(K, V, num_blocks, bs, Hkv, &tmK, &tmV);
     const bool win = window > 0;
+    // Where the items are few and a KV head's chunks fit a cluster, one launch does it all.
+    if (win && p.chunks <= kClusterMost && items <= 2 * static_cast<int64_t>(info->sm_count)) {
+        const bi_status st = G == 1   ? launch_cluster<1>(items, tmK, tmV, p, s)
+                             : G == 2 ? launch_cluster<2>(items, tmK, tmV, p, s)
+                             : G == 4 ? launch_cluster<4>(items, tmK, tmV, p, s)
+                                      : launch_cluster<8>(items, tmK, tmV, p, s);
+        if (st != BI_ERR_UNSUPPORTED) return st;
+    }
     const bi_status st = win ? launch_split_win<true>(G, items, info->sm_count, tmK, tmV, p, s)
                              : launch_split_win<false>(G, items, info->sm_count, tmK, tmV, p, s);
     if (st != BI_OK) return st;

@@ -87,6 +87,23 @@ def test_decode(bi, Hq, Hkv, bs, W, S):
     assert bi.device_status() == bi.BI_OK
 
 
+@pytest.mark.parametrize("B", [1, 3, 40])                               # chunks in clusters, an item a CTA, the ring
+@pytest.mark.parametrize("W,S", [(1920, 0), (1900, 5), (4000, 0), (6000, 300)])
+def test_decode_long(bi, B, W, S):
+    """Sixteen chunks and more (a cluster holds sixteen); the sequences' bits are those of each alone."""
+    import torch
+    c = Case([6000, 4100, 2049][:B] + [130] * (B - 3), [1] * B, 8, 2, 16, seed=W + S)
+    got = c.decode(bi, W, S)
+    for b in range(min(B, 4)):
+        one = c.decode(bi, W, S, Q=c.Q[b:b + 1], table=c.table[b:b + 1].contiguous(), lens=c.len_t[b:b + 1], max_len=c.lens[b])
+        assert torch.equal(one[0], got[b])
+    if B < 40:
+        assert_close_rel(f64_of(got), c.reference(W, S), RTOL, ATOL)
+        cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+        assert torch.equal(got, c.tiled(bi, W, S, cu=cu)) and torch.equal(got, c.extend(bi, W, S, cu=cu))
+    assert bi.device_status() == bi.BI_OK
+
+
 @pytest.mark.parametrize("W,S", WINDOWS)
 @pytest.mark.parametrize("Hq,Hkv,bs", [(8, 2, 16), (8, 1, 24), (4, 4, 128), (6, 3, 64)])
 def test_extend(bi, Hq, Hkv, bs, W, S):
