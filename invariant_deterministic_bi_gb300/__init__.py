@@ -902,6 +902,12 @@ def _attention_window_args(Q, K_cache, V_cache, block_table, seq_lens, workspace
     return shape, cache, table
 
 
+def _most(x) -> int:
+    """A number as 32 bits hold it (what is past them is refused, or counts as the largest)."""
+    x = operator.index(x)
+    return x if 0 <= x < 1 << 31 else -1 if x < 0 else (1 << 31) - 1
+
+
 def _window(window, sinks):
     """Both as 32-bit numbers: anything past the longest sequence counts as that, anything below 0 is refused by the call."""
     window, sinks = operator.index(window), operator.index(sinks)
@@ -912,7 +918,7 @@ def _window(window, sinks):
 
 def attention_decode_window_workspace_size(B: int, Hq: int, max_seq_len: int, window: int, sinks: int = 0) -> int:
     window, sinks = _window(window, sinks)
-    return int(load().bi_attention_decode_window_workspace_size(B, Hq, max_seq_len, window, sinks))
+    return int(load().bi_attention_decode_window_workspace_size(B, Hq, _most(max_seq_len), window, sinks))
 
 
 def attention_decode_window(Q, K_cache, V_cache, block_table, seq_lens, max_seq_len: int, scale: float, window: int,
@@ -933,7 +939,7 @@ def attention_decode_window(Q, K_cache, V_cache, block_table, seq_lens, max_seq_
         O = _out(Q, stream)
     raw = _current_raw_stream(cur) if stream is None else stream.cuda_stream
     st = load().bi_attention_decode_window(Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), block_table.data_ptr(),
-                                           table[1], nblk, seq_lens.data_ptr(), B, Hq, Hkv, D, bs, max_seq_len, scale, window,
+                                           table[1], nblk, seq_lens.data_ptr(), B, Hq, Hkv, D, bs, _most(max_seq_len), scale, window,
                                            sinks, workspace.data_ptr(), workspace.numel(), O.data_ptr(), raw)
     if st:
         raise BiError(st, "bi_attention_decode_window")
@@ -943,7 +949,7 @@ def attention_decode_window(Q, K_cache, V_cache, block_table, seq_lens, max_seq_
 def attention_extend_window_workspace_size(total_q: int, Hq: int, Hkv: int, max_seq_len: int, max_q_len: int, window: int,
                                            sinks: int = 0) -> int:
     window, sinks = _window(window, sinks)
-    return int(load().bi_attention_extend_window_workspace_size(total_q, Hq, Hkv, max_seq_len, max_q_len, window, sinks))
+    return int(load().bi_attention_extend_window_workspace_size(total_q, Hq, Hkv, _most(max_seq_len), _most(max_q_len), window, sinks))
 
 
 def attention_extend_window(Q, cu_q, K_cache, V_cache, block_table, seq_lens, max_seq_len: int, max_q_len: int, scale: float,
@@ -967,7 +973,7 @@ def attention_extend_window(Q, cu_q, K_cache, V_cache, block_table, seq_lens, ma
     raw = _current_raw_stream(cur) if stream is None else stream.cuda_stream
     st = load().bi_attention_extend_window(Q.data_ptr(), cu_q.data_ptr(), T, K_cache.data_ptr(), V_cache.data_ptr(),
                                            block_table.data_ptr(), table[1], nblk, seq_lens.data_ptr(), B, Hq, Hkv, D, bs,
-                                           max_seq_len, max_q_len, scale, window, sinks,
+                                           _most(max_seq_len), _most(max_q_len), scale, window, sinks,
                                            workspace.data_ptr() if workspace is not None else None,
                                            workspace.numel() if workspace is not None else 0, O.data_ptr(), raw)
     if st:

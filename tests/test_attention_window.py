@@ -332,6 +332,40 @@ def test_captured_on_streams_and_with_workspaces(bi):
     assert torch.equal(got, want) and bi.device_status() == bi.BI_OK
 
 
+def test_two_streams_and_a_capture_that_forks(bi):
+    """Calls of both forms on two streams at once, with their own workspaces, eager and from a captured graph."""
+    import torch
+    W, S = 180, 3
+    cases = [Case([700, 50, 1300], [1, 1, 1], 8, 2, 16, seed=1), Case([900, 400, 64], [300, 5, 1], 8, 2, 16, seed=2)]
+    want = [cases[0].decode(bi, W, S), cases[1].extend(bi, W, S)]
+    sizes = [bi.attention_decode_window_workspace_size(3, 8, 1300, W, S), bi.attention_extend_window_workspace_size(306, 8, 2, 900, 300, W, S)]
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+    outs = [torch.zeros_like(w) for w in want]
+    side = [torch.cuda.Stream() for _ in range(2)]
+
+    def both():
+        here = torch.cuda.current_stream()
+        for s, call, c, w, o in zip(side, (Case.decode, Case.extend), cases, ws, outs):
+            s.wait_stream(here)
+            with torch.cuda.stream(s):
+                for _ in range(3):
+                    call(c, bi, W, S, ws=w, O=o)
+            here.wait_stream(s)
+
+    both()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        both()
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert bi.device_status() == bi.BI_OK
+
+
 def test_from_projection_to_attention(bi):
     """A model's layer as it is served: projection, append with norms and rotation, attention; a prompt in two chunks, then
     single tokens, against the plain form of the whole in 64 bits."""
@@ -392,6 +426,11 @@ def test_refusals(bi):
         assert bi.attention_decode_window_workspace_size(2, 8, 64, W, S) == -1 == bi.attention_extend_window_workspace_size(2, 8, 2, 64, 1, W, S)
     with pytest.raises(TypeError):
         c.decode(bi, 5.0, 0)
+    for n in (0, -1, (1 << 30) + 1, 1 << 31, (1 << 32) + 64):
+        for call in (c.decode, c.extend):
+            with pytest.raises(bi.BiError):
+                call(bi, 5, 0, max_len=n)
+    assert torch.equal(c.extend(bi, 5, 0, max_q=(1 << 32) + 1), c.extend(bi, 5, 0))
     with pytest.raises(ValueError):
         c.decode(bi, 5, 0, V=c.V[:2])
     with pytest.raises(ValueError):
