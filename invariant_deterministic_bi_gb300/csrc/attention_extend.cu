@@ -330,6 +330,9 @@ attn_extend_window_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     };
 
     constexpr int kTokens = 16 / G;                    // of this warp's rows
+    const f2 scale2 = f2_of(p.scale, p.scale);
+    auto pair = [](const float (&x)[4], int h) { return f2_of(x[2 * h], x[2 * h + 1]); };
+    auto unpair = [](f2 v, float (&x)[4], int h) { x[2 * h] = __uint_as_float(lo_of(v)), x[2 * h + 1] = __uint_as_float(hi_of(v)); };
     // scores q . k of the tile's 16 rows and a chunk's 128 tokens, dimensions ascending in
     // 16-dimension steps. s[nt][e]: row ra (e < 2) or rb, token 8 nt + 2 cq + (e & 1).
     float s[kChunk / 8][4];
@@ -433,9 +436,12 @@ attn_extend_window_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
             tmem_ld_32x32b_x32(o_run + 32 * i, run);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                const int nt = 8 * i + k / 4, e = k % 4;
-                if (in[e >> 1]) run[k] = __float_as_uint(merge_value(__uint_as_float(run[k]), acc[nt][e], al[e >> 1], be[e >> 1]));
+            for (int k = 0; k < 32; k += 2) {              // (merge_value, two dimensions at once)
+                const int nt = 8 * i + k / 4, h = (k >> 1) & 1;
+                if (in[h]) {
+                    const f2 x = fma2(pair(acc[nt], h), f2_of(be[h], be[h]), mul2(f2_of(run[k], run[k + 1]), f2_of(al[h], al[h])));
+                    run[k] = lo_of(x), run[k + 1] = hi_of(x);
+                }
             }
             tmem_st_32x32b_x16(o_run + 32 * i, run, 0);
             tmem_st_32x32b_x16(o_run + 32 * i + 16, run, 16);
@@ -469,9 +475,9 @@ attn_extend_window_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
 #pragma unroll
                 for (int nt = 0; nt < kChunk / 8; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s[nt][e] = __fmul_rn(s[nt][e], p.scale);
-                        m[e >> 1] = fmaxf(m[e >> 1], s[nt][e]);
+                    for (int h = 0; h < 2; ++h) {
+                        unpair(mul2(pair(s[nt], h), scale2), s[nt], h);
+                        m[h] = fmaxf(m[h], fmaxf(s[nt][2 * h], s[nt][2 * h + 1]));
                     }
             } else {
                 int any[2] = {0, 0};
@@ -501,10 +507,15 @@ attn_extend_window_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                 m[h] = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], 2));
             }
             if (whole) {
+                const f2 minus[2] = {f2_of(-m[0], -m[0]), f2_of(-m[1], -m[1])};
 #pragma unroll
                 for (int nt = 0; nt < kChunk / 8; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[nt][e] = expf(s[nt][e] - m[e >> 1]);
+                    for (int h = 0; h < 2; ++h) {
+                        unpair(add2(pair(s[nt], h), minus[h]), s[nt], h);
+                        s[nt][2 * h] = expf(s[nt][2 * h]);
+                        s[nt][2 * h + 1] = expf(s[nt][2 * h + 1]);
+                    }
             } else {
 #pragma unroll
                 for (int nt = 0; nt < kChunk / 8; ++nt)
@@ -523,22 +534,19 @@ attn_extend_window_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
             // so every lane's total is the same bits as decode's.
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float x[2];
+                f2 col[4];                                                    // both e & 1 at once
+#pragma unroll
+                for (int n4 = 0; n4 < 4; ++n4) {
+                    col[n4] = pair(s[n4], h);
+#pragma unroll
+                    for (int k = 1; k < 4; ++k) col[n4] = add2(col[n4], pair(s[n4 + 4 * k], h));
+                }
+                const f2 v = add2(add2(col[0], col[2]), add2(col[1], col[3]));   // steps 16 and 8
+                float x[2] = {__uint_as_float(lo_of(v)), __uint_as_float(hi_of(v))};
 #pragma unroll
                 for (int e0 = 0; e0 < 2; ++e0) {
-                    float col[4];
-#pragma unroll
-                    for (int n4 = 0; n4 < 4; ++n4) {
-                        float sum = s[n4][2 * h + e0];
-#pragma unroll
-                        for (int k = 1; k < 4; ++k) sum += s[n4 + 4 * k][2 * h + e0];
-                        col[n4] = sum;
-                    }
-                    const float u0 = col[0] + col[2], u1 = col[1] + col[3];   // step 16
-                    float v = u0 + u1;                                        // step 8
-                    v += __shfl_xor_sync(0xffffffffu, v, 2);                  // step 4
-                    v += __shfl_xor_sync(0xffffffffu, v, 1);                  // step 2
-                    x[e0] = v;
+                    x[e0] += __shfl_xor_sync(0xffffffffu, x[e0], 2);          // step 4
+                    x[e0] += __shfl_xor_sync(0xffffffffu, x[e0], 1);          // step 2
                 }
                 l[h] = x[0] + x[1];                                           // step 1
             }

@@ -410,4 +410,26 @@ __device__ __forceinline__ void st_global_v4(void *p, uint32_t a, uint32_t b, ui
     asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// Two fp32 numbers in a register pair, for the packed instructions.
+using f2 = uint64_t;
+__device__ __forceinline__ f2 f2_of(uint32_t lo, uint32_t hi) { return lo | static_cast<uint64_t>(hi) << 32; }
+__device__ __forceinline__ f2 f2_of(float lo, float hi) { return f2_of(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ uint32_t lo_of(f2 x) { return static_cast<uint32_t>(x); }
+__device__ __forceinline__ uint32_t hi_of(f2 x) { return static_cast<uint32_t>(x >> 32); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 }  // namespace bi

@@ -36,22 +36,6 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kDepth = 4;    // groups of heads a warp has on the way (2: 29.8 us, 3: 28.1, 6: 28.6; in registers, one ahead: 34.9)
 
-// Two fp32 numbers in a register pair, for the packed instructions.
-using f2 = uint64_t;
-__device__ __forceinline__ f2 f2_of(uint32_t lo, uint32_t hi) { return lo | static_cast<uint64_t>(hi) << 32; }
-__device__ __forceinline__ f2 f2_of(float lo, float hi) { return f2_of(__float_as_uint(lo), __float_as_uint(hi)); }
-__device__ __forceinline__ uint32_t lo_of(f2 x) { return static_cast<uint32_t>(x); }
-__device__ __forceinline__ uint32_t hi_of(f2 x) { return static_cast<uint32_t>(x >> 32); }
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
 constexpr f2 kMinus2 = 0x8000000080000000ull;          // (xor: both negated)
 
 // A lane's two vectors of a row: the eight pairs (a_k, b_k) as packed a and b (interleaved, a vector holds four of them).
