@@ -85,11 +85,15 @@ attn_extend_window_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     volatile int *odd_of = bad_of + kFlagSets;                                          // [kStages]: p.V by tokens
     volatile int *abort_flag = odd_of + kStages;
     __shared__ uint32_t tmem_base;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (warp == kThreads / 32 - 1) {                   // beside the others' search for the tile
+        tmem_alloc(&tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
     // blockIdx.x = (tile from the last, KV head): late tokens, which see more, start first. Sequence b's tiles are numbered from cu_q[b] / kTQ + b on, so that there are
     // no more of them than tokens / kTQ + sequences, whatever the longest: the last b that begins at or before this one, 32 at a time.
     const int g = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.Hkv));
     const int64_t v = (gridDim.x - 1 - blockIdx.x) / static_cast<unsigned>(p.Hkv);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int64_t b = 0;
     for (int64_t span = p.batch; span > 1;) {
         const int64_t step = (span + 31) / 32, at = b + lane * step;
@@ -108,7 +112,13 @@ attn_extend_window_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     if (blockIdx.x == 0)                               // one CTA looks at every sequence
         for (int64_t x = tid; x < p.batch; x += kThreads)
             if (wrong(p.cu_q[x], p.cu_q[x + 1], p.lens[x])) atomicOr(p.status, kDevBadOffsets);
-    if (wrong(q0, q1, L) || qlen <= p.few || tile < 0 || tile * kTQ >= qlen) return;
+    if (wrong(q0, q1, L) || qlen <= p.few || tile < 0 || tile * kTQ >= qlen) {
+        tc_fence_before();
+        __syncthreads();                               // (the allocation has been written)
+        tc_fence_after();
+        if (warp == kThreads / 32 - 1) tmem_dealloc(tmem_base, kTmemCols);
+        return;
+    }
     const int i0 = static_cast<int>(tile) * kTQ;       // first query token of this CTA
     const int ntok = static_cast<int>(qlen - i0 < kTQ ? qlen - i0 : static_cast<int64_t>(kTQ));
     const int base = L - static_cast<int>(qlen);       // position of query token 0
@@ -138,10 +148,6 @@ attn_extend_window_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                         v ? p.Q + ((q0 + i0 + r / G) * p.Hq + g * G + r % G) * kD + x * 8 : p.Q, v ? 16u : 0u);
         }
         cp_async_commit();
-        if (warp == 0) {
-            tmem_alloc(&tmem_base, kTmemCols);
-            tmem_relinquish();
-        }
     }
     tc_fence_before();
     __syncthreads();
@@ -480,51 +486,52 @@ attn_extend_window_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                         m[h] = fmaxf(m[h], fmaxf(s[nt][2 * h], s[nt][2 * h + 1]));
                     }
             } else {
-                int any[2] = {0, 0};
+                // what a row does not see scores -inf, so p = 0 there
 #pragma unroll
                 for (int nt = 0; nt < kChunk / 8; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int t = nt * 8 + 2 * cq + (e & 1);
-                        const bool v = sees(e >> 1, t) && in_cache[t];
-                        any[e >> 1] |= v;
-                        s[nt][e] = v ? __fmul_rn(s[nt][e], p.scale) : -INFINITY;
-                        m[e >> 1] = fmaxf(m[e >> 1], s[nt][e]);
+                        s[nt][e] = sees(e >> 1, t) ? __fmul_rn(s[nt][e], p.scale) : -INFINITY;
                     }
-                // a chunk counts nothing for a row that sees no token of it in the cache
+                if (bad) {                                 // a row of the chunk is not in the cache
+                    int any[2] = {0, 0};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    any[h] |= __shfl_xor_sync(0xffffffffu, any[h], 1);
-                    any[h] |= __shfl_xor_sync(0xffffffffu, any[h], 2);
-                    if (!any[h]) m[h] = kNoScore;
+                    for (int nt = 0; nt < kChunk / 8; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int t = nt * 8 + 2 * cq + (e & 1);
+                            any[e >> 1] |= sees(e >> 1, t) && in_cache[t];
+                            if (!in_cache[t]) s[nt][e] = -INFINITY;
+                        }
+                    // the chunk counts nothing for a token that sees no row of it in the cache
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        any[h] |= __shfl_xor_sync(0xffffffffu, any[h], 1);
+                        any[h] |= __shfl_xor_sync(0xffffffffu, any[h], 2);
+                        if (!any[h]) m[h] = kNoScore;
+                    }
                 }
+#pragma unroll
+                for (int nt = 0; nt < kChunk / 8; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m[e >> 1] = fmaxf(m[e >> 1], s[nt][e]);
             }
-            // per row: max (any order gives the same value), then e^(s - m) for the
-            // tokens it sees (0 for the others: e^-inf, or masked where every score is)
+            // per row: max (any order gives the same value), then e^(s - m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 m[h] = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], 1));
                 m[h] = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], 2));
             }
-            if (whole) {
-                const f2 minus[2] = {f2_of(-m[0], -m[0]), f2_of(-m[1], -m[1])};
+            const f2 minus[2] = {f2_of(-m[0], -m[0]), f2_of(-m[1], -m[1])};
 #pragma unroll
-                for (int nt = 0; nt < kChunk / 8; ++nt)
+            for (int nt = 0; nt < kChunk / 8; ++nt)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        unpair(add2(pair(s[nt], h), minus[h]), s[nt], h);
-                        s[nt][2 * h] = expf(s[nt][2 * h]);
-                        s[nt][2 * h + 1] = expf(s[nt][2 * h + 1]);
-                    }
-            } else {
-#pragma unroll
-                for (int nt = 0; nt < kChunk / 8; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int t = nt * 8 + 2 * cq + (e & 1);
-                        s[nt][e] = sees(e >> 1, t) ? expf(s[nt][e] - m[e >> 1]) : 0.0f;
-                    }
-            }
+                for (int h = 0; h < 2; ++h) {
+                    unpair(add2(pair(s[nt], h), minus[h]), s[nt], h);
+                    s[nt][2 * h] = expf(s[nt][2 * h]);
+                    s[nt][2 * h + 1] = expf(s[nt][2 * h + 1]);
+                }
             // per row: the sum in decode's order. Lane L of decode sums tokens
             // L, L + 32, L + 64, L + 96 in turn, then a butterfly over lanes xor
             // 16, 8, 4, 2, 1. Here L = 8 (nt % 4) + 2 cq + (e & 1): the column
@@ -578,16 +585,37 @@ attn_extend_window_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
         uint32_t run[32];
         tmem_ld_32x32b_x32(o_run + 32 * i, run);
         tmem_wait_ld();
+        // a row's quad has two dimensions of each tile in every lane: turned round, a lane has all eight of tiles cq, 4 + cq
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = h ? rb : ra;
-            if (dead || r / G >= ntok || !BI_IN_BOUNDS(q0 + i0 + r / G < p.total_q, p.status)) continue;
-            uint16_t *orow = p.O + ((q0 + i0 + r / G) * p.Hq + g * G + r % G) * kD + 2 * cq + 64 * i;
+            const bool stored = !dead && r / G < ntok && BI_IN_BOUNDS(q0 + i0 + r / G < p.total_q, p.status);
+            uint16_t *orow = p.O + ((q0 + i0 + r / G) * p.Hq + g * G + r % G) * kD + 64 * i;
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                const float x0 = __fdiv_rn(__uint_as_float(run[4 * nt + 2 * h]), l_run[h]);
-                const float x1 = __fdiv_rn(__uint_as_float(run[4 * nt + 2 * h + 1]), l_run[h]);
-                *reinterpret_cast<uint32_t *>(orow + nt * 8) = pack_bf16x2(__float_as_uint(x0), __float_as_uint(x1));
+            for (int four = 0; four < 2; ++four) {
+                uint32_t x[4], y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int at = 16 * four + 4 * k + 2 * h;
+                    x[k] = pack_bf16x2(__float_as_uint(__fdiv_rn(__uint_as_float(run[at]), l_run[h])),
+                                       __float_as_uint(__fdiv_rn(__uint_as_float(run[at + 1]), l_run[h])));
+                }
+                // lane cq gives tile k to lane k: exchanges with lanes cq ^ 1, then cq ^ 2
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, cq & 1 ? x[k] : x[k + 1], 1);
+                    y[k] = cq & 1 ? got : x[k];
+                    y[k + 1] = cq & 1 ? x[k + 1] : got;
+                }
+                // y[k], y[k + 1]: tile k + (cq & 1) of lanes cq & ~1 and cq | 1
+                uint32_t lo[2], hi[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, cq & 2 ? y[k] : y[2 + k], 2);
+                    lo[k] = cq & 2 ? got : y[k];
+                    hi[k] = cq & 2 ? y[2 + k] : got;
+                }
+                if (stored) *reinterpret_cast<uint4 *>(orow + 32 * four + 8 * cq) = make_uint4(lo[0], lo[1], hi[0], hi[1]);
             }
         }
         __syncwarp();
