@@ -676,8 +676,9 @@ bi_status launch_attention_extend_window(const WindowCall &a, void *workspace, c
         if (st != BI_OK) return st;
         few = few_tokens(a, info->sm_count);
         const int32_t most = few < a.max_q ? few : a.max_q;
-        // one sequence of more tokens, or too many results to merge in one launch: the tiled kernel alone
-        if ((a.B == 1 && a.max_q > few) || a.B * most > 0x7fffffff / a.Hq) few = 0;
+        // mostly sequences of more tokens (a sequence of few has a tile of its own then; without any, the split's two launches
+        // would cost 7 us for nothing), or too many results to merge in one launch: the tiled kernel alone
+        if ((a.max_q > few && (a.B == 1 || a.total_q > 4 * a.B * few)) || a.B * most > 0x7fffffff / a.Hq) few = 0;
         if (few > 0) {
             const bi_status st2 = launch_attention_few_window(a, few, workspace, s);
             if (st2 != BI_OK || a.max_q <= few) return st2;
