@@ -660,11 +660,12 @@ static int32_t few_tokens(const WindowCall &a, int sms) {
     constexpr int kFewRows = 64;
     const int G = a.Hq / a.Hkv;
     const double chunks = static_cast<double>(seen_chunks(a.max_len, a.window, a.sinks));
-    const int64_t rows = static_cast<int64_t>(a.total_q) * G, seqs = (a.total_q + a.max_q - 1) / a.max_q;   // of these at least
+    const int64_t rows = static_cast<int64_t>(a.total_q) * G, seqs = a.B < a.total_q ? a.B : a.total_q;
     const int64_t tiles = (rows + kRows - 1) / kRows > seqs ? (rows + kRows - 1) / kRows : seqs;
     const double tiled = static_cast<double>((tiles * a.Hkv + sms - 1) / sms) * (10.0 + 5.3 * chunks);
     const double split = 10.0 + static_cast<double>(((rows + 15) / 16 + seqs) * a.Hkv) * chunks * 1.4 / sms;
-    return split < tiled ? a.max_q : kFewRows / G;
+    // (the split lays its work out for the most new tokens of every sequence: not where most of that would be empty)
+    return split < tiled && a.B * a.max_q <= 4 * static_cast<int64_t>(a.total_q) ? a.max_q : kFewRows / G;
 }
 
 bi_status launch_attention_extend_window(const WindowCall &a, void *workspace, cudaStream_t s) {
