@@ -271,19 +271,22 @@ attn_extend_window_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                     __syncwarp();
                     break;
                 }
+                // (rows that every token sees need neither)
+                const int every = first_n - j0, from = last_n - p.window - j0;
                 bool fine = true;
 #pragma unroll 4
                 for (int i = 0; i < kChunk / 2; ++i) {
-                        const int t = 2 * i + (lane >> 4);
-                        const uint32_t a = smem_u32(Vs) + kv_piece(t, lane & 15);
-                        if (t < n && !(t >= h0 && t < h1)) {
-                            uint32_t x0, x1, x2, x3;
-                            ld_shared_v4(a, x0, x1, x2, x3);
-                            fine = fine && finite_pair(x0) && finite_pair(x1) && finite_pair(x2) && finite_pair(x3);
-                        } else {
-                            st_shared_v4(a, 0u, 0u, 0u, 0u);
-                        }
+                    const int t = 2 * i + (lane >> 4);
+                    if (t < every && (t < p.sinks - j0 || t >= from)) continue;
+                    const uint32_t a = smem_u32(Vs) + kv_piece(t, lane & 15);
+                    if (t < n && !(t >= h0 && t < h1)) {
+                        uint32_t x0, x1, x2, x3;
+                        ld_shared_v4(a, x0, x1, x2, x3);
+                        fine = fine && finite_pair(x0) && finite_pair(x1) && finite_pair(x2) && finite_pair(x3);
+                    } else {
+                        st_shared_v4(a, 0u, 0u, 0u, 0u);
                     }
+                }
                 fence_proxy_async_smem();              // before later bulk copies into these rows
                 fine = __all_sync(0xffffffffu, fine);
                 if (lane == 0) odd_of[s] = !fine;
