@@ -13,8 +13,8 @@
 // counted on "full" barriers and given back, K and V apart, on "empty" ones. Eight
 // warps of 16 rows compute, each at its own pace: no barrier of all warps stands
 // between two chunks, so one warp's softmax and merge run under the other's products on
-// the same scheduler (1 x 4096 tokens over 8192, window 2000: 744 us; when the two had
-// to take turns on the tensor pipe 817, and with barriers between the chunks, as
+// the same scheduler (1 x 4096 tokens over 8192, window 2000: 744 us when this was measured; with
+// the two taking turns on the tensor pipe 817, and with barriers between the chunks, as
 // in the kernel without a window, 859). A warp goes from p.V of a chunk straight to q.k of the next.
 // Scores, p and a chunk's sums are in registers; the running outputs, 64 a thread, are
 // in tensor memory and fetched to merge a chunk. Twelve warps of 160 registers were
@@ -28,10 +28,10 @@
 // value, p.V runs once for every token of a warp's rows, with zeros for the tokens
 // out of that one's sight.
 //
-// Bound by mma.sync (1.5 times the operations, for p in two parts: 62 % of its pipe while
-// an SM is busy) and the eight warps' ldmatrix of K and V, then by what surrounds a tile's 18
-// chunks (some 10 of 107 us) and the last round of tiles. Without a window that matters, 4096 tokens over 8192:
-// 1714 us (240 TFLOP/s); attention.cu's kernel 1909.
+// Bound by mma.sync (1.5 times the operations, for p in two parts: some 62 % of its pipe
+// while an SM is busy) and the eight warps' ldmatrix of K and V, then by a tile's start
+// (6600 cycles of 80000 for five chunks) and the last round of tiles. 4096 tokens over 8192: window 2000
+// 694 us (195 TFLOP/s); without a window that matters 1661 (248), attention.cu's kernel 1909.
 #include "attn_common.cuh"
 #include "bi_internal.h"
 

@@ -27,7 +27,7 @@
 // words of eight codes takes 1408 of them, their scales 256, mma.sync 192, softmax,
 // transposes, stores and the walk the rest, on pipes that overlap only partly (a
 // word and a product: 21.6-24.7 cycles per warp and scheduler, 17 and 8 apart). Measured (GB300): 64 x 4096, 32 heads over 8
-// 91 us, 3.3 TB/s (bf16 cache: 187 us); 1 x 4096 10.1 us (9.9); 2 x 131072, 64 over
+// 91 us, 3.3 TB/s (bf16 cache: 172 us); 1 x 4096 10.1 us (9.4); 2 x 131072, 64 over
 // 8 heads 102 us; 16 sequences x 5 new tokens over 100..4000 58 us. Per warp two 9 KB
 // buffers and 12 warps; 16 warps with three 4.5 KB buffers each took 102 us (the
 // pipes, not the latencies, are what a warp waits for); reading the codes from
