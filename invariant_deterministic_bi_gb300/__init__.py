@@ -117,8 +117,22 @@ def load() -> ctypes.CDLL:
         for name in ("bi_attention_extend_int4_workspace_size", "bi_attention_decode_window_workspace_size",
                      "bi_attention_extend_window_workspace_size"):
             getattr(lib, name).restype = ctypes.c_int64
+        _bind_torch()
         _lib = lib
         return lib
+
+
+# What the calls over heads and the windowed ones use of torch, bound once by load(): where a call takes a few
+# microseconds, looking them up is a tenth of it.
+_bfloat16 = _int64 = _int32 = _uint8 = _empty_like = _current_device = _raw_stream = None
+
+
+def _bind_torch():
+    global _bfloat16, _int64, _int32, _uint8, _empty_like, _current_device, _raw_stream
+    import torch
+    _bfloat16, _int64, _int32, _uint8, _empty_like = torch.bfloat16, torch.int64, torch.int32, torch.uint8, torch.empty_like
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def status_string(status: int) -> str:
@@ -733,12 +747,6 @@ def rope_freqs(rotary_dim: int, base: float = 10000.0, interleaved: bool = False
 
 # A call's checks are a good part of its time where it is short, so each of the following looks at a tensor once and
 # leaves the wording of what is wrong to _refuse.
-def _current_device() -> int:
-    import torch
-    get = getattr(torch._C, "_cuda_getDevice", None)
-    return get() if get is not None else torch.cuda.current_device()
-
-
 def _refuse(t, dtype, name, cur, what):
     """Raises what is wrong with a tensor that should be contiguous, of this type and on this device, else ValueError(what)."""
     _typed(t, dtype, name, contiguous=False)
@@ -759,28 +767,26 @@ def _tensor(t, dtype, shape, name, cur):
 
 def _heads(t, name, cur, T=-1, D=-1, H=-1):
     """(T, heads, D, token stride) of bf16 heads [T, H, D] that are contiguous within a token (-1: any size)."""
-    import torch
     try:
         (t_, h, d), (st, sh, sd) = t.shape, t.stride()
-        if (t.dtype is torch.bfloat16 and t.get_device() == cur and (T < 0 or (t_ == T and d == D)) and (H < 0 or h == H) and
+        if (t.dtype is _bfloat16 and t.get_device() == cur and (T < 0 or (t_ == T and d == D)) and (H < 0 or h == H) and
                 ((sd == 1 and (sh == d or h == 1)) or not t_ * h)):
             return t_, h, d, st if t_ > 1 else h * d
     except (AttributeError, TypeError, ValueError):
         pass                                             # not a tensor, or not of three dimensions
     sizes = ", ".join(n if v < 0 else str(v) for n, v in (("T", T), ("heads", H), ("head_dim", D)))
-    _refuse(t, torch.bfloat16, name, cur, f"[{sizes}], the heads of a token contiguous (a token stride is allowed)")
+    _refuse(t, _bfloat16, name, cur, f"[{sizes}], the heads of a token contiguous (a token stride is allowed)")
 
 
 def _rope_args(positions, freqs, T, cur):
     """Pointers of the positions and the rotation, both or neither given."""
-    import torch
     if freqs is None:
         if positions is not None:
             raise ValueError("positions without freqs")
         return None, None
     if not isinstance(freqs, RopeFreqs):
         raise TypeError("freqs must be a RopeFreqs")
-    _tensor(positions, torch.int64, (T,), "positions", cur)
+    _tensor(positions, _int64, (T,), "positions", cur)
     if freqs.turns.get_device() != cur:
         raise ValueError(f"freqs must be on the current device cuda:{cur}, they are on {freqs.turns.device}")
     return positions.data_ptr(), freqs._ref
@@ -788,14 +794,14 @@ def _rope_args(positions, freqs, T, cur):
 
 def _out(like, stream):
     """A new tensor of a checked tensor's shape and type, contiguous, for a call on `stream`."""
-    import torch
-    return torch.empty_like(like) if stream is None else _new(like.shape, like.dtype, like, stream)
+    return _empty_like(like) if stream is None else _new(like.shape, like.dtype, like, stream)
 
 
 def rope(X, positions, freqs: RopeFreqs, Y=None, stream=None):
     """Rotary positions: Y[t, h] = X[t, h] turned by positions[t].
 
     X bf16 [T, H, head_dim] (a token stride is allowed); positions int64 [T]. Y may be X (in place)."""
+    call = load()
     cur = _current_device()
     T, H, D, ldx = _heads(X, "X", cur)
     if freqs is None:
@@ -805,8 +811,8 @@ def rope(X, positions, freqs: RopeFreqs, Y=None, stream=None):
         Y, ldy = _out(X, stream), H * D
     else:
         ldy = _heads(Y, "Y", cur, T, D, H)[3]
-    raw = _current_raw_stream(cur) if stream is None else stream.cuda_stream
-    st = load().bi_rope(X.data_ptr(), ldx, pos, T, H, D, c, Y.data_ptr(), ldy, raw)
+    raw = _raw_stream(cur) if stream is None else stream.cuda_stream
+    st = call.bi_rope(X.data_ptr(), ldx, pos, T, H, D, c, Y.data_ptr(), ldy, raw)
     if st:
         raise BiError(st, "bi_rope")
     return Y
@@ -817,12 +823,12 @@ def qk_norm_rope(Q, K, q_weight, k_weight, eps: float, positions=None, freqs=Non
 
     Q bf16 [T, Hq, head_dim], K [T, Hkv, head_dim] (token strides allowed); weights bf16 [head_dim];
     positions int64 [T]; freqs None: the norms alone. Q_out may be Q and K_out K (in place)."""
-    import torch
+    call = load()
     cur = _current_device()
     T, Hq, D, ldq = _heads(Q, "Q", cur)
     _, Hkv, _, ldk = _heads(K, "K", cur, T, D)
-    _tensor(q_weight, torch.bfloat16, (D,), "q_weight", cur)
-    _tensor(k_weight, torch.bfloat16, (D,), "k_weight", cur)
+    _tensor(q_weight, _bfloat16, (D,), "q_weight", cur)
+    _tensor(k_weight, _bfloat16, (D,), "k_weight", cur)
     pos, c = _rope_args(positions, freqs, T, cur)
     if Q_out is None:
         Q_out, ldqo = _out(Q, stream), Hq * D
@@ -832,8 +838,8 @@ def qk_norm_rope(Q, K, q_weight, k_weight, eps: float, positions=None, freqs=Non
         K_out, ldko = _out(K, stream), Hkv * D
     else:
         ldko = _heads(K_out, "K_out", cur, T, D, Hkv)[3]
-    raw = _current_raw_stream(cur) if stream is None else stream.cuda_stream
-    st = load().bi_qk_norm_rope(Q.data_ptr(), ldq, K.data_ptr(), ldk, q_weight.data_ptr(), k_weight.data_ptr(), eps, pos, T,
+    raw = _raw_stream(cur) if stream is None else stream.cuda_stream
+    st = call.bi_qk_norm_rope(Q.data_ptr(), ldq, K.data_ptr(), ldk, q_weight.data_ptr(), k_weight.data_ptr(), eps, pos, T,
                                 Hq, Hkv, D, c, Q_out.data_ptr(), ldqo, K_out.data_ptr(), ldko, raw)
     if st:
         raise BiError(st, "bi_qk_norm_rope")
@@ -848,23 +854,23 @@ def kv_append(K, V, slots, K_cache, V_cache, positions=None, freqs=None, k_weigh
     K, V bf16 [T, Hkv, head_dim] and Q [T, Hq, head_dim] (token strides allowed: slices of a fused projection);
     slots int64 [T]: block * block_size + offset, -1 to store nothing for a token (its query is computed all the
     same). The slots of one call must differ. K_cache, V_cache bf16 [blocks, block_size, Hkv, head_dim]. Q_out may be Q."""
-    import torch
+    call = load()
     cur = _current_device()
     T, Hkv, D, ldk = _heads(K, "K", cur)
     ldv = _heads(V, "V", cur, T, D, Hkv)[3]
-    _tensor(slots, torch.int64, (T,), "slots", cur)
-    _tensor(K_cache, torch.bfloat16, None, "K_cache", cur)
+    _tensor(slots, _int64, (T,), "slots", cur)
+    _tensor(K_cache, _bfloat16, None, "K_cache", cur)
     shape = K_cache.shape
     if len(shape) != 4 or shape[2] != Hkv or shape[3] != D:
         raise ValueError(f"K_cache must be [blocks, block_size, {Hkv}, {D}], got {tuple(shape)}")
-    _tensor(V_cache, torch.bfloat16, shape, "V_cache", cur)
+    _tensor(V_cache, _bfloat16, shape, "V_cache", cur)
     if k_weight is not None:
-        _tensor(k_weight, torch.bfloat16, (D,), "k_weight", cur)
+        _tensor(k_weight, _bfloat16, (D,), "k_weight", cur)
     pos, c = _rope_args(positions, freqs, T, cur)
     if Q is not None:
         _, Hq, _, ldq = _heads(Q, "Q", cur, T, D)
         if q_weight is not None:
-            _tensor(q_weight, torch.bfloat16, (D,), "q_weight", cur)
+            _tensor(q_weight, _bfloat16, (D,), "q_weight", cur)
         if Q_out is None:
             Q_out, ldqo = _out(Q, stream), Hq * D
         else:
@@ -874,8 +880,8 @@ def kv_append(K, V, slots, K_cache, V_cache, positions=None, freqs=None, k_weigh
         raise ValueError("q_weight and Q_out belong to Q")
     else:
         queries = None, 0, None, 0, None, 0
-    raw = _current_raw_stream(cur) if stream is None else stream.cuda_stream
-    st = load().bi_kv_append(K.data_ptr(), ldk, V.data_ptr(), ldv, T, slots.data_ptr(),
+    raw = _raw_stream(cur) if stream is None else stream.cuda_stream
+    st = call.bi_kv_append(K.data_ptr(), ldk, V.data_ptr(), ldv, T, slots.data_ptr(),
                              None if k_weight is None else k_weight.data_ptr(), eps, pos, c, K_cache.data_ptr(),
                              V_cache.data_ptr(), shape[0], Hkv, D, shape[1], *queries, raw)
     if st:
@@ -885,20 +891,19 @@ def kv_append(K, V, slots, K_cache, V_cache, positions=None, freqs=None, k_weigh
 
 def _attention_window_args(Q, K_cache, V_cache, block_table, seq_lens, workspace, O, cur):
     """Checks shared by the windowed calls: Q's and the cache's shapes, the rows of the table."""
-    import torch
-    _tensor(Q, torch.bfloat16, None, "Q", cur)
-    _tensor(K_cache, torch.bfloat16, None, "K_cache", cur)
-    _tensor(block_table, torch.int32, None, "block_table", cur)
+    _tensor(Q, _bfloat16, None, "Q", cur)
+    _tensor(K_cache, _bfloat16, None, "K_cache", cur)
+    _tensor(block_table, _int32, None, "block_table", cur)
     shape, cache, table = Q.shape, K_cache.shape, block_table.shape
     if len(shape) != 3 or shape[2] != 128 or len(cache) != 4 or cache[3] != 128 or len(table) != 2:
         raise ValueError(f"Q must be [tokens, Hq, 128], K_cache [blocks, block_size, Hkv, 128], block_table [B, max_blocks]; got "
                          f"{tuple(shape)}, {tuple(cache)}, {tuple(table)}")
-    _tensor(V_cache, torch.bfloat16, cache, "V_cache", cur)
-    _tensor(seq_lens, torch.int32, (table[0],), "seq_lens", cur)
+    _tensor(V_cache, _bfloat16, cache, "V_cache", cur)
+    _tensor(seq_lens, _int32, (table[0],), "seq_lens", cur)
     if workspace is not None:
-        _tensor(workspace, torch.uint8, None, "workspace", cur)
+        _tensor(workspace, _uint8, None, "workspace", cur)
     if O is not None:
-        _tensor(O, torch.bfloat16, shape, "O", cur)
+        _tensor(O, _bfloat16, shape, "O", cur)
     return shape, cache, table
 
 
@@ -927,18 +932,18 @@ def attention_decode_window(Q, K_cache, V_cache, block_table, seq_lens, max_seq_
 
     Table entries of blocks out of sight may be anything (-1 once given back). The workspace (uint8,
     ``attention_decode_window_workspace_size`` bytes) is allocated with torch if not given."""
-    import torch
+    call = load()
     cur = _current_device()
     (B, Hq, D), (nblk, bs, Hkv, _), table = _attention_window_args(Q, K_cache, V_cache, block_table, seq_lens, workspace, O, cur)
     if table[0] != B:
         raise ValueError("one query token a sequence: block_table must be [B, max_blocks], B the rows of Q")
     window, sinks = _window(window, sinks)
     if workspace is None:
-        workspace = _new(max(attention_decode_window_workspace_size(B, Hq, max_seq_len, window, sinks), 16), torch.uint8, Q, stream)
+        workspace = _new(max(attention_decode_window_workspace_size(B, Hq, max_seq_len, window, sinks), 16), _uint8, Q, stream)
     if O is None:
         O = _out(Q, stream)
-    raw = _current_raw_stream(cur) if stream is None else stream.cuda_stream
-    st = load().bi_attention_decode_window(Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), block_table.data_ptr(),
+    raw = _raw_stream(cur) if stream is None else stream.cuda_stream
+    st = call.bi_attention_decode_window(Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), block_table.data_ptr(),
                                            table[1], nblk, seq_lens.data_ptr(), B, Hq, Hkv, D, bs, _most(max_seq_len), scale, window,
                                            sinks, workspace.data_ptr(), workspace.numel(), O.data_ptr(), raw)
     if st:
@@ -959,19 +964,19 @@ def attention_extend_window(Q, cu_q, K_cache, V_cache, block_table, seq_lens, ma
 
     Table entries of blocks out of every new token's sight may be anything. The workspace (uint8,
     ``attention_extend_window_workspace_size`` bytes) is allocated with torch if not given."""
-    import torch
+    call = load()
     cur = _current_device()
     (T, Hq, D), (nblk, bs, Hkv, _), table = _attention_window_args(Q, K_cache, V_cache, block_table, seq_lens, workspace, O, cur)
     B = table[0]
-    _tensor(cu_q, torch.int32, (B + 1,), "cu_q", cur)
+    _tensor(cu_q, _int32, (B + 1,), "cu_q", cur)
     window, sinks = _window(window, sinks)
     if workspace is None:
         need = attention_extend_window_workspace_size(T, Hq, Hkv, max_seq_len, max_q_len, window, sinks)
-        workspace = _new(need, torch.uint8, Q, stream) if need > 0 else None
+        workspace = _new(need, _uint8, Q, stream) if need > 0 else None
     if O is None:
         O = _out(Q, stream)
-    raw = _current_raw_stream(cur) if stream is None else stream.cuda_stream
-    st = load().bi_attention_extend_window(Q.data_ptr(), cu_q.data_ptr(), T, K_cache.data_ptr(), V_cache.data_ptr(),
+    raw = _raw_stream(cur) if stream is None else stream.cuda_stream
+    st = call.bi_attention_extend_window(Q.data_ptr(), cu_q.data_ptr(), T, K_cache.data_ptr(), V_cache.data_ptr(),
                                            block_table.data_ptr(), table[1], nblk, seq_lens.data_ptr(), B, Hq, Hkv, D, bs,
                                            _most(max_seq_len), _most(max_q_len), scale, window, sinks,
                                            workspace.data_ptr() if workspace is not None else None,
