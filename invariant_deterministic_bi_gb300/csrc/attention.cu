@@ -606,7 +606,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 // chunks, at most 16 (a window of 1024 has ten), and its CTAs merge a share of the outputs each,
 // reading the chunk records from each other's shared memory, by the same operations in the same order as
 // attn_combine_kernel. 1 x 32768 tokens, window 1024, 32 heads over 8: 6.9 us
-// on the device (6.7 in two launches), a call from Python 14.2 us (16.7).
+// on the device (6.7 in two launches), and a launch less for the host (2.5 us of a call).
 template <int G>
 __global__ void __launch_bounds__(dec_threads<1>(), 2)
 attn_cluster_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p) {

@@ -90,8 +90,9 @@ attn_extend_window_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
         tmem_alloc(&tmem_base, kTmemCols);
         tmem_relinquish();
     }
-    // blockIdx.x = (tile from the last, KV head): late tokens, which see more, start first. Sequence b's tiles are numbered from cu_q[b] / kTQ + b on, so that there are
-    // no more of them than tokens / kTQ + sequences, whatever the longest: the last b that begins at or before this one, 32 at a time.
+    // blockIdx.x = (tile from the last, KV head): late tokens, which see more, start first. Sequence b's tiles are
+    // numbered from cu_q[b] / kTQ + b on, so that there are no more of them than tokens / kTQ + sequences, whatever
+    // the longest: the last b that begins at or before this one, 32 at a time.
     const int g = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.Hkv));
     const int64_t v = (gridDim.x - 1 - blockIdx.x) / static_cast<unsigned>(p.Hkv);
     int64_t b = 0;

@@ -263,7 +263,8 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     mbar_arrive(bar);
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
                 };
-                for (int y = lane; y < rows * 16; y += 32) cp_async_16(smem_u32(qs) + (y >> 4) * kQStride + (y & 15) * 16, q_row(y >> 4) + (y & 15) * 8, 16u);
+                for (int y = lane; y < rows * 16; y += 32)
+                    cp_async_16(smem_u32(qs) + (y >> 4) * kQStride + (y & 15) * 16, q_row(y >> 4) + (y & 15) * 8, 16u);
                 copy(Ks, p.K, fb);
                 last = k;
                 if (!freed(&emptyV[slot])) break;
