@@ -2,19 +2,19 @@
 // tokens (drafts to verify, single tokens in a batch with prompts): split over
 // the cache's chunks like decode, with the same bits.
 //
-// An item is (sequence, tile of 16 / G new tokens, KV head, chunk in which one of
-// them sees something); its 16 query rows are the tokens' G heads, and each row masks
+// An item is (sequence, tile of 16 / G or 32 / G new tokens, KV head, chunk in which one
+// of them sees something); its 16 or 32 query rows are the tokens' G heads, and each row masks
 // what is out of its own token's sight. The kernel is decode's ring
-// (attention.cu): one CTA per SM walks the items, three loading warps fill three
-// slots, K and V halves apart, two groups of four warps compute. A row's chunk
+// (attention.cu): one CTA per SM walks the items, three (two, for 32 rows) loading warps fill as
+// many slots, K and V halves apart, two groups of four warps compute. A row's chunk
 // results go to the workspace where decode of its cut sequence would put them,
 // record by record; attn_few_merge_kernel merges them in chunk order.
 //
-// Differences from decode: 16 rows in the products instead of 8; one score buffer a
-// group instead of two (a barrier after p is read takes the second one's place);
-// no L2 policy, since a sequence's other tiles read the same chunks; and where
-// V holds a value that is not finite out of some token's sight, p.V token by token with
-// zeros there.
+// Differences from decode: one score buffer a group instead of two (the next item's barrier
+// comes before it is written again); p is split into bf16 hi and lo once, by the softmax, and
+// read with ldmatrix (split by each warp as it reads: 381 us where this takes 357); no L2 policy, since a sequence's
+// other tiles read the same chunks; and where V holds a value that is not finite out of
+// some token's sight, p.V token by token with zeros there.
 //
 // 16 sequences of 5 drafts over 100 to 4000 tokens, window 1024, 32 heads over 8: 40 us for
 // both kernels (the tiled kernel, one CTA a sequence and KV head: 80); 64 single tokens over 4000, 60 (271).
@@ -25,14 +25,21 @@ namespace bi {
 namespace {
 
 constexpr int kConsumers = 8;                  // warps, in two groups
-constexpr int kSlots = 3, NG = 2;
-constexpr int kThreads = 32 * (kConsumers + kSlots);
+constexpr int NG = 2;
 constexpr int kQStride = kRowBytes + 16;       // q rows 16 bytes apart more than they are long: no bank conflicts
-constexpr int kSlot = 4 * kHalfTile + 5 * 1024;   // K, V, 16 q rows (a multiple of the swizzle's 1024)
 constexpr int kSStride = kChunk + 8;           // scores of one row (padded)
-constexpr int kSFloats = 16 * kSStride;
-constexpr int kSmem = 1024 + kSlots * kSlot + NG * kSFloats * 4 + 2 * kSlots * (kChunk + 32) + (2 * NG + 2) * kSlots * 8 + 16;
-static_assert(16 * kQStride <= 5 * 1024 && kSmem <= 232448, "one CTA's shared memory");
+
+// Shared memory and threads of the kernel for items of 16 MT rows: what fits, three slots or two.
+template <int MT>
+struct Shape {
+    static constexpr int kSlots = MT == 1 ? 3 : 2;
+    static constexpr int kThreads = 32 * (kConsumers + kSlots);
+    static constexpr int kSlot = 4 * kHalfTile + (16 * MT * kQStride + 1023) / 1024 * 1024;   // K, V, q rows (the swizzle's 1024)
+    static constexpr int kSFloats = 16 * MT * kSStride;
+    static constexpr int kSmem = 1024 + kSlots * kSlot + NG * kSFloats * 4 + 2 * kSlots * (kChunk + 32) + (2 * NG + 2) * kSlots * 8 + 16;
+    static constexpr int kTurn = kSlots % NG == 0 ? kSlots : kSlots * NG;   // items until a slot meets the same group again
+    static_assert(kSmem <= 232448, "one CTA's shared memory");
+};
 
 struct FewParams {
     const uint16_t *Q;       // [total_q][Hq][D]
@@ -60,15 +67,16 @@ __device__ __forceinline__ int sequence(const FewParams &p, int64_t b, int64_t &
     return !bad && q <= p.few ? static_cast<int>(q) : 0;
 }
 
-template <int G>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int G, int MT>
+__global__ void __launch_bounds__(Shape<MT>::kThreads, 1)
 attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const FewParams p) {
-    constexpr int TQ = 16 / G;                             // tokens a tile
+    constexpr int ROWS = 16 * MT, TQ = ROWS / G;           // query rows and tokens a tile
+    constexpr int kSlots = Shape<MT>::kSlots, kSlot = Shape<MT>::kSlot, kTurn = Shape<MT>::kTurn, kSFloats = Shape<MT>::kSFloats;
     grid_dep_wait();      // earlier work of the stream is complete and visible
     grid_dep_launch();
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    float *S0 = reinterpret_cast<float *>(smem + kSlots * kSlot);                 // [group][16][kSStride] scores
+    float *S0 = reinterpret_cast<float *>(smem + kSlots * kSlot);                 // [group][ROWS][kSStride] scores
     uint8_t *valid = reinterpret_cast<uint8_t *>(S0 + NG * kSFloats);             // [2][kSlots][kChunk]: row has K/V
     int *what = reinterpret_cast<int *>(valid + 2 * kSlots * kChunk);             // [2][kSlots][8]: the item (Item)
     // barriers and flag sets as in attn_split_kernel; the items are found by the loading warps alone, which hand them on with K
@@ -93,7 +101,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         fence_mbar_init();
     }
     __syncthreads();
-    for (int64_t b = tid; b < p.batch; b += kThreads) {
+    for (int64_t b = tid; b < p.batch; b += Shape<MT>::kThreads) {
         int64_t q0;
         int L;
         bool bad;
@@ -273,6 +281,9 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             lastV = k;
             ++k;
         }
+        // the copies of this warp's last item must land before the CTA exits (K's wait comes first: the item below
+        // may be counted on the same barrier)
+        if (last >= 0) mbar_wait(&full[(last % kSlots) * NG + last % NG], (last / kTurn) & 1, nullptr);
         // one more item says that there are none: the group that comes to this slot next stops (the wait is that of any item)
         if (!gave_up) {
             while (k % kSlots != lw) ++k;
@@ -288,9 +299,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 *abort_flag = 1;
             }
         }
-        // the copies of this warp's last item must land before the CTA exits
-        if (last >= 0) mbar_wait(&full[(last % kSlots) * NG + last % NG], (last / (kSlots * NG)) & 1, nullptr);
-        if (lastV >= 0) mbar_wait(&fullV[(lastV % kSlots) * NG + lastV % NG], (lastV / (kSlots * NG)) & 1, nullptr);
+        if (lastV >= 0) mbar_wait(&fullV[(lastV % kSlots) * NG + lastV % NG], (lastV / kTurn) & 1, nullptr);
         return;
     }
 
@@ -311,7 +320,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             }
             return true;
         };
-        if (stop(mbar_wait(&full[slot * NG + grp], (k / (kSlots * NG)) & 1, abort_flag))) break;
+        if (stop(mbar_wait(&full[slot * NG + grp], (k / kTurn) & 1, abort_flag))) break;
         const uint8_t *Ks = smem + slot * kSlot, *Vs = Ks + 2 * kHalfTile, *qb = Vs + 2 * kHalfTile;
         const uint8_t *vrow = valid + (((k / kSlots) & 1) * kSlots + slot) * kChunk;
         const int4 *w = reinterpret_cast<const int4 *>(what + (((k / kSlots) & 1) * kSlots + slot) * 8);
@@ -337,15 +346,17 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         const bool masked = x.j0 + kChunk > x.first_n || (x.j0 < last_n - p.window && x.j0 + kChunk > p.sinks);
         const bool whole = __all_sync(0xffffffffu, reinterpret_cast<const uint32_t *>(vrow)[lane] == 0x01010101u) && !masked;
 
-        // scores of the 16 rows: warp gw takes tokens 8 NT gw .. 8 NT gw + 8 NT - 1, K ascending in 16-dimension steps
+        // scores of the rows: warp gw takes tokens 8 NT gw .. 8 NT gw + 8 NT - 1, K ascending in 16-dimension steps
         {
-            float acc[NT][4] = {};
-            uint32_t qa[kD / 16][4];                       // rows gq, gq + 8; dimensions + 0, + 8
+            float acc[MT][NT][4] = {};
+            uint32_t qa[MT][kD / 16][4];                   // rows gq, gq + 8; dimensions + 0, + 8
 #pragma unroll
-            for (int ks = 0; ks < kD / 16; ++ks)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    qa[ks][i] = *reinterpret_cast<const uint32_t *>(qb + (gq + 8 * (i & 1)) * kQStride + 32 * ks + 16 * (i >> 1) + 4 * cq);
+                for (int ks = 0; ks < kD / 16; ++ks) {
+                    uint32_t(&a)[4] = qa[mt][ks];
+                    ldmatrix_x4(a[0], a[1], a[2], a[3], smem_u32(qb + (16 * mt + (lane & 15)) * kQStride + 32 * ks + 16 * (lane >> 4)));
+                }
 #pragma unroll
             for (int kp = 0; kp < kD / 32; ++kp) {         // two 16-dimension steps per ldmatrix
                 uint32_t bf[NT][4];
@@ -355,30 +366,34 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     ldmatrix_x4(bf[nb][0], bf[nb][1], bf[nb][2], bf[nb][3], smem_u32(Ks + kv_piece(t, 4 * kp + (lane >> 3))));
                 }
 #pragma unroll
-                for (int k2 = 0; k2 < 2; ++k2) {
-                    const uint32_t(&a)[4] = qa[2 * kp + k2];
+                for (int k2 = 0; k2 < 2; ++k2)
 #pragma unroll
-                    for (int nb = 0; nb < NT; ++nb) mma_16816(acc[nb], a[0], a[1], a[2], a[3], bf[nb][2 * k2], bf[nb][2 * k2 + 1]);
-                }
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const uint32_t(&a)[4] = qa[mt][2 * kp + k2];
+#pragma unroll
+                        for (int nb = 0; nb < NT; ++nb) mma_16816(acc[mt][nb], a[0], a[1], a[2], a[3], bf[nb][2 * k2], bf[nb][2 * k2 + 1]);
+                    }
             }
             float *Sw = S + gq * kSStride + gw * 8 * NT + 2 * cq;
             if (whole) {                                   // (rows that do not exist are written too, and not read)
 #pragma unroll
-                for (int nb = 0; nb < NT; ++nb)
+                for (int h = 0; h < 2 * MT; ++h)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        *reinterpret_cast<float2 *>(Sw + 8 * h * kSStride + 8 * nb) =
-                            make_float2(__fmul_rn(acc[nb][2 * h], p.scale), __fmul_rn(acc[nb][2 * h + 1], p.scale));
+                    for (int nb = 0; nb < NT; ++nb) {
+                        const float *v = acc[h >> 1][nb] + 2 * (h & 1);
+                        *reinterpret_cast<float2 *>(Sw + 8 * h * kSStride + 8 * nb) = make_float2(__fmul_rn(v[0], p.scale), __fmul_rn(v[1], p.scale));
+                    }
             } else {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < 2 * MT; ++h) {
                     const int end = end_of(gq + 8 * h);
 #pragma unroll
                     for (int nb = 0; nb < NT; ++nb)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int t = gw * 8 * NT + nb * 8 + 2 * cq + e;
-                            Sw[8 * h * kSStride + 8 * nb + e] = sees(end, t) && vrow[t] ? __fmul_rn(acc[nb][2 * h + e], p.scale) : -INFINITY;
+                            Sw[8 * h * kSStride + 8 * nb + e] =
+                                sees(end, t) && vrow[t] ? __fmul_rn(acc[h >> 1][nb][2 * (h & 1) + e], p.scale) : -INFINITY;
                         }
                 }
             }
@@ -408,6 +423,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
             for (int y = 0; y < R; ++y) {
                 const int r = gw + GW * y;
+                __syncwarp();                              // the row has been read
                 if (m[y] == -INFINITY) {                   // does it see any token of the chunk in the cache?
                     bool any = false;
 #pragma unroll
@@ -417,9 +433,19 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 l[y] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kChunk / 32; ++i) {    // (-inf, and p = 0, for what it does not see)
-                    const float e = expf(sc[y][i] - m[y]);
-                    S[r * kSStride + lane + 32 * i] = e;
-                    l[y] += e;
+                    sc[y][i] = expf(sc[y][i] - m[y]);
+                    l[y] += sc[y][i];
+                }
+                // p takes the row's place as bf16, 128 hi and then 128 lo (see probability)
+#pragma unroll
+                for (int i = 0; i < kChunk / 32; i += 2) {
+                    uint32_t hi, lo;
+                    split_bf16x2(sc[y][i], sc[y][i + 1], hi, lo);
+                    uint16_t *at = reinterpret_cast<uint16_t *>(S + r * kSStride) + (lane ^ (2 * r & 8));
+                    at[32 * i] = static_cast<uint16_t>(hi);
+                    at[32 * i + 32] = static_cast<uint16_t>(hi >> 16);
+                    at[32 * i + kChunk] = static_cast<uint16_t>(lo);
+                    at[32 * i + kChunk + 32] = static_cast<uint16_t>(lo >> 16);
                 }
             }
 #pragma unroll
@@ -437,11 +463,15 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 if (rec) *reinterpret_cast<float2 *>(rec) = make_float2(ml, ll);
             }
         };
-        if (rows > GW)
-            softmax(std::integral_constant<int, 16 / GW>{});
-        else
+        if (rows <= GW)
             softmax(std::integral_constant<int, 1>{});
-        const bool ok_v = mbar_wait(&fullV[slot * NG + grp], (k / (kSlots * NG)) & 1, abort_flag);
+        else if (rows <= 16)
+            softmax(std::integral_constant<int, 16 / GW>{});
+        else if (rows <= 24)
+            softmax(std::integral_constant<int, MT == 1 ? 16 / GW : 24 / GW>{});
+        else
+            softmax(std::integral_constant<int, ROWS / GW>{});
+        const bool ok_v = mbar_wait(&fullV[slot * NG + grp], (k / kTurn) & 1, abort_flag);
         // rows behind the last token's and rows out of the tile's sight, whether they came with a box or not: p = 0 has to
         // meet finite values
         if (p.box_rows > 0 && (x.n < kChunk || x.h1 > x.h0)) {
@@ -454,17 +484,13 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (stop(ok_v)) break;
 
         // values: warp gw takes dimensions DW gw .. DW gw + DW - 1, tokens ascending in 16-token steps, hi before lo
-        uint32_t ph[kChunk / 16][4], pl[kChunk / 16][4];
-#pragma unroll
-        for (int ks = 0; ks < kChunk / 16; ++ks)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {                  // rows gq, gq + 8; tokens + 0, + 8
-                const int r = gq + 8 * (i & 1);
-                float2 e = make_float2(0.0f, 0.0f);
-                if (r < rows) e = *reinterpret_cast<const float2 *>(S + r * kSStride + ks * 16 + 2 * cq + 8 * (i >> 1));
-                split_bf16x2(e.x, e.y, ph[ks][i], pl[ks][i]);
-            }
-        group_sync<GW>(grp);                               // the scores' buffer may be written again
+        // p of rows 16 mt .. and tokens 16 ks .. (+ kChunk: lo). A row's 16-byte pieces are swapped in pairs in every other
+        // four rows, so that eight rows' pieces lie in different banks. (The buffer is written again after the next item's
+        // barrier; rows that do not exist hold anything.)
+        auto probability = [&](int mt, int at, uint32_t (&a)[4]) {
+            const int r = 16 * mt + (lane & 15);
+            ldmatrix_x4(a[0], a[1], a[2], a[3], smem_u32(reinterpret_cast<const uint16_t *>(S + r * kSStride) + ((at + 8 * (lane >> 4)) ^ (2 * r & 8))));
+        };
         const int d0 = gw * DW, mi = lane >> 3, mr = lane & 7;   // ldmatrix: matrix, row
         auto fetch = [&](int ks, uint32_t (&v)[DW / 16][4]) {
 #pragma unroll
@@ -472,7 +498,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 ldmatrix_x4_trans(v[hf][0], v[hf][1], v[hf][2], v[hf][3],
                                   smem_u32(Vs + kv_piece(ks * 16 + (mi & 1) * 8 + mr, ((d0 + 16 * hf) >> 3) + (mi >> 1))));
         };
-        auto products = [&](float (&acc)[DW / 8][4], auto by_token, int end) {
+        auto products = [&](float (&acc)[MT][DW / 8][4], auto by_token, int end) {
 #pragma unroll
             for (int ks = 0; ks < kChunk / 16; ++ks) {
                 uint32_t v[DW / 16][4];
@@ -489,16 +515,23 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
                         for (int i = 0; i < 4; ++i) v[hf][i] &= keep[i & 1];
                 }
+                uint32_t ph[MT][4], pl[MT][4];
 #pragma unroll
-                for (int hf = 0; hf < DW / 16; ++hf) {
-                    mma_16816(acc[2 * hf], ph[ks][0], ph[ks][1], ph[ks][2], ph[ks][3], v[hf][0], v[hf][1]);
-                    mma_16816(acc[2 * hf + 1], ph[ks][0], ph[ks][1], ph[ks][2], ph[ks][3], v[hf][2], v[hf][3]);
+                for (int mt = 0; mt < MT; ++mt) {
+                    probability(mt, 16 * ks, ph[mt]);
+                    probability(mt, 16 * ks + kChunk, pl[mt]);
                 }
 #pragma unroll
-                for (int hf = 0; hf < DW / 16; ++hf) {
-                    mma_16816(acc[2 * hf], pl[ks][0], pl[ks][1], pl[ks][2], pl[ks][3], v[hf][0], v[hf][1]);
-                    mma_16816(acc[2 * hf + 1], pl[ks][0], pl[ks][1], pl[ks][2], pl[ks][3], v[hf][2], v[hf][3]);
-                }
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const uint32_t(&a)[4] = part == 0 ? ph[mt] : pl[mt];
+#pragma unroll
+                        for (int hf = 0; hf < DW / 16; ++hf) {
+                            mma_16816(acc[mt][2 * hf], a[0], a[1], a[2], a[3], v[hf][0], v[hf][1]);
+                            mma_16816(acc[mt][2 * hf + 1], a[0], a[1], a[2], a[3], v[hf][2], v[hf][3]);
+                        }
+                    }
             }
         };
         // in a chunk that is masked for some of several tokens: a value that is not finite among this warp's dimensions?
@@ -516,28 +549,31 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             }
             odd = __any_sync(0xffffffffu, !fine);
         }
-        float acc[DW / 8][4] = {};
+        float acc[MT][DW / 8][4] = {};
         if (!odd) {
             products(acc, std::false_type{}, 0);
         } else {
 #pragma unroll 1
             for (int u = 0; u < x.ntok; ++u) {
-                float one[DW / 8][4] = {};
+                float one[MT][DW / 8][4] = {};
                 products(one, std::true_type{}, end_of(u * G));
 #pragma unroll
-                for (int nb = 0; nb < DW / 8; ++nb)
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if ((gq + 8 * (e >> 1)) / G == u) acc[nb][e] = one[nb][e];
+                    for (int nb = 0; nb < DW / 8; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if ((16 * mt + gq + 8 * (e >> 1)) / G == u) acc[mt][nb][e] = one[mt][nb][e];
             }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2 * MT; ++h) {
             float *rec = record(gq + 8 * h);
             if (!rec) continue;
             rec += 2 + d0 + 2 * cq;
 #pragma unroll
-            for (int nb = 0; nb < DW / 8; ++nb) *reinterpret_cast<float2 *>(rec + nb * 8) = make_float2(acc[nb][2 * h], acc[nb][2 * h + 1]);
+            for (int nb = 0; nb < DW / 8; ++nb)
+                *reinterpret_cast<float2 *>(rec + nb * 8) = make_float2(acc[h >> 1][nb][2 * (h & 1)], acc[h >> 1][nb][2 * (h & 1) + 1]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&emptyV[slot]);         // this warp is done with V
@@ -573,11 +609,27 @@ attn_few_merge_kernel(const FewParams p, const int per) {
     }
 }
 
-template <int G>
-bi_status launch_g(const CUtensorMap &tmK, const CUtensorMap &tmV, FewParams p, int sms, cudaStream_t s) {
+template <int G, int MT>
+bi_status launch_mt(const CUtensorMap &tmK, const CUtensorMap &tmV, const FewParams &p, int sms, cudaStream_t s) {
     static unsigned long long configured = 0;
-    if (ensure_smem_attr(reinterpret_cast<const void *>(attn_few_kernel<G>), kSmem, &configured) != BI_OK) return BI_ERR_CUDA;
-    return launch_pdl(attn_few_kernel<G>, dim3(static_cast<unsigned>(sms)), dim3(kThreads), kSmem, s, tmK, tmV, p);
+    constexpr int smem = Shape<MT>::kSmem;
+    if (ensure_smem_attr(reinterpret_cast<const void *>(attn_few_kernel<G, MT>), smem, &configured) != BI_OK) return BI_ERR_CUDA;
+    return launch_pdl(attn_few_kernel<G, MT>, dim3(static_cast<unsigned>(sms)), dim3(Shape<MT>::kThreads), smem, s, tmK, tmV, p);
+}
+// Items of 32 rows read a chunk half as often, for the fewer slots, where the longest sequence's tiles of 16 pair up and
+// either there are many of them or the loading warps' copies by row are what takes the time. Tiles of 16, of 32 rows, in us for
+// both kernels: 64 x 5 tokens, window 4096, 32 heads over 8: 357, 320; 32 x 5, window 2048: 158, 135; 16 x 5, window 4096
+// (55 items an SM): 106, 101; 16 x 8, window 1024 (15 an SM): 51.7, 55.8; 64 x 12 (three tiles): 635, 727; blocks of 24,
+// 16 x 5, window 1024: 140, 105.
+template <int G>
+bi_status launch_g(const CUtensorMap &tmK, const CUtensorMap &tmV, FewParams p, int most, int sms, cudaStream_t s) {
+    p.tiles = (most + 16 / G - 1) / (16 / G);
+    const double items = static_cast<double>(p.batch) * p.tiles * p.Hkv * p.chunks;
+    if (p.tiles % 2 == 0 && (p.box_rows == 0 || items > 40.0 * sms)) {
+        p.tiles /= 2;
+        return launch_mt<G, 2>(tmK, tmV, p, sms, s);
+    }
+    return launch_mt<G, 1>(tmK, tmV, p, sms, s);
 }
 
 }  // namespace
@@ -608,7 +660,6 @@ bi_status launch_attention_few_window(const WindowCall &a, int32_t few, void *wo
     p.max_len = a.max_len;
     p.max_q = a.max_q;
     p.few = few;
-    p.tiles = (most + 16 / G - 1) / (16 / G);
     p.window = a.window;
     p.sinks = a.sinks;
     p.scale = a.scale;
@@ -616,10 +667,10 @@ bi_status launch_attention_few_window(const WindowCall &a, int32_t few, void *wo
     CUtensorMap tmK{}, tmV{};
     p.box_rows = kv_box_maps(a.K, a.V, a.num_blocks, a.bs, a.Hkv, &tmK, &tmV);
     switch (G) {
-        case 1: st = launch_g<1>(tmK, tmV, p, info->sm_count, s); break;
-        case 2: st = launch_g<2>(tmK, tmV, p, info->sm_count, s); break;
-        case 4: st = launch_g<4>(tmK, tmV, p, info->sm_count, s); break;
-        case 8: st = launch_g<8>(tmK, tmV, p, info->sm_count, s); break;
+        case 1: st = launch_g<1>(tmK, tmV, p, most, info->sm_count, s); break;
+        case 2: st = launch_g<2>(tmK, tmV, p, most, info->sm_count, s); break;
+        case 4: st = launch_g<4>(tmK, tmV, p, most, info->sm_count, s); break;
+        case 8: st = launch_g<8>(tmK, tmV, p, most, info->sm_count, s); break;
         default: return BI_ERR_UNSUPPORTED;
     }
     if (st != BI_OK) return st;

@@ -229,6 +229,26 @@ def test_values_that_are_not_finite_reach_only_tokens_that_see_them(bi, Hq, Hkv)
     assert bi.device_status() == bi.BI_OK
 
 
+@pytest.mark.parametrize("Hq,bs", [(8, 16), (16, 64), (32, 16), (64, 128), (32, 24)])
+@pytest.mark.parametrize("W,S", [(130, 5), (1 << 30, 0)])
+def test_many_sequences_of_drafts(bi, Hq, bs, W, S):
+    """Up to 32 query rows a KV head and more than 40 (sequence, 16 rows, KV head, chunk) an SM: two tiles of 16 rows at
+    once. Every token has decode's bits, also where some of its neighbours see values that are not finite."""
+    import torch
+    most = 32 // (Hq // 8)
+    c = Case([300, 129, 40, 256, 299] * 20, [most, most - 1, 1, most // 2 + 1, 0] * 20, Hq, 8, bs, seed=Hq)
+    for value in (None, "nan", "-inf"):
+        V = c.V.clone()
+        if value:
+            for b, j in ((0, 297), (1, 128), (3, 120), (5, 299), (10, 0), (10, 170), (15, 299 - W % 128)):
+                j = min(j, c.lens[b] - 1)
+                V[c.table_np[b, j // bs], j % bs, b % 8, (37 * j) % D] = float(value)
+        cut = torch.nan_to_num(c.cut(bi, W, S, V=V).float(), nan=123.0)
+        for got in (c.extend(bi, W, S, V=V, max_len=20000), c.extend(bi, W, S, V=V), c.tiled(bi, W, S, V=V)):
+            assert torch.equal(torch.nan_to_num(got.float(), nan=123.0), cut)
+    assert bi.device_status() == bi.BI_OK
+
+
 @pytest.mark.parametrize("bs", [16, 24])
 def test_blocks_outside_the_cache(bi, bs):
     """A block in sight that lies outside: its tokens count nothing, also where it holds all that a token sees of a chunk."""

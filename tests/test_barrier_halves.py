@@ -8,6 +8,7 @@ loading warps find the items: a consumer takes the next one that is handed on wi
 K, until one says that there are no more. Checked: no deadlock, every half and flag set that
 is read holds the reader's own item, nothing lands in what is being read. The
 form with one flag set has to break."""
+import math
 import random
 
 import pytest
@@ -25,7 +26,7 @@ def _run(slots, groups, items, seed, flag_sets=2, handed=False):
     flags = [[None] * slots for _ in range(flag_sets)]
     pending = []
     bar_of = lambda h, k: full[h][(k % slots) * groups + k % groups]
-    parity = lambda k: (k // (slots * groups)) & 1
+    parity = lambda k: (k // math.lcm(slots, groups)) & 1
     flag_of = lambda k: flags[(k // slots) % flag_sets]
 
     def loader(lw):
@@ -39,6 +40,10 @@ def _run(slots, groups, items, seed, flag_sets=2, handed=False):
                 bar_of(h, k).arrive(tx=1)
                 pending.append((h, k % slots, k, bar_of(h, k)))
                 yield
+        last = max((k for k in range(lw, items, slots)), default=None)
+        if last is not None:                             # its copies land before the loader leaves
+            while not bar_of("K", last).try_wait(parity(last)):
+                yield
         if handed:                                       # no more items
             k = next(k for k in range(items, items + slots) if k % slots == lw)
             if k >= slots:
@@ -46,6 +51,9 @@ def _run(slots, groups, items, seed, flag_sets=2, handed=False):
                     yield
             flag_of(k)[k % slots] = "none"
             bar_of("K", k).arrive()
+        if last is not None:
+            while not bar_of("V", last).try_wait(parity(last)):
+                yield
 
     def consumer(g):
         for k in range(g, items + slots * groups if handed else items, groups):
@@ -98,8 +106,9 @@ def test_ring_of_halves(slots, groups, items):
 
 @pytest.mark.parametrize("items", [0, 1, 2, 3, 4, 5, 6, 7, 13, 40])
 def test_items_handed_on(items):
-    for seed in range(150):
-        assert _run(3, 2, items, seed, handed=True) == "ok", f"seed={seed}"
+    for slots in (3, 2):
+        for seed in range(150):
+            assert _run(slots, 2, items, seed, handed=True) == "ok", f"slots={slots} seed={seed}"
 
 
 def test_the_model_catches_a_single_flag_set():
