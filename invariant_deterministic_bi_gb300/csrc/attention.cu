@@ -95,12 +95,11 @@ __device__ __forceinline__ bool seq_ok(const AttnParams &p, int64_t b, int &L) {
 // chunk) items blockIdx.x, blockIdx.x + gridDim.x, ... (which CTA computes an
 // item changes no arithmetic). A loading warp keeps up to kSlots chunks in
 // flight: per item it resolves the chunk's block-table entries and loads the
-// chunk's K and V rows of KV head g with TMA, one box per cache block (a 4-D
+// chunk's K and V rows of KV head g with TMA, one box per cache block or part of one (a 4-D
 // tensor map over [blocks][block size][KV heads][128], two 64-dimension
 // halves per box, 128-byte swizzle), plus the G q rows by a bulk copy, counted
 // on "full" barriers of the slot's K (and q) and V halves. Block sizes that boxes cannot tile
-// (not a multiple of 128 and not 8, 16, 32 or 64) take 16-byte cp.async
-// copies per row instead. Blocks outside the cache arrive as zeros and their
+// (not a multiple of 8) take 16-byte cp.async copies per row instead. Blocks outside the cache arrive as zeros and their
 // tokens score -inf. Eight consumer warps, in NG groups, compute the chunks
 // and hand each half back through its "empty" barrier: the next item's K loads
 // while the softmax and p.V of this one run.
@@ -329,7 +328,7 @@ __device__ __forceinline__ void split_items(const CUtensorMap &tmK, const CUtens
             for (int i = 0; i < kChunk / 32; ++i) flags[lane + 32 * i] = ok_row[i];
             const uint16_t *qsrc = p.Q + (b * p.Hq + g * G) * kD;
             if (p.box_rows > 0) {
-                // one box per cache block (box_rows tokens), both halves
+                // one box of box_rows tokens a lane, both halves
                 const int boxes = WIN ? __popc(__ballot_sync(0xffffffffu, box)) : nbox;
                 const int kv_bytes = boxes * p.box_rows * 2 * 128;  // the K rows, or the V rows
                 const int tok = (j0 + lane * p.box_rows) % p.bs;
@@ -1132,10 +1131,12 @@ int64_t attention_decode_workspace_bytes(int64_t B, int32_t Hq, int32_t max_len,
     return B * Hq * chunks * kRecord;
 }
 
-// TMA boxes of whole cache blocks (box start rows on 1024-byte swizzle atoms): tokens a box, 0 without boxes.
+// TMA boxes of the most tokens (128, 64, ... 8: box start rows on 1024-byte swizzle atoms) that divide a block, so that a
+// chunk's boxes never pass a block's end: tokens a box, 0 without boxes. Blocks of 24 (32 heads over 8), with boxes and with copies by
+// row: decode of 64 x 4096 tokens 188 and 310 us, 64 x 5 new tokens over 4000, window 1024, 130 and 394, 512 over 1500 76 and 273.
 int32_t kv_box_maps(const void *K, const void *V, int64_t num_blocks, int32_t bs, int32_t Hkv, CUtensorMap *tmK, CUtensorMap *tmV) {
-    const int32_t rows = bs % kChunk == 0 ? kChunk : (kChunk % bs == 0 && bs >= 8 ? bs : 0);
-    if (rows == 0) return 0;
+    const int32_t lowest = bs & -bs, rows = lowest < kChunk ? lowest : kChunk;
+    if (rows < 8) return 0;
     const uint64_t dims[4] = {static_cast<uint64_t>(kD), static_cast<uint64_t>(Hkv), static_cast<uint64_t>(bs),
                               static_cast<uint64_t>(num_blocks)};
     const uint64_t strides[3] = {static_cast<uint64_t>(kRowBytes), static_cast<uint64_t>(Hkv) * kRowBytes,

@@ -16,7 +16,7 @@
 // other tiles read the same chunks; and where V holds a value that is not finite out of
 // some token's sight, p.V token by token with zeros there.
 //
-// 16 sequences of 5 drafts over 100 to 4000 tokens, window 1024, 32 heads over 8: 40 us for
+// 16 sequences of 5 drafts over 100 to 4000 tokens, window 1024, 32 heads over 8: 39 us for
 // both kernels (the tiled kernel, one CTA a sequence and KV head: 80); 64 single tokens over 4000, 60 (271).
 #include "attn_common.cuh"
 #include "bi_internal.h"
@@ -619,8 +619,8 @@ bi_status launch_mt(const CUtensorMap &tmK, const CUtensorMap &tmV, const FewPar
 // Items of 32 rows read a chunk half as often, for the fewer slots, where the longest sequence's tiles of 16 pair up and
 // either there are many of them or the loading warps' copies by row are what takes the time. Tiles of 16, of 32 rows, in us for
 // both kernels: 64 x 5 tokens, window 4096, 32 heads over 8: 357, 320; 32 x 5, window 2048: 158, 135; 16 x 5, window 4096
-// (55 items an SM): 106, 101; 16 x 8, window 1024 (15 an SM): 51.7, 55.8; 64 x 12 (three tiles): 635, 727; blocks of 24,
-// 16 x 5, window 1024: 140, 105.
+// (55 items an SM): 106, 101; 16 x 8, window 1024 (15 an SM): 51.7, 55.8; 64 x 12 (three tiles): 635, 727; copied
+// by row, 16 x 5, window 1024: 140, 105.
 template <int G>
 bi_status launch_g(const CUtensorMap &tmK, const CUtensorMap &tmV, FewParams p, int most, int sms, cudaStream_t s) {
     p.tiles = (most + 16 / G - 1) / (16 / G);

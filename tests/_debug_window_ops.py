@@ -30,7 +30,7 @@ def main():
             slots = torch.randperm(Kc.shape[0] * 16, device="cuda", generator=g)[:T]
             q = bi.kv_append(x[:, 5:7], x[:, 7:], slots, Kc, Vc, pos, fr, k_weight=w, Q=x[:, :5], q_weight=w)
             out[f"heads{T}_{D}"] = digest(bi.rope(x, pos, fr), *bi.qk_norm_rope(x[:, :5], x[:, 5:], w, w, 1e-6, pos, fr), Kc, Vc, q)
-    for Hq, Hkv, bs in ((8, 2, 16), (8, 1, 24), (4, 4, 128)):
+    for Hq, Hkv, bs in ((8, 2, 16), (8, 1, 24), (8, 1, 20), (4, 4, 128)):
         nb = -(-2600 // bs)
         K, V = bf(4 * nb, bs, Hkv, 128), bf(4 * nb, bs, Hkv, 128)
         table = torch.randperm(4 * nb, device="cuda", generator=g).to(torch.int32).view(4, nb)

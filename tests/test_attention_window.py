@@ -80,7 +80,7 @@ WINDOWS = [(1, 0), (1, 1), (3, 130), (127, 0), (128, 4), (129, 128), (200, 300),
 
 
 @pytest.mark.parametrize("W,S", WINDOWS)
-@pytest.mark.parametrize("Hq,Hkv,bs", [(8, 2, 16), (8, 1, 24), (4, 4, 128), (6, 3, 64), (8, 1, 1)])
+@pytest.mark.parametrize("Hq,Hkv,bs", [(8, 2, 16), (8, 1, 24), (4, 4, 128), (6, 3, 64), (8, 1, 1), (8, 2, 192)])
 def test_decode(bi, Hq, Hkv, bs, W, S):
     c = Case([1, 2, 127, 128, 129, 255, 257, 384, 700, 1300], [1] * 10, Hq, Hkv, bs, seed=W + S)
     assert_close_rel(f64_of(c.decode(bi, W, S)), c.reference(W, S), RTOL, ATOL, f"W={W} S={S}")
@@ -105,7 +105,7 @@ def test_decode_long(bi, B, W, S):
 
 
 @pytest.mark.parametrize("W,S", WINDOWS)
-@pytest.mark.parametrize("Hq,Hkv,bs", [(8, 2, 16), (8, 1, 24), (4, 4, 128), (6, 3, 64)])
+@pytest.mark.parametrize("Hq,Hkv,bs", [(8, 2, 16), (8, 1, 24), (8, 2, 20), (4, 4, 128), (6, 3, 64)])
 def test_extend(bi, Hq, Hkv, bs, W, S):
     c = Case([1, 128, 300, 513, 40], [1, 128, 200, 33, 0], Hq, Hkv, bs, seed=W + S + 1)
     got = c.extend(bi, W, S)
@@ -131,7 +131,7 @@ def test_a_window_that_holds_everything_changes_no_bit(bi, B):
     assert bi.device_status() == bi.BI_OK
 
 
-@pytest.mark.parametrize("Hq,Hkv,bs", [(16, 4, 16), (4, 4, 24), (16, 2, 64)])
+@pytest.mark.parametrize("Hq,Hkv,bs", [(16, 4, 16), (4, 4, 24), (16, 2, 64), (8, 2, 12)])
 @pytest.mark.parametrize("W,S", [(200, 5), (1000, 0)])
 def test_prompts_and_single_tokens_in_one_batch(bi, Hq, Hkv, bs, W, S):
     """Sequences of a few tokens go to the split, the others to the tiles, in one call (all to one of them by other
@@ -191,7 +191,7 @@ def hide(c, W, S, value):
 
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), 3.0e38])
-@pytest.mark.parametrize("W,S,bs", [(100, 4, 16), (300, 0, 24), (130, 129, 128), (17, 3, 256), (64, 5, 8)])
+@pytest.mark.parametrize("W,S,bs", [(100, 4, 16), (300, 0, 24), (200, 5, 20), (130, 129, 128), (17, 3, 256), (64, 5, 8)])
 def test_what_is_out_of_sight_has_no_effect(bi, value, W, S, bs):
     import torch
     for lens, q in (([700, 129, 3, 1290], [1] * 4), ([700, 129, 3, 1290] * 30, [1] * 120), ([700, 129, 3, 1290], [150, 2, 3, 1])):
@@ -229,7 +229,7 @@ def test_values_that_are_not_finite_reach_only_tokens_that_see_them(bi, Hq, Hkv)
     assert bi.device_status() == bi.BI_OK
 
 
-@pytest.mark.parametrize("Hq,bs", [(8, 16), (16, 64), (32, 16), (64, 128), (32, 24)])
+@pytest.mark.parametrize("Hq,bs", [(8, 16), (16, 64), (32, 16), (64, 128), (32, 24), (32, 20), (8, 1)])
 @pytest.mark.parametrize("W,S", [(130, 5), (1 << 30, 0)])
 def test_many_sequences_of_drafts(bi, Hq, bs, W, S):
     """Up to 32 query rows a KV head and more than 40 (sequence, 16 rows, KV head, chunk) an SM: two tiles of 16 rows at
@@ -249,7 +249,7 @@ def test_many_sequences_of_drafts(bi, Hq, bs, W, S):
     assert bi.device_status() == bi.BI_OK
 
 
-@pytest.mark.parametrize("bs", [16, 24])
+@pytest.mark.parametrize("bs", [16, 24, 20])
 def test_blocks_outside_the_cache(bi, bs):
     """A block in sight that lies outside: its tokens count nothing, also where it holds all that a token sees of a chunk."""
     import torch
