@@ -100,6 +100,7 @@ def load() -> ctypes.CDLL:
             "bi_attention_decode_window_workspace_size": [I64, I32, I32, I32, I32],
             "bi_attention_decode_window": [P, P, P, P, I32, I64, P, I64, I32, I32, I32, I32, I32, F, I32, I32, P, I64, P, P],
             "bi_attention_extend_window_workspace_size": [I64, I32, I32, I32, I32, I32, I32],
+            "bi_attention_extend_window_batch_workspace_size": [I64, I64, I32, I32, I32, I32, I32, I32],
             "bi_attention_extend_window": [P, P, I32, P, P, P, I32, I64, P, I64, I32, I32, I32, I32, I32, I32, F, I32, I32,
                                            P, I64, P, P],
             "bi_plan": [I32, I64, I64, I64, I32, ctypes.POINTER(Plan)],
@@ -115,7 +116,7 @@ def load() -> ctypes.CDLL:
         lib.bi_status_string.restype = ctypes.c_char_p
         lib.bi_attention_decode_workspace_size.restype = ctypes.c_int64
         for name in ("bi_attention_extend_int4_workspace_size", "bi_attention_decode_window_workspace_size",
-                     "bi_attention_extend_window_workspace_size"):
+                     "bi_attention_extend_window_workspace_size", "bi_attention_extend_window_batch_workspace_size"):
             getattr(lib, name).restype = ctypes.c_int64
         _bind_torch()
         _lib = lib
@@ -952,9 +953,13 @@ def attention_decode_window(Q, K_cache, V_cache, block_table, seq_lens, max_seq_
 
 
 def attention_extend_window_workspace_size(total_q: int, Hq: int, Hkv: int, max_seq_len: int, max_q_len: int, window: int,
-                                           sinks: int = 0) -> int:
+                                           sinks: int = 0, B=None) -> int:
+    """Bytes for a call over B sequences, 0 where it splits nothing; without B, enough for any number of them, 0 past 512 MB."""
     window, sinks = _window(window, sinks)
-    return int(load().bi_attention_extend_window_workspace_size(total_q, Hq, Hkv, _most(max_seq_len), _most(max_q_len), window, sinks))
+    sizes = total_q, Hq, Hkv, _most(max_seq_len), _most(max_q_len), window, sinks
+    if B is None:
+        return int(load().bi_attention_extend_window_workspace_size(*sizes))
+    return int(load().bi_attention_extend_window_batch_workspace_size(B, *sizes))
 
 
 def attention_extend_window(Q, cu_q, K_cache, V_cache, block_table, seq_lens, max_seq_len: int, max_q_len: int, scale: float,
@@ -963,7 +968,7 @@ def attention_extend_window(Q, cu_q, K_cache, V_cache, block_table, seq_lens, ma
     bits of ``attention_decode_window`` of each token's cut sequence.
 
     Table entries of blocks out of every new token's sight may be anything. The workspace (uint8,
-    ``attention_extend_window_workspace_size`` bytes) is allocated with torch if not given."""
+    ``attention_extend_window_workspace_size`` bytes for these B sequences) is allocated with torch if not given."""
     call = load()
     cur = _current_device()
     (T, Hq, D), (nblk, bs, Hkv, _), table = _attention_window_args(Q, K_cache, V_cache, block_table, seq_lens, workspace, O, cur)
@@ -971,7 +976,7 @@ def attention_extend_window(Q, cu_q, K_cache, V_cache, block_table, seq_lens, ma
     _tensor(cu_q, _int32, (B + 1,), "cu_q", cur)
     window, sinks = _window(window, sinks)
     if workspace is None:
-        need = attention_extend_window_workspace_size(T, Hq, Hkv, max_seq_len, max_q_len, window, sinks)
+        need = attention_extend_window_workspace_size(T, Hq, Hkv, max_seq_len, max_q_len, window, sinks, B)
         workspace = _new(need, _uint8, Q, stream) if need > 0 else None
     if O is None:
         O = _out(Q, stream)

@@ -391,12 +391,25 @@ bi_status bi_attention_decode_window(const void *Q, const void *K_cache, const v
                             workspace_bytes, O, stream);
 }
 
+namespace {
+bool extend_window_sizes_ok(int64_t total_q, int32_t Hq, int32_t Hkv, int32_t max_seq_len, int32_t max_q_len, int32_t window,
+                            int32_t sinks) {
+    return total_q >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && max_q_len >= 1 && max_seq_len >= 1 &&
+           max_seq_len <= BI_ATTENTION_MAX_SEQ_LEN && window >= 1 && sinks >= 0;
+}
+}  // namespace
+
 int64_t bi_attention_extend_window_workspace_size(int64_t total_q, int32_t Hq, int32_t Hkv, int32_t max_seq_len,
                                                   int32_t max_q_len, int32_t window, int32_t sinks) {
-    if (total_q < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || max_q_len < 1 || max_seq_len < 1 ||
-        max_seq_len > BI_ATTENTION_MAX_SEQ_LEN || window < 1 || sinks < 0)
-        return -1;
+    if (!extend_window_sizes_ok(total_q, Hq, Hkv, max_seq_len, max_q_len, window, sinks)) return -1;
     return attention_extend_window_workspace_bytes(total_q, Hq, max_seq_len, at_most_max_len(window), at_most_max_len(sinks));
+}
+
+int64_t bi_attention_extend_window_batch_workspace_size(int64_t B, int64_t total_q, int32_t Hq, int32_t Hkv, int32_t max_seq_len,
+                                                        int32_t max_q_len, int32_t window, int32_t sinks) {
+    if (B < 0 || B > 65535 || total_q > kI32Max || !extend_window_sizes_ok(total_q, Hq, Hkv, max_seq_len, max_q_len, window, sinks))
+        return -1;
+    return plan_few(B, total_q, Hq, Hkv, max_seq_len, max_q_len, at_most_max_len(window), at_most_max_len(sinks)).bytes;
 }
 
 bi_status bi_attention_extend_window(const void *Q, const int32_t *cu_q, int32_t total_q, const void *K_cache,
@@ -408,8 +421,9 @@ bi_status bi_attention_extend_window(const void *Q, const int32_t *cu_q, int32_t
     if (window < 1 || sinks < 0 || workspace_bytes < 0) return BI_ERR_INVALID_ARG;
     if (!aligned16(workspace)) return BI_ERR_MISALIGNED;
     window = at_most_max_len(window), sinks = at_most_max_len(sinks);
-    if (workspace && total_q >= 0 && Hq >= 1 && max_seq_len >= 1 && max_seq_len <= BI_ATTENTION_MAX_SEQ_LEN) {
-        const int64_t need = attention_extend_window_workspace_bytes(total_q, Hq, max_seq_len, window, sinks);
+    if (workspace) {
+        const int64_t need =
+            bi_attention_extend_window_batch_workspace_size(B, total_q, Hq, Hkv, max_seq_len, max_q_len, window, sinks);
         if (need <= 0 || workspace_bytes < need) workspace = nullptr;
     }
     return attention_extend(Q, cu_q, total_q, K_cache, V_cache, block_table, max_blocks_per_seq, num_blocks, seq_lens, B, Hq,

@@ -682,35 +682,54 @@ int64_t attention_extend_window_workspace_bytes(int64_t total_q, int32_t Hq, int
 
 // Which sequences are split over the chunks: all, where that should take less time for the call; else those of at most
 // kFewRows query rows, for which it takes less of an SM's time (a chunk of a tile of 16 rows 1.4 us, of 128 rows 5.3).
-// In us, on the sums that the host knows: drafts 16 x 5 over 4000, window 1024, 80 tiled, 40 split.
-static int32_t few_tokens(const WindowCall &a, int sms) {
-    constexpr int kFewRows = 64;
-    const int G = a.Hq / a.Hkv;
-    const double chunks = static_cast<double>(seen_chunks(a.max_len, a.window, a.sinks));
-    const int64_t rows = static_cast<int64_t>(a.total_q) * G, seqs = a.B < a.total_q ? a.B : a.total_q;
+// In us, on the sums that the host knows and for 152 SMs, so that the choice is the same wherever a size is asked for: drafts
+// 16 x 5 over 4000, window 1024, 80 tiled, 40 split.
+static bool split_all(int64_t B, int64_t total_q, int G, int32_t Hkv, int64_t seen, int64_t max_q) {
+    constexpr int kSms = 152;
+    const double chunks = static_cast<double>(seen);
+    const int64_t rows = total_q * G, seqs = B < total_q ? B : total_q;
     const int64_t tiles = (rows + kRows - 1) / kRows > seqs ? (rows + kRows - 1) / kRows : seqs;
-    const double tiled = static_cast<double>((tiles * a.Hkv + sms - 1) / sms) * (10.0 + 5.3 * chunks);
-    const double split = 10.0 + static_cast<double>(((rows + 15) / 16 + seqs) * a.Hkv) * chunks * 1.4 / sms;
+    const double tiled = static_cast<double>((tiles * Hkv + kSms - 1) / kSms) * (10.0 + 5.3 * chunks);
+    const double split = 10.0 + static_cast<double>(((rows + 15) / 16 + seqs) * Hkv) * chunks * 1.4 / kSms;
     // (the split lays its work out for the most new tokens of every sequence: not where most of that would be empty)
-    return split < tiled && a.B * a.max_q <= 4 * static_cast<int64_t>(a.total_q) ? a.max_q : kFewRows / G;
+    return split < tiled && B * max_q <= 4 * total_q;
+}
+
+// Results are held for the tokens that can be split, at most kFewBytes: for every row of Q, or, where those are fewer, `few`
+// places a sequence (63 single tokens and a prompt of 2048, window 1024, 32 heads: 170 MB where every row would take 351). Where
+// they would not fit, `few` is what does (the same with a window of 4096: 14 places a sequence instead of 16; 584 us, with
+// the single tokens in tiles 1009).
+FewPlan plan_few(int64_t B, int64_t total_q, int32_t Hq, int32_t Hkv, int32_t max_len, int32_t max_q, int32_t window, int32_t sinks) {
+    constexpr int kFewRows = 64;
+    const FewPlan none{0, 0, 0};
+    if (B < 1 || total_q < 1) return none;
+    const int64_t place = attention_decode_workspace_bytes(1, Hq, max_len, window, sinks), room = place > 0 ? kFewBytes / place : 0;
+    const int G = Hq / Hkv;
+    if (max_q > total_q) max_q = static_cast<int32_t>(total_q);
+    int64_t few = kFewRows / G, places = total_q;
+    if (total_q <= room && split_all(B, total_q, G, Hkv, seen_chunks(max_len, window, sinks), max_q)) {
+        few = max_q;
+    } else {
+        if (total_q > room && few > room / B) {
+            if (max_q <= few && total_q > B * (room / B)) return none;     // short ones alone, most of which would not fit
+            few = room / B;
+        }
+        // mostly sequences of more tokens (a sequence of few has a tile of its own then; without any, the split's two
+        // launches would cost 7 us for nothing): the tiled kernel alone
+        if (max_q > few && (B == 1 || total_q > 4 * B * few)) few = 0;
+        if (places > B * few) places = B * few;
+    }
+    // (the merge's grid)
+    if (few == 0 || B * (few < max_q ? few : max_q) > 0x7fffffff / Hq) return none;
+    return FewPlan{static_cast<int32_t>(few), places, places * place};
 }
 
 bi_status launch_attention_extend_window(const WindowCall &a, void *workspace, cudaStream_t s) {
-    int32_t few = 0;
-    if (workspace) {
-        int dev = 0;
-        const DeviceInfo *info = nullptr;
-        const bi_status st = current_device(&dev, &info);
-        if (st != BI_OK) return st;
-        few = few_tokens(a, info->sm_count);
-        const int32_t most = few < a.max_q ? few : a.max_q;
-        // mostly sequences of more tokens (a sequence of few has a tile of its own then; without any, the split's two launches
-        // would cost 7 us for nothing), or too many results to merge in one launch: the tiled kernel alone
-        if ((a.max_q > few && (a.B == 1 || a.total_q > 4 * a.B * few)) || a.B * most > 0x7fffffff / a.Hq) few = 0;
-        if (few > 0) {
-            const bi_status st2 = launch_attention_few_window(a, few, workspace, s);
-            if (st2 != BI_OK || a.max_q <= few) return st2;
-        }
+    FewPlan plan{0, 0, 0};
+    if (workspace) plan = plan_few(a.B, a.total_q, a.Hq, a.Hkv, a.max_len, a.max_q, a.window, a.sinks);
+    if (plan.few > 0) {
+        const bi_status st = launch_attention_few_window(a, plan, workspace, s);
+        if (st != BI_OK || a.max_q <= plan.few) return st;
     }
     ExtParams p{};
     p.Q = static_cast<const uint16_t *>(a.Q);
@@ -729,7 +748,7 @@ bi_status launch_attention_extend_window(const WindowCall &a, void *workspace, c
     p.bs = a.bs;
     p.max_len = a.max_len;
     p.max_q = a.max_q;
-    p.few = few;
+    p.few = plan.few;
     p.window = a.window;
     p.sinks = a.sinks;
     p.scale = a.scale;

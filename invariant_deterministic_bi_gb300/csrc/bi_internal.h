@@ -148,11 +148,18 @@ struct WindowCall {
     int32_t total_q, max_blocks, Hq, Hkv, bs, max_len, max_q, window, sinks;
     float scale;
 };
-// workspace: null, or attention_extend_window_workspace_bytes() > 0 of them
+// How a windowed extend call goes: sequences of at most `few` new tokens are split over the cache's chunks (0: none), with
+// room in the workspace for the results of `places` tokens, `bytes` in all.
+struct FewPlan {
+    int32_t few;
+    int64_t places, bytes;
+};
+FewPlan plan_few(int64_t B, int64_t total_q, int32_t Hq, int32_t Hkv, int32_t max_len, int32_t max_q, int32_t window, int32_t sinks);
+// workspace: null, or plan_few().bytes > 0 of them
 bi_status launch_attention_extend_window(const WindowCall &a, void *workspace, cudaStream_t s);
-// The sequences of at most `few` new tokens, split over the cache's chunks.
-bi_status launch_attention_few_window(const WindowCall &a, int32_t few, void *workspace, cudaStream_t s);
-// Bytes the split wants for these sizes; 0: the tiled kernel alone is used; -1: past int64_t.
+// The sequences of at most plan.few new tokens, split over the cache's chunks.
+bi_status launch_attention_few_window(const WindowCall &a, const FewPlan &plan, void *workspace, cudaStream_t s);
+// Bytes that are enough for every batch of total_q tokens; 0: that would pass what the split takes; -1: past int64_t.
 int64_t attention_extend_window_workspace_bytes(int64_t total_q, int32_t Hq, int32_t max_len, int32_t window, int32_t sinks);
 // The most chunks in which a token of at most max_len sees something (window 0: none).
 int64_t seen_chunks(int32_t max_len, int32_t window, int32_t sinks);
