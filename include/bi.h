@@ -541,7 +541,11 @@ BI_API bi_status bi_gemm_int4(const void *X, int64_t ldx, const uint8_t *W, cons
  * the pair being dimensions (i, i + rotary_dim / 2), or (2i, 2i + 1) interleaved;
  * dimensions from rotary_dim on stay as they are. The frequencies are held in
  * turns per position as 64-bit fractions (f / 2 pi = turns * 2^-64), so that the
- * angle of any position is exact to 2^-65 turns a position.
+ * angle of any position is an exact product, modulo a turn. The frequencies
+ * themselves are computed in double precision: off by at most some
+ * (ln base + 8) 2^-53 of f / 2 pi (f = 1: 2^-56 turns a position, so 2^-39 turns at
+ * position 2^17, 2^-25 at 2^31), and the cut to 64 bits by 2^-64 (for a negative
+ * given frequency 2^-54).
  * Norm: x / sqrt(mean x^2 + eps) * w over the head's dimensions, before the rotation.
  *
  *   positions i64 [T] (device)  any that fits in 32 bits, negative ones too (they turn

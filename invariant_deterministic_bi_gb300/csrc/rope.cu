@@ -11,8 +11,8 @@
 //
 // Angles: a frequency is held in turns per position as a 64-bit fraction, so
 // p f_i modulo one turn is the low 64 bits of an integer product: exact but for
-// the frequency's own rounding (2^-65 turns a position), at any position, with
-// no table of positions and no argument reduction. sincospif takes the top 32
+// the frequency itself, which is a double's (2^-56 turns a position for f = 1), at any
+// position, with no table of positions and no argument reduction. sincospif takes the top 32
 // bits as a signed number of half turns.
 //
 // Layout: LANES lanes hold a row, 16 dimensions each as two 16-byte vectors half the
