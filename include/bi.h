@@ -655,12 +655,12 @@ BI_API bi_status bi_attention_decode_window(const void *Q, const void *K_cache, 
  *            few new tokens, and sequences of few among others, are split over the chunks
  *            like decode; without, or where that size is 0 (a single prompt, mostly longer
  *            sequences), one CTA walks the chunks of each tile of new tokens. The bits are
- *            the same. (16 sequences of 5 new tokens over 4000, window 1024: 41 us and 79.)
+ *            the same. (16 sequences of 5 new tokens over 100 to 4000, window 1024: 38 us and 70.)
  *            The size is at most 512 MB; where the results of all that could be split would
  *            take more, sequences of fewer new tokens are. bi_attention_extend_window_workspace_size,
  *            which does not know B, is enough for any B, or 0 where that would pass 512 MB.
- * max_q_len  the most new tokens of a sequence; a larger one costs little (64 single tokens,
- *            60 us with 1, 81 with 100000).
+ * max_q_len  the most new tokens of a sequence; where they are few, a larger one costs time
+ *            (64 single tokens over 4000, window 1024: 58 us with 1, 92 with 100000).
  */
 BI_API int64_t bi_attention_extend_window_workspace_size(int64_t total_q, int32_t Hq, int32_t Hkv, int32_t max_seq_len,
                                                          int32_t max_q_len, int32_t window, int32_t sinks);

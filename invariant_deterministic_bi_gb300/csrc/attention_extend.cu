@@ -31,7 +31,7 @@
 // Bound by mma.sync (1.5 times the operations, for p in two parts: some 62 % of its pipe
 // while an SM is busy) and the eight warps' ldmatrix of K and V, then by a tile's start
 // (6600 cycles of 80000 for five chunks) and the last round of tiles. 4096 tokens over 8192: window 2000
-// 694 us (195 TFLOP/s); without a window that matters 1661 (248), attention.cu's kernel 1909.
+// 698 us (194 TFLOP/s); without a window that matters 1669 (247), attention.cu's kernel 1909.
 #include "attn_common.cuh"
 #include "bi_internal.h"
 
@@ -683,7 +683,7 @@ int64_t attention_extend_window_workspace_bytes(int64_t total_q, int32_t Hq, int
 // Which sequences are split over the chunks: all, where that should take less time for the call; else those of at most
 // kFewRows query rows, for which it takes less of an SM's time (a chunk of a tile of 16 rows 1.4 us, of 128 rows 5.3).
 // In us, on the sums that the host knows and for 152 SMs, so that the choice is the same wherever a size is asked for: drafts
-// 16 x 5 over 4000, window 1024, 80 tiled, 40 split.
+// 16 x 5 over 100 to 4000, window 1024, 70 tiled, 38 split.
 static bool split_all(int64_t B, int64_t total_q, int G, int32_t Hkv, int64_t seen, int64_t max_q) {
     constexpr int kSms = 152;
     const double chunks = static_cast<double>(seen);

@@ -16,8 +16,9 @@
 // other tiles read the same chunks; and where V holds a value that is not finite out of
 // some token's sight, p.V token by token with zeros there.
 //
-// 16 sequences of 5 drafts over 100 to 4000 tokens, window 1024, 32 heads over 8: 39 us for
-// both kernels (the tiled kernel, one CTA a sequence and KV head: 80); 64 single tokens over 4000, 60 (271).
+// 16 sequences of 5 drafts over 100 to 4000 tokens, window 1024, 32 heads over 8: 38 us for
+// both kernels (the tiled kernel, one CTA a sequence and KV head: 70); 64 single tokens over 4000, 58 (260), and 92 where the
+// call says that a sequence may have more than 16: its items and merges are laid out for 16 places then.
 #include "attn_common.cuh"
 #include "bi_internal.h"
 

@@ -14,8 +14,8 @@ constexpr int kChunk = 128;                    // tokens per chunk: fixed, by po
 constexpr int kRowBytes = kD * 2;              // one token's K (or V) row of one KV head
 constexpr int kTileBytes = kChunk * kRowBytes; // 32 KB
 constexpr int kHalfTile = kChunk * 128;        // one 64-dimension half of a K or V tile (128-byte swizzle)
-// Over the 4-bit cache: the maximum of a chunk of which a row sees no token in
-// the cache (its blocks lie outside). The least number, so that the chunk's sums,
+// Over the 4-bit cache and with a window: the maximum of a chunk of which a row sees
+// no token in the cache (its blocks lie outside). The least number, so that the chunk's sums,
 // which are 0, leave every other chunk's weight as it is, whatever its scores;
 // with -inf its exponentials would be NaN, as they have to be where the scores of
 // tokens in the cache are all -inf (bi_attention_decode gives NaN there).
